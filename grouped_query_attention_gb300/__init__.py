@@ -3,7 +3,10 @@
 The compute path is the CUDA library libgqa_gb300.so behind the C ABI of
 include/gqa.h. This package adds argument marshalling for torch tensors:
 ``GroupQueryAttention`` keeps the handle and a workspace buffer obtained from
-torch's allocator and calls ``gqa_forward`` on the current stream.
+torch's allocator and calls ``gqa_forward`` on the current stream. Its methods
+``rotary_axes``, ``block_forward`` and ``block_evict`` (block_cache.py) are the
+multi-axis rotary embedding, attention over a block-scaled int8 cache
+(``BlockCache``) and the eviction from one.
 """
 
 from __future__ import annotations
@@ -11,22 +14,8 @@ from __future__ import annotations
 import torch
 
 from . import capi
+from .block_cache import BlockCache, BlockCacheOps, tensor_desc  # noqa: F401
 from .capi import GqaError, GqaInputs, GqaOutputs, describe, make_attrs  # noqa: F401
-
-_DTYPE_CODE = {torch.float32: capi.GQA_F32, torch.float16: capi.GQA_F16, torch.int8: capi.GQA_I8,
-               torch.uint8: capi.GQA_U8, torch.int32: capi.GQA_I32, torch.bfloat16: capi.GQA_BF16}
-
-
-def tensor_desc(t: torch.Tensor | None) -> capi.GqaTensor:
-    """C descriptor of a contiguous CUDA tensor (or an absent input for None)."""
-    if t is None:
-        return capi.GqaTensor()
-    if not t.is_contiguous():
-        raise ValueError("tensors passed to the GQA library must be contiguous")
-    if t.dtype not in _DTYPE_CODE:
-        raise ValueError(f"unsupported dtype {t.dtype}")
-    return describe(t.data_ptr(), _DTYPE_CODE[t.dtype], tuple(t.shape))
-
 
 def _tensor_key(t: torch.Tensor | None):
     """What a tensor's C descriptor depends on (None for an absent input)."""
@@ -35,7 +24,7 @@ def _tensor_key(t: torch.Tensor | None):
     return t.data_ptr(), t.shape, t.dtype, t.is_contiguous()
 
 
-class GroupQueryAttention:
+class GroupQueryAttention(BlockCacheOps):
     """One operator instance: attributes fixed at construction (section Attributes)."""
 
     def __init__(self, num_heads: int, kv_num_heads: int, **attrs):
@@ -47,6 +36,7 @@ class GroupQueryAttention:
         # keeps its address, shape, dtype and layout (a decode loop over fixed buffers).
         self._call_key = None
         self._call_structs = None
+        self._init_block_ops()
 
     def close(self) -> None:
         if getattr(self, "handle", None) is not None and self.handle.value:

@@ -26,9 +26,12 @@ GQA_DEVICE_BAD_SEQLEN, GQA_DEVICE_BAD_ROTARY, GQA_DEVICE_TIMEOUT = 1, 2, 4
 EXPORTS = ["gqa_attrs_default", "gqa_create", "gqa_workspace_size", "gqa_forward",
            "gqa_read_device_status", "gqa_describe_plan", "gqa_destroy", "gqa_status_string",
            "gqa_last_error", "gqa_forward_noalloc", "gqa_profile_begin", "gqa_profile_end",
-           "gqa_set_wait_limit"]
+           "gqa_set_wait_limit", "gqa_rotary_axes", "gqa_block_workspace_size", "gqa_block_forward",
+           "gqa_block_evict"]
 KERNEL_KINDS = {1: "copy_past", 2: "prepass", 3: "decode", 4: "prefill_cuda_core", 5: "prefill_tensor_core",
-                6: "decode_tensor_core", 7: "window_shift", 8: "bias_stage"}
+                6: "decode_tensor_core", 7: "window_shift", 8: "bias_stage", 9: "rotary_axes", 10: "block_append",
+                11: "block_attention", 12: "block_merge", 13: "block_prefill", 14: "block_weights",
+                15: "evict_select", 16: "evict_gather"}
 GQA_REGIME_DECODE, GQA_REGIME_PREFILL = 1, 2
 
 
@@ -56,6 +59,41 @@ class GqaInputs(ctypes.Structure):
 
 class GqaOutputs(ctypes.Structure):
     _fields_ = [("output", GqaTensor), ("present_key", GqaTensor), ("present_value", GqaTensor)]
+
+
+GQA_MAX_ROTARY_AXES = 8
+
+
+class GqaRotaryInputs(ctypes.Structure):
+    _fields_ = [(n, GqaTensor) for n in ("query", "key", "positions", "cos_cache", "sin_cache", "q_norm_weight",
+                                         "k_norm_weight")] + \
+               [("sections", ctypes.c_int32 * GQA_MAX_ROTARY_AXES), ("num_axes", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+class GqaRotaryOutputs(ctypes.Structure):
+    _fields_ = [("query", GqaTensor), ("key", GqaTensor)]
+
+
+class GqaBlockCache(ctypes.Structure):
+    _fields_ = [(n, GqaTensor) for n in ("key_codes", "value_codes", "key_scales", "value_scales")] + \
+               [("block_size", ctypes.c_int32)]
+
+
+class GqaBlockInputs(ctypes.Structure):
+    _fields_ = [(n, GqaTensor) for n in ("query", "key", "value", "seqlens_k", "new_lens", "head_sink",
+                                         "past_weights")] + [("total_sequence_length", ctypes.c_int32)]
+
+
+class GqaBlockOutputs(ctypes.Structure):
+    _fields_ = [("output", GqaTensor), ("present_weights", GqaTensor)]
+
+
+# "from" is a keyword; the C field `from` is `source` here and `into` is `into`
+class GqaEvictArgs(ctypes.Structure):
+    _fields_ = [("source", GqaBlockCache), ("into", GqaBlockCache)] + \
+               [(n, GqaTensor) for n in ("weights", "seqlens_k", "into_weights", "kept", "into_seqlens_k")] + \
+               [(n, ctypes.c_int32) for n in ("total_sequence_length", "keep", "recent", "first")]
 
 
 class GqaPlanInfo(ctypes.Structure):
@@ -108,6 +146,17 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.gqa_profile_end.restype = ctypes.c_int
     lib.gqa_set_wait_limit.argtypes = [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32]
     lib.gqa_set_wait_limit.restype = ctypes.c_int
+    P, V = ctypes.POINTER, ctypes.c_void_p
+    lib.gqa_rotary_axes.argtypes = [V, P(GqaRotaryInputs), P(GqaRotaryOutputs), V, V]
+    lib.gqa_rotary_axes.restype = ctypes.c_int
+    lib.gqa_block_workspace_size.argtypes = [V, P(GqaBlockCache), P(GqaBlockInputs), P(GqaBlockOutputs),
+                                             P(ctypes.c_size_t)]
+    lib.gqa_block_workspace_size.restype = ctypes.c_int
+    lib.gqa_block_forward.argtypes = [V, P(GqaBlockCache), P(GqaBlockInputs), P(GqaBlockOutputs), V, ctypes.c_size_t,
+                                      V, V]
+    lib.gqa_block_forward.restype = ctypes.c_int
+    lib.gqa_block_evict.argtypes = [V, P(GqaEvictArgs), V, V]
+    lib.gqa_block_evict.restype = ctypes.c_int
     lib.gqa_destroy.argtypes = [ctypes.c_void_p]
     lib.gqa_destroy.restype = None
     lib.gqa_status_string.argtypes = [ctypes.c_int]
@@ -193,6 +242,25 @@ def gqa_profile_end(handle, capacity: int = 4096) -> list:
 def gqa_set_wait_limit(handle, cycles: int, withhold_copy: int = -1) -> None:
     """Bound of the tensor-core kernels' pipeline waits (0: default) and the timeout-path test switch."""
     _check(load_library().gqa_set_wait_limit(handle, int(cycles), int(withhold_copy)))
+
+
+def gqa_rotary_axes(handle, inputs: GqaRotaryInputs, outputs: GqaRotaryOutputs, status: int, stream: int) -> None:
+    _check(load_library().gqa_rotary_axes(handle, inputs, outputs, status, stream))
+
+
+def gqa_block_workspace_size(handle, cache: GqaBlockCache, inputs: GqaBlockInputs, outputs: GqaBlockOutputs) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().gqa_block_workspace_size(handle, cache, inputs, outputs, ctypes.byref(n)))
+    return n.value
+
+
+def gqa_block_forward(handle, cache: GqaBlockCache, inputs: GqaBlockInputs, outputs: GqaBlockOutputs, workspace: int,
+                      workspace_bytes: int, status: int, stream: int) -> None:
+    _check(load_library().gqa_block_forward(handle, cache, inputs, outputs, workspace, workspace_bytes, status, stream))
+
+
+def gqa_block_evict(handle, args: GqaEvictArgs, status: int, stream: int) -> None:
+    _check(load_library().gqa_block_evict(handle, args, status, stream))
 
 
 def gqa_destroy(handle) -> None:

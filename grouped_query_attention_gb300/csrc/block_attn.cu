@@ -1,0 +1,946 @@
+// Attention over the block-scaled int8 cache by a split over the keys (decode
+// steps, short chunks, and every shape the tensor-core prefill does not take).
+//
+// Rows of a KV head (b, g): query rows (position, grouped head), in row tiles
+// of 16 (fp16) or 8 (fp32). One warp MMA (m16n8k16, fp16 in, fp32 sums) takes
+// the 16 rows against 8 keys (scores) or against 8 coordinates (output). The
+// codes are small integers, exact in fp16; the block's K scale multiplies the
+// scores, its V scale the probabilities (both are one number for 16 keys).
+// fp32 queries keep their precision as two fp16 parts: MMA rows 0..7 hold
+// hi = fp16(q 2^-e), rows 8..15 lo = fp16(q 2^-e - hi), 2^e from the row's
+// largest value, and the two halves of the accumulator are added; so are
+// P_hi and P_lo. That fills the rows an 8-row tile would leave idle.
+//
+// Bound: HBM, 2 H bytes per cache row. Every warp is a worker of its own: the
+// 32-key units of all ranges (b, g, row tile) are laid end to end, a worker
+// takes an equal share, copies its units through a private ring with
+// asynchronous 16-byte copies (chunks swizzled so that the fragment reads do
+// not conflict), and nothing waits for another warp. A worker's piece of a
+// range ends as a partial (m, l, O) in the workspace; a second launch merges
+// the pieces of each row and adds the attention weights of the cache rows.
+#include <cuda_fp16.h>
+
+#include "block_internal.h"
+#include "common.cuh"
+
+namespace gqa {
+namespace {
+
+constexpr int kWarps = 4;
+
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Four bytes, or zeros when !on.
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool on) {
+  const int n = on ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Bytes 0, 1 (lo) or 2, 3 (hi) of x (codes ^ 0x80) as two fp16 values: under
+// the exponent of 1024 a byte u reads 1024 + u; 1152 = 1024 + 128 comes off.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t x) {
+  const uint32_t h = __byte_perm(x, 0x64646464u, 0x4140u);
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), __floats2half2_rn(1152.f, 1152.f));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t codes_hi(uint32_t x) {
+  const uint32_t h = __byte_perm(x, 0x64646464u, 0x4342u);
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), __floats2half2_rn(1152.f, 1152.f));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
+
+// 16-byte chunk `c` of row `r` of a staged tile of HP-byte rows.
+template <int HP>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  if constexpr (HP == 64) return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+  return (uint32_t)(r * HP + (((c & ~7) | ((c ^ r) & 7)) << 4));
+}
+
+// Key range of sequence b shared by its row tiles: units [t0, t0 + nt).
+__device__ __forceinline__ void units_of(const BlockParams& p, int total, int fresh, int* t0, int* nt) {
+  *t0 = 0;
+  *nt = 0;
+  if (fresh <= 0) return;
+  const int kmin = p.window >= 0 ? max(0, total - fresh - p.window) : 0;
+  *t0 = kmin / kBlockUnit;
+  *nt = (total + kBlockUnit - 1) / kBlockUnit - *t0;
+}
+
+// Units [lo, hi) (of the nt above) that row tile rt sees a key of.
+__device__ __forceinline__ void tile_units(const BlockParams& p, int total, int fresh, int t0, int nt, int rt,
+                                           int* lo, int* hi) {
+  const int r0 = rt * p.rt_rows, r1 = min(r0 + p.rt_rows, p.S * p.G) - 1;
+  const int i0 = r0 / p.G, i1 = min(r1 / p.G, fresh - 1);
+  if (i0 > i1) {   // padding rows only
+    *lo = *hi = 0;
+    return;
+  }
+  const int past = total - fresh;
+  const int kmin = p.window >= 0 ? max(0, past + i0 - p.window) : 0;
+  *lo = kmin / kBlockUnit - t0;
+  *hi = (past + i1) / kBlockUnit + 1 - t0;
+}
+
+// Units of sequence b counting every range's extra cost; 0 when nothing is to do.
+__device__ __forceinline__ long long seq_units(const BlockParams& p, int b, int* total, int* fresh, int* t0, int* nt) {
+  if (!block_lengths(p, b, total, fresh)) *fresh = 0;
+  units_of(p, *total, *fresh, t0, nt);
+  return *nt > 0 ? (long long)p.Nkv * p.nrt * (*nt + kBlockRangeCost) : 0;
+}
+
+// Sum of seq_units over the batch, by one warp.
+__device__ long long all_units(const BlockParams& p) {
+  const int lane = threadIdx.x & 31;
+  long long sum = 0;
+  for (int b = lane; b < p.B; b += 32) {
+    int a, f, t0, nt;
+    sum += seq_units(p, b, &a, &f, &t0, &nt);
+  }
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// Walk over a worker's units: cell (b, gr = g * nrt + rt) and unit `off` of
+// the sequence's units; `left` units of the share remain.
+struct Walk {
+  int b, gr, off, nt, t0, total, fresh, hi;
+  long long left;
+
+  __device__ void enter_seq(const BlockParams& p) {
+    while (b < p.B && seq_units(p, b, &total, &fresh, &t0, &nt) == 0) ++b;
+    if (b >= p.B) left = 0;
+  }
+  // Skip the units no row of the tile sees, and the ends of ranges.
+  __device__ void settle(const BlockParams& p) {
+    while (left > 0) {
+      int lo;
+      tile_units(p, total, fresh, t0, nt, gr % p.nrt, &lo, &hi);
+      if (off < lo) {
+        left -= lo - off;
+        off = lo;
+        if (left <= 0) return;
+      }
+      if (off < hi) return;
+      left -= nt + kBlockRangeCost - off;
+      off = 0;
+      if (++gr == p.Nkv * p.nrt) {
+        gr = 0;
+        ++b;
+        if (left > 0) enter_seq(p);
+      }
+    }
+  }
+  // A share of n units from unit u on (u below the sum of all); one warp.
+  __device__ void start(const BlockParams& p, long long u, long long n) {
+    left = n;
+    const int lane = threadIdx.x & 31;
+    for (b = 0; b < p.B; b += 32) {   // the sequence that holds unit u, 32 at a time
+      long long s = b + lane < p.B ? seq_units(p, b + lane, &total, &fresh, &t0, &nt) : 0;
+      const long long own = s;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += v;
+      }
+      const unsigned past_u = __ballot_sync(0xffffffffu, s > u);
+      if (past_u) {
+        const int at = __ffs(past_u) - 1;
+        u -= __shfl_sync(0xffffffffu, s - own, at);
+        b += at;
+        break;
+      }
+      u -= __shfl_sync(0xffffffffu, s, 31);
+    }
+    seq_units(p, b, &total, &fresh, &t0, &nt);
+    gr = (int)(u / (nt + kBlockRangeCost));
+    off = (int)(u % (nt + kBlockRangeCost));
+    settle(p);
+  }
+  __device__ void next(const BlockParams& p) {
+    --left;
+    ++off;
+    if (off >= hi || left <= 0) settle(p);
+  }
+};
+
+template <int HP>
+struct RingShape {
+  static constexpr int kStages = HP == 64 ? 6 : 3;
+  static constexpr int kStageBytes = 2 * kBlockUnit * HP;   // K tile, V tile
+};
+
+template <typename T, int HP>
+struct __align__(16) WarpSmem {
+  uint8_t ring[RingShape<HP>::kStages][RingShape<HP>::kStageBytes];
+  float sc[RingShape<HP>::kStages][4];    // K scales of the unit's two 16-key groups, V scales
+  uint4 q[HP > 128 ? HP / 16 * 32 : 1];   // query fragments of the large head sizes
+};
+
+// Fragments of the row tile's queries: thread t of a quad holds coordinates
+// t HP/4 .. of its rows (the order of the contraction is free as long as the
+// keys use the same), four per MMA step. Returns the factor of the scores.
+template <typename T, int HP>
+__device__ float load_queries(const BlockParams& p, int b, int g, int rt, uint32_t (*qf)[4], uint4* qs) {
+  const int lane = threadIdx.x & 31, gq = lane >> 2, t = lane & 3;
+  const int nrows = p.S * p.G, r0 = rt * p.rt_rows;
+  constexpr bool kF16 = sizeof(T) == 2;
+  const T* row[2];
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    const int r = r0 + gq + (kF16 ? 8 * hf : 0);
+    row[hf] = r < nrows ? static_cast<const T*>(p.q) +
+                              ((long long)(b * (long long)p.S + r / p.G) * p.N + g * p.G + r % p.G) * p.H
+                        : nullptr;
+  }
+  float up = 1.f, down = 1.f;
+  if constexpr (!kF16) {
+    float mx = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < HP / 16; ++ks) {
+      const int d = t * (HP / 4) + 4 * ks;
+      if (row[0] && d < p.H) {
+        const float4 v = *reinterpret_cast<const float4*>(row[0] + d);
+        mx = fmax3(mx, fabsf(v.x), fabsf(v.y));
+        mx = fmax3(mx, fabsf(v.z), fabsf(v.w));
+      }
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const int ex = (__float_as_int(mx) >> 23) & 0xff;
+    const int e = ex == 0 ? 0 : min(ex, 253) - 127;
+    down = __int_as_float((127 - e) << 23);
+    up = __int_as_float((127 + e) << 23);
+  }
+#pragma unroll
+  for (int ks = 0; ks < HP / 16; ++ks) {
+    const int d = t * (HP / 4) + 4 * ks;
+    uint32_t a[4] = {0u, 0u, 0u, 0u};
+    if constexpr (kF16) {
+      if (row[0] && d < p.H) {
+        const uint2 v = *reinterpret_cast<const uint2*>(row[0] + d);
+        a[0] = v.x;
+        a[2] = v.y;
+      }
+      if (row[1] && d < p.H) {
+        const uint2 v = *reinterpret_cast<const uint2*>(row[1] + d);
+        a[1] = v.x;
+        a[3] = v.y;
+      }
+    } else if (row[0] && d < p.H) {
+      float4 v = *reinterpret_cast<const float4*>(row[0] + d);
+      v.x *= down;
+      v.y *= down;
+      v.z *= down;
+      v.w *= down;
+      a[0] = pack(v.x, v.y);
+      a[2] = pack(v.z, v.w);
+      const float2 h0 = unpack(a[0]), h1 = unpack(a[2]);
+      a[1] = pack(v.x - h0.x, v.y - h0.y);
+      a[3] = pack(v.z - h1.x, v.w - h1.y);
+    }
+    if constexpr (HP > 128) {
+      qs[ks * 32 + lane] = make_uint4(a[0], a[1], a[2], a[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qf[ks][i] = a[i];
+    }
+  }
+  return up;
+}
+
+template <typename T, int HP>
+__global__ void __launch_bounds__(kWarps * 32, HP > 128 ? 1 : 2)
+block_attn_kernel(const BlockParams p) {
+  constexpr bool kHalf = sizeof(T) == 2;
+  constexpr int kStages = RingShape<HP>::kStages;
+  constexpr int kTileBytes = kBlockUnit * HP;
+  constexpr int kSteps = HP / 16;           // MMA steps over the coordinates
+  constexpr int kNT = HP / 8;               // output tiles of 8 coordinates
+  constexpr float kGrow = 4.f;              // log2 growth of a maximum tolerated before rescaling
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  WarpSmem<T, HP>& sm = reinterpret_cast<WarpSmem<T, HP>*>(smem_raw)[threadIdx.x >> 5];
+  const int lane = threadIdx.x & 31, gq = lane >> 2, t = lane & 3;
+  const long long worker = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+
+  if (blockIdx.x == 0 && threadIdx.x < 32 && p.status) {   // lengths out of range
+    bool bad = false;
+    for (int b = lane; b < p.B; b += 32) {
+      int a, f;
+      bad |= !block_lengths(p, b, &a, &f);
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.status, GQA_DEVICE_BAD_SEQLEN_BIT);
+  }
+  const long long units = all_units(p);
+  const long long u0 = units * worker / p.workers, u1 = units * (worker + 1) / p.workers;
+  if (u0 >= u1) return;
+  Walk ld, cp;
+  ld.start(p, u0, u1 - u0);
+  cp = ld;
+
+  const int chunks = p.H / 16;
+  // Start the copies of the unit at `ld` into stage s and move on.
+  auto fetch = [&](int s) {
+    if (ld.left > 0) {
+      const int j0 = (ld.t0 + ld.off) * kBlockUnit, rows = min(kBlockUnit, ld.total - j0);
+      const long long bg = (long long)ld.b * p.Nkv + ld.gr / p.nrt;
+      const int8_t* ksrc = p.kc + (bg * p.C + j0) * p.H;
+      const int8_t* vsrc = p.vc + (bg * p.C + j0) * p.H;
+      const uint32_t kd = (uint32_t)__cvta_generic_to_shared(sm.ring[s]), vd = kd + kTileBytes;
+      if (chunks == HP / 16) {
+#pragma unroll
+        for (int i = 0; i < kBlockUnit * HP / 512; ++i) {
+          const int x = i * 32 + lane, r = x / (HP / 16), c = x % (HP / 16);
+          if (r < rows) {
+            cp16(kd + chunk_at<HP>(r, c), ksrc + r * HP + 16 * c);
+            cp16(vd + chunk_at<HP>(r, c), vsrc + r * HP + 16 * c);
+          }
+        }
+      } else {
+        for (int x = lane; x < rows * chunks; x += 32) {
+          const int r = x / chunks, c = x - r * chunks;
+          cp16(kd + chunk_at<HP>(r, c), ksrc + r * p.H + 16 * c);
+          cp16(vd + chunk_at<HP>(r, c), vsrc + r * p.H + 16 * c);
+        }
+      }
+      if (lane < 4) {   // scales of the two 16-key groups; 0 behind the last row
+        const int j = j0 + 16 * (lane & 1);
+        const float* src = (lane < 2 ? p.ks : p.vs) + bg * p.nblk;
+        const bool on = j < ld.total;
+        cp4((uint32_t)__cvta_generic_to_shared(&sm.sc[s][lane]), src + (on ? j >> p.bs_log2 : 0), on);
+      }
+      ld.next(p);
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) fetch(s);
+
+  uint32_t qf[HP > 128 ? 1 : kSteps][4];
+  float o[kNT][4];
+  float m[2], l[2], mul[2];     // rows gq and gq + 8 (fp32: row gq only)
+  int pos[2];
+  int wexp = -200;              // the V scales enter as vs 2^-wexp
+  bool fresh_piece = true;
+  int stage = 0;
+  while (cp.left > 0) {
+    const int b = cp.b, g = cp.gr / p.nrt, rt = cp.gr % p.nrt;
+    const int j0 = (cp.t0 + cp.off) * kBlockUnit, total = cp.total, past = cp.total - cp.fresh;
+    if (fresh_piece) {
+      fresh_piece = false;
+      const float f = load_queries<T, HP>(p, b, g, rt, qf, sm.q) * p.scale;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mul[h] = p.softcap > 0.f ? f : f * kLog2e;
+        m[h] = kNegBig;
+        l[h] = 0.f;
+        pos[h] = past + (rt * p.rt_rows + gq + (kHalf ? 8 * h : 0)) / p.G;
+      }
+#pragma unroll
+      for (int i = 0; i < kNT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      wexp = -200;
+    }
+    cp_wait<kStages - 2>();
+    __syncwarp();
+    fetch(stage == 0 ? kStages - 1 : stage - 1);   // the stage read one unit ago
+    const uint8_t* kt = sm.ring[stage];
+    const uint8_t* vt = kt + kTileBytes;
+
+    // ---- scores of 32 keys: s[n] holds rows gq (0, 1) and gq + 8 (2, 3), keys 8 n + 2 t, + 1
+    float s[4][4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+      const int r = 8 * n + gq;
+      uint32_t kw[kSteps];
+#pragma unroll
+      for (int i = 0; i < kSteps / 4; ++i) {
+        const uint4 v = *reinterpret_cast<const uint4*>(kt + chunk_at<HP>(r, t * (HP / 64) + i));
+        kw[4 * i] = v.x ^ 0x80808080u;
+        kw[4 * i + 1] = v.y ^ 0x80808080u;
+        kw[4 * i + 2] = v.z ^ 0x80808080u;
+        kw[4 * i + 3] = v.w ^ 0x80808080u;
+      }
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks) {
+        if constexpr (HP > 128) {
+          const uint4 a = sm.q[ks * 32 + lane];
+          const uint32_t av[4] = {a.x, a.y, a.z, a.w};
+          mma16816(s[n], av, codes_lo(kw[ks]), codes_hi(kw[ks]));
+        } else {
+          mma16816(s[n], qf[ks], codes_lo(kw[ks]), codes_hi(kw[ks]));
+        }
+      }
+    }
+    const float ksc[2] = {sm.sc[stage][0], sm.sc[stage][1]};
+    const float vsc[2] = {sm.sc[stage][2], sm.sc[stage][3]};
+    // Log2-domain scores; hi and lo parts of an fp32 row are added.
+    const bool edge = j0 + kBlockUnit - 1 > past + (rt * p.rt_rows) / p.G ||
+                      (p.window >= 0 && j0 < past + (rt * p.rt_rows + p.rt_rows - 1) / p.G - p.window);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      if (!kHalf) {
+        s[n][0] += s[n][2];
+        s[n][1] += s[n][3];
+      }
+#pragma unroll
+      for (int e = 0; e < (kHalf ? 4 : 2); ++e) {
+        float x = s[n][e] * (mul[e >> 1] * ksc[n >> 1]);
+        if (p.softcap > 0.f) x = p.softcap * kLog2e * tanhf(x / p.softcap);
+        if (edge) {
+          const int j = j0 + 8 * n + 2 * t + (e & 1);
+          if (j > pos[e >> 1] || (p.window >= 0 && j < pos[e >> 1] - p.window)) x = -INFINITY;
+        }
+        s[n][e] = x;
+      }
+    }
+    if (p.stash) {
+#pragma unroll
+      for (int h = 0; h < (kHalf ? 2 : 1); ++h) {
+        const int r = gq + 8 * h;
+        if (r < p.S * p.G) {
+          float* dst = p.stash + (((long long)b * p.Nkv + g) * p.S * p.G + r) * p.stash_ld + j0 + 2 * t;
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+            *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(s[n][2 * h], s[n][2 * h + 1]);
+        }
+      }
+    }
+    // ---- running maximum; O is rescaled only when one grows by more than 2^4
+    // or the V scales outgrow their reference.
+    float mx[2];
+#pragma unroll
+    for (int h = 0; h < (kHalf ? 2 : 1); ++h) {
+      mx[h] = fmaxf(fmax3(s[0][2 * h], s[0][2 * h + 1], s[1][2 * h]), fmax3(s[1][2 * h + 1], s[2][2 * h], s[2][2 * h + 1]));
+      mx[h] = fmax3(mx[h], s[3][2 * h], s[3][2 * h + 1]);
+      mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+      mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+    }
+    const bool grow0 = mx[0] > m[0] + kGrow, grow1 = kHalf && mx[kHalf ? 1 : 0] > m[1] + kGrow;
+    // P enters the MMA as p vs 2^-wexp, at most 2^14: vs 2^-wexp in [2^9, 2^10)
+    // for the block that set it, and fp16 keeps its 11 bits down to 2^-14.
+    const int vexp = (__float_as_int(fmaxf(vsc[0], vsc[1])) >> 23) - 127 - 9;
+    if (__any_sync(0xffffffffu, grow0 || grow1) || vexp > wexp) {
+      const int dw = vexp > wexp ? max(wexp - vexp, -126) : 0;
+      if (vexp > wexp) wexp = max(vexp, -110);
+      const float fw = __int_as_float((127 + dw) << 23);
+      float f[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool grow = h == 0 ? grow0 : grow1;
+        const float mn = grow ? mx[kHalf ? h : 0] : m[h];
+        const float e = grow ? ex2(m[h] - mn) : 1.f;
+        m[h] = mn;
+        l[h] *= e;
+        f[h] = e * fw;
+      }
+      if (!kHalf) f[1] = f[0];
+#pragma unroll
+      for (int i = 0; i < kNT; ++i) {
+        o[i][0] *= f[0];
+        o[i][1] *= f[0];
+        o[i][2] *= f[1];
+        o[i][3] *= f[1];
+      }
+    }
+    const float down = __int_as_float((127 - wexp < 1 ? 1 : 127 - wexp > 254 ? 254 : 127 - wexp) << 23);
+    const float vm[2] = {vsc[0] * down, vsc[1] * down};
+    // ---- P, and O += P V, 16 keys per step
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      uint32_t a[4];
+      if constexpr (kHalf) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float p0 = ex2(s[2 * kk + u][2 * h] - m[h]), p1 = ex2(s[2 * kk + u][2 * h + 1] - m[h]);
+            l[h] += p0 + p1;
+            a[2 * u + h] = pack(p0 * vm[kk], p1 * vm[kk]);
+          }
+      } else {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float p0 = ex2(s[2 * kk + u][0] - m[0]), p1 = ex2(s[2 * kk + u][1] - m[0]);
+          l[0] += p0 + p1;
+          const float x0 = p0 * vm[kk], x1 = p1 * vm[kk];
+          a[2 * u] = pack(x0, x1);
+          const float2 hi = unpack(a[2 * u]);
+          a[2 * u + 1] = pack(x0 - hi.x, x1 - hi.y);
+        }
+      }
+      // Keys 16 kk + 2 t, + 1, + 8, + 9; output tile i, column n = gq: coordinate gq HP/8 + i.
+      const int k0 = 16 * kk + 2 * t;
+      constexpr int kWords = HP / 32 < 4 ? HP / 32 : 4;   // 4-coordinate words per pass
+#pragma unroll
+      for (int hf = 0; hf < HP / 32 / kWords; ++hf) {
+        uint32_t w[4][kWords];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int r = k0 + (x & 1) + 8 * (x >> 1);
+          const int byte = gq * (HP / 8) + 16 * hf;
+          const uint8_t* src = vt + chunk_at<HP>(r, byte >> 4) + (byte & 15);
+          if constexpr (kWords == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src);
+            w[x][0] = v.x ^ 0x80808080u;
+            w[x][1] = v.y ^ 0x80808080u;
+            w[x][2] = v.z ^ 0x80808080u;
+            w[x][3] = v.w ^ 0x80808080u;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(src);
+            w[x][0] = v.x ^ 0x80808080u;
+            w[x][1] = v.y ^ 0x80808080u;
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < kWords; ++y) {
+          const uint32_t alo = __byte_perm(w[0][y], w[1][y], 0x5140u), ahi = __byte_perm(w[0][y], w[1][y], 0x7362u);
+          const uint32_t blo = __byte_perm(w[2][y], w[3][y], 0x5140u), bhi = __byte_perm(w[2][y], w[3][y], 0x7362u);
+          const int i = 16 * hf + 4 * y;
+          mma16816(o[i], a, codes_lo(alo), codes_lo(blo));
+          mma16816(o[i + 1], a, codes_hi(alo), codes_hi(blo));
+          mma16816(o[i + 2], a, codes_lo(ahi), codes_lo(bhi));
+          mma16816(o[i + 3], a, codes_hi(ahi), codes_hi(bhi));
+        }
+      }
+    }
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    const int range = cp.b * p.Nkv * p.nrt + cp.gr;
+    cp.next(p);
+    if (cp.left > 0 && cp.b * p.Nkv * p.nrt + cp.gr == range) continue;
+
+    // ---- the piece ends: (m, l) and O of its rows into slot worker + range
+    fresh_piece = true;
+    const long long slot = worker + range;
+    const float upw = __int_as_float((127 + max(wexp, -126)) << 23);   // O in units of 2^wexp (no V scale seen: O is 0)
+#pragma unroll
+    for (int h = 0; h < (kHalf ? 2 : 1); ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      const int row = gq + 8 * h;
+      if (rt * p.rt_rows + row < p.S * p.G) {
+        if (t == 0)
+          *reinterpret_cast<float2*>(p.part_ml + (slot * p.rt_rows + row) * 2) = make_float2(m[h], l[h]);
+        float* dst = p.part_o + (slot * p.rt_rows + row) * p.H;
+#pragma unroll
+        for (int col = 0; col < 2; ++col)
+#pragma unroll
+          for (int i = 0; i < kNT; i += 4) {
+            const int d = (2 * t + col) * (HP / 8) + i;
+            if (d >= p.H) continue;
+            float4 v;
+            if constexpr (kHalf) {
+              v = make_float4(o[i][2 * h + col] * upw, o[i + 1][2 * h + col] * upw, o[i + 2][2 * h + col] * upw,
+                              o[i + 3][2 * h + col] * upw);
+            } else {
+              v = make_float4((o[i][col] + o[i][2 + col]) * upw, (o[i + 1][col] + o[i + 1][2 + col]) * upw,
+                              (o[i + 2][col] + o[i + 2][2 + col]) * upw, (o[i + 3][col] + o[i + 3][2 + col]) * upw);
+            }
+            *reinterpret_cast<float4*>(dst + d) = v;
+          }
+      }
+    }
+  }
+  cp_wait<0>();
+}
+
+// ------------------------------------------------------------------ merge
+
+constexpr int kMergeThreads = 128;
+
+// Slots of the pieces of range (b, g, rt) in the split above: [first, first + n).
+__device__ __forceinline__ int pieces_of(const BlockParams& p, long long units, int b, int gr, int total, int fresh,
+                                         int t0, int nt, long long before, long long* first) {
+  int lo, hi;
+  tile_units(p, total, fresh, t0, nt, gr % p.nrt, &lo, &hi);
+  if (nt <= 0 || lo >= hi) return 0;
+  const long long base = before + (long long)gr * (nt + kBlockRangeCost);
+  const long long w0 = ((base + lo + 1) * p.workers - 1) / units, w1 = ((base + hi) * p.workers - 1) / units;
+  *first = w0 + (long long)b * p.Nkv * p.nrt + gr;
+  return (int)(w1 - w0) + 1;
+}
+
+// Log2-domain maximum and sum of one row over its pieces and the sink.
+__device__ __forceinline__ void row_stats(const BlockParams& p, long long slot0, int n, int row, int head, float* m,
+                                          float* l) {
+  // one warp: lanes over the pieces
+  const int lane = threadIdx.x & 31;
+  float mm = kNegBig;
+  for (int i = lane; i < n; i += 32) mm = fmaxf(mm, p.part_ml[((slot0 + i) * p.rt_rows + row) * 2]);
+  for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+  float sink = kNegBig;
+  if (p.sink || p.smooth) {
+    sink = (p.sink ? load_t(p.sink, head, p.t_type) : 0.f) * kLog2e;
+    mm = fmaxf(mm, sink);
+  }
+  float ll = 0.f;
+  for (int i = lane; i < n; i += 32) {
+    const float2 v = *reinterpret_cast<const float2*>(p.part_ml + ((slot0 + i) * p.rt_rows + row) * 2);
+    ll += v.y * ex2(v.x - mm);
+  }
+  for (int o = 16; o; o >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, o);
+  if (p.sink || p.smooth) ll += ex2(sink - mm);
+  *m = mm;
+  *l = ll;
+}
+
+struct RangeInfo {
+  long long slot0;
+  int n, total, fresh;
+};
+
+// All of the block: the batch's units and the pieces of range (b, gr).
+__device__ RangeInfo range_info(const BlockParams& p, int b, int gr) {
+  const int lane = threadIdx.x & 31;
+  long long units = 0, before = 0;
+  for (int x = lane; x < p.B; x += 32) {
+    int a, f, t0, nt;
+    const long long u = seq_units(p, x, &a, &f, &t0, &nt);
+    units += u;
+    if (x < b) before += u;
+  }
+  for (int o = 16; o; o >>= 1) {
+    units += __shfl_xor_sync(0xffffffffu, units, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  RangeInfo r;
+  int t0, nt;
+  r.slot0 = 0;
+  seq_units(p, b, &r.total, &r.fresh, &t0, &nt);
+  r.n = pieces_of(p, units, b, gr, r.total, r.fresh, t0, nt, before, &r.slot0);
+  return r;
+}
+
+// Blocks of kMergeThreads; blocks [0, rows) merge one query row each, the
+// others add the weights of 4 * kMergeThreads cache rows of one (b, g).
+template <typename T>
+__global__ void __launch_bounds__(kMergeThreads)
+block_merge_kernel(const BlockParams p, long long row_blocks, int weight_chunks) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ float s_m, s_l;
+  __shared__ float4 acc[kMergeThreads];
+  if (blockIdx.x < row_blocks) {
+    const int nrows = p.S * p.G;
+    const int bg = (int)(blockIdx.x / nrows), r = (int)(blockIdx.x % nrows), b = bg / p.Nkv, g = bg % p.Nkv;
+    int total, fresh;
+    if (!block_lengths(p, b, &total, &fresh)) return;
+    const int i = r / p.G, h = g * p.G + r % p.G, rt = r / p.rt_rows, row = r % p.rt_rows;
+    T* out = static_cast<T*>(p.out) + (((long long)b * p.S + i) * p.N + h) * p.H;
+    const int q4 = p.H / 4;            // float4 columns, 4 .. 64
+    if (i >= fresh) {
+      for (int d = tid; d < p.H; d += kMergeThreads) out[d] = T(0.f);
+      return;
+    }
+    const RangeInfo ri = range_info(p, b, g * p.nrt + rt);
+    if (warp == 0) {
+      float m, l;
+      row_stats(p, ri.slot0, ri.n, row, h, &m, &l);
+      if (lane == 0) {
+        s_m = m;
+        s_l = l;
+        if (p.lse) p.lse[(long long)bg * nrows + r] = l > 0.f ? m + log2f(l) : INFINITY;
+      }
+    }
+    __syncthreads();
+    const float m = s_m, l = s_l;
+    const int groups = kMergeThreads / q4, grp = tid / q4, c = tid % q4;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (grp < groups) {
+      for (int x = grp; x < ri.n; x += groups) {
+        const long long slot = (ri.slot0 + x) * p.rt_rows + row;
+        const float f = ex2(p.part_ml[slot * 2] - m);
+        const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot * p.H + 4 * c);
+        a.x = fmaf(v.x, f, a.x);
+        a.y = fmaf(v.y, f, a.y);
+        a.z = fmaf(v.z, f, a.z);
+        a.w = fmaf(v.w, f, a.w);
+      }
+    }
+    acc[tid] = a;
+    __syncthreads();
+    if (tid < q4) {
+      for (int x = 1; x < groups; ++x) {
+        const float4 v = acc[x * q4 + tid];
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
+      }
+      const float f = l > 0.f ? 1.f / l : 0.f;
+      if constexpr (sizeof(T) == 2) {
+        const uint2 v = make_uint2(pack(a.x * f, a.y * f), pack(a.z * f, a.w * f));
+        *reinterpret_cast<uint2*>(out + 4 * tid) = v;
+      } else {
+        *reinterpret_cast<float4*>(out + 4 * tid) = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+      }
+    }
+    return;
+  }
+  // ---- weights (one row tile: p.stash holds every row's scores)
+  const long long x = blockIdx.x - row_blocks;
+  const int bg = (int)(x / weight_chunks), chunk = (int)(x % weight_chunks), b = bg / p.Nkv, g = bg % p.Nkv;
+  int total, fresh;
+  if (!block_lengths(p, b, &total, &fresh)) return;
+  const int j0 = chunk * 4 * kMergeThreads;
+  if (j0 >= total) return;
+  __shared__ float lse[16];
+  const int nrows = fresh * p.G;   // live rows (at most one row tile)
+  if (nrows > 0) {
+    const RangeInfo ri = range_info(p, b, g);
+    for (int r = warp; r < nrows; r += kMergeThreads / 32) {
+      float m, l;
+      row_stats(p, ri.slot0, ri.n, r, g * p.G + r % p.G, &m, &l);
+      if (lane == 0) lse[r] = m + log2f(l);
+    }
+  }
+  __syncthreads();
+  int t0, nt;
+  units_of(p, total, fresh, &t0, &nt);
+  for (int k = 0; k < 4; ++k) {
+    const int j = j0 + k * kMergeThreads + tid;
+    if (j >= total) break;
+    const long long at = (long long)bg * p.C + j;
+    float w = 0.f;
+    if (j >= t0 * kBlockUnit)
+      for (int r = 0; r < nrows; ++r)
+        w += ex2(p.stash[((long long)bg * p.S * p.G + r) * p.stash_ld + j] - lse[r]);
+    if (p.past_w && j < total - fresh) w += p.past_w[at];
+    p.present_w[at] = w;
+  }
+}
+
+// ------------------------------------------------------------------ weights of long chunks
+
+constexpr int kWKeys = 64;       // cache rows per block, 16 per warp
+constexpr int kWRows = 64;       // query rows staged at a time
+
+// present_weights from the rows' log-sum-exp: a warp holds 16 keys as the A
+// operand and runs over the query rows (B operand, staged in shared memory in
+// fragment order, hi and lo parts for fp32).
+template <typename T, int HP>
+__global__ void __launch_bounds__(128)
+block_weights_kernel(const BlockParams p) {
+  constexpr bool kHalf = sizeof(T) == 2;
+  constexpr int kSteps = HP / 16;
+  constexpr int kParts = kHalf ? 1 : 2;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  uint2* qs = reinterpret_cast<uint2*>(smem_raw);              // [row tile of 8][step][part][lane]
+  float4* rp = reinterpret_cast<float4*>(smem_raw + kWRows * HP * 2 * kParts);  // per row: factor, lse, position
+  float* up = reinterpret_cast<float*>(rp + kWRows);                              // per row: 2^e of an fp32 row
+  const int bg = blockIdx.y, b = bg / p.Nkv, g = bg % p.Nkv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, t = lane & 3;
+  int total, fresh;
+  if (!block_lengths(p, b, &total, &fresh)) return;
+  const int j0 = blockIdx.x * kWKeys;
+  if (j0 >= total) return;
+  const int past = total - fresh, jw = j0 + 16 * warp;
+  const float ks = jw < total ? p.ks[(long long)bg * p.nblk + (jw >> p.bs_log2)] : 0.f;
+  uint32_t a[kSteps][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int j = jw + gq + 8 * h;
+    const int8_t* row = p.kc + ((long long)bg * p.C + j) * p.H;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int d = t * (HP / 4) + 4 * i;
+      const uint32_t w = (j < total && d < p.H ? *reinterpret_cast<const uint32_t*>(row + d) : 0u) ^ 0x80808080u;
+      a[i][h] = codes_lo(w);
+      a[i][2 + h] = codes_hi(w);
+    }
+  }
+  float sum[2] = {0.f, 0.f};
+  // Query rows that see a key of this block: positions j0 .. j0 + 63 + W.
+  const int i_lo = max(0, j0 - past);
+  const int i_hi = p.window >= 0 ? min(fresh, j0 + kWKeys + p.window - past) : fresh;
+  for (int r0 = i_lo * p.G; r0 < i_hi * p.G; r0 += kWRows) {
+    __syncthreads();
+    for (int x = tid; x < kWRows; x += 128) {
+      const int r = r0 + x;
+      float4 v = make_float4(0.f, INFINITY, 0.f, 0.f);   // a row that does not count: exp2(0 - inf) = 0
+      if (r < i_hi * p.G) {
+        v.x = p.softcap > 0.f ? p.scale : p.scale * kLog2e;
+        v.y = p.lse[(long long)bg * p.S * p.G + r];
+        v.z = __int_as_float(past + r / p.G);
+      }
+      rp[x] = v;
+    }
+    for (int x = warp; x < kWRows / 8; x += 4) {
+      const int r = r0 + 8 * x + gq;
+      const T* q = r < i_hi * p.G ? static_cast<const T*>(p.q) +
+                                        (((long long)b * p.S + r / p.G) * p.N + g * p.G + r % p.G) * p.H
+                                  : nullptr;
+      float down = 1.f;
+      if constexpr (!kHalf) {
+        float mx = 0.f;
+        for (int i = 0; i < kSteps; ++i) {
+          const int d = t * (HP / 4) + 4 * i;
+          if (q && d < p.H) {
+            const float4 v = *reinterpret_cast<const float4*>(q + d);
+            mx = fmax3(mx, fabsf(v.x), fabsf(v.y));
+            mx = fmax3(mx, fabsf(v.z), fabsf(v.w));
+          }
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int ex = (__float_as_int(mx) >> 23) & 0xff;
+        const int e = ex == 0 ? 0 : min(ex, 253) - 127;
+        down = __int_as_float((127 - e) << 23);
+        if (t == 0) up[8 * x + gq] = __int_as_float((127 + e) << 23);
+      }
+      for (int i = 0; i < kSteps; ++i) {
+        const int d = t * (HP / 4) + 4 * i;
+        uint2 hi = make_uint2(0u, 0u), lo = hi;
+        if (q && d < p.H) {
+          if constexpr (kHalf) {
+            hi = *reinterpret_cast<const uint2*>(q + d);
+          } else {
+            float4 v = *reinterpret_cast<const float4*>(q + d);
+            v.x *= down;
+            v.y *= down;
+            v.z *= down;
+            v.w *= down;
+            hi = make_uint2(pack(v.x, v.y), pack(v.z, v.w));
+            const float2 h0 = unpack(hi.x), h1 = unpack(hi.y);
+            lo = make_uint2(pack(v.x - h0.x, v.y - h0.y), pack(v.z - h1.x, v.w - h1.y));
+          }
+        }
+        qs[((x * kSteps + i) * kParts) * 32 + lane] = hi;
+        if constexpr (!kHalf) qs[((x * kSteps + i) * kParts + 1) * 32 + lane] = lo;
+      }
+    }
+    __syncthreads();
+    if (jw < total) {
+      for (int x = 0; x < kWRows / 8; ++x) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+          for (int part = 0; part < kParts; ++part) {
+            const uint2 q = qs[((x * kSteps + i) * kParts + part) * 32 + lane];
+            mma16816(c, a[i], q.x, q.y);
+          }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {   // rows 8 x + 2 t + u
+          const float4 v = rp[8 * x + 2 * t + u];
+          const int pos = __float_as_int(v.z);
+          const float f = v.x * ks * (kHalf ? 1.f : up[8 * x + 2 * t + u]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int j = jw + gq + 8 * h;
+            float z = c[2 * h + u] * f;
+            if (p.softcap > 0.f) z = p.softcap * kLog2e * tanhf(z / p.softcap);
+            const bool see = j <= pos && (p.window < 0 || j >= pos - p.window);
+            sum[h] += see ? ex2(z - v.y) : 0.f;
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+    sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+    const int j = jw + gq + 8 * h;
+    if (t == 0 && j < total) {
+      const long long at = (long long)bg * p.C + j;
+      p.present_w[at] = sum[h] + (p.past_w && j < past ? p.past_w[at] : 0.f);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ launches
+
+constexpr int kMaxDevices = 64;
+
+// Dynamic shared memory above 48 KB is allowed once per kernel and device.
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes, bool* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!done[dev]) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+    done[dev] = true;
+  }
+  return cudaSuccess;
+}
+
+template <typename T, int HP>
+cudaError_t attn_one(const BlockParams& p, cudaStream_t st) {
+  static bool done[kMaxDevices];
+  const int smem = kWarps * (int)sizeof(WarpSmem<T, HP>);
+  cudaError_t e = allow_smem(block_attn_kernel<T, HP>, smem, done);
+  if (e != cudaSuccess) return e;
+  block_attn_kernel<T, HP><<<(unsigned)(p.workers / kWarps), kWarps * 32, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T, int HP>
+cudaError_t weights_one(const BlockParams& p, cudaStream_t st) {
+  static bool done[kMaxDevices];
+  const int smem = kWRows * HP * 2 * (sizeof(T) == 2 ? 1 : 2) + kWRows * 20;
+  cudaError_t e = allow_smem(block_weights_kernel<T, HP>, smem, done);
+  if (e != cudaSuccess) return e;
+  block_weights_kernel<T, HP><<<dim3((unsigned)((p.T + kWKeys - 1) / kWKeys), (unsigned)(p.B * p.Nkv)), 128, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int block_row_tile(int t_type) { return t_type == kF16 ? 16 : 8; }
+
+// One worker per warp, two CTAs of four per SM (one for head sizes above 128);
+// fewer when there are not four units for each.
+int block_workers(const BlockParams& p) {
+  const long long most = 152LL * kWarps * (p.H > 128 ? 1 : 2);
+  const int keys = p.window >= 0 && (long long)p.window + p.S < p.T ? p.window + p.S + kBlockUnit : p.T;
+  const long long units =
+      (long long)p.B * p.Nkv * p.nrt * ((keys + kBlockUnit - 1) / kBlockUnit + kBlockRangeCost);
+  long long w = (units + 3) / 4;
+  w = (w + kWarps - 1) / kWarps * kWarps;
+  return (int)(w < most ? w : most);
+}
+
+cudaError_t launch_block_attn(const BlockParams& p, cudaStream_t st) {
+  if (p.t_type == kF16)
+    return p.H <= 64 ? attn_one<__half, 64>(p, st) : p.H <= 128 ? attn_one<__half, 128>(p, st) : attn_one<__half, 256>(p, st);
+  return p.H <= 64 ? attn_one<float, 64>(p, st) : p.H <= 128 ? attn_one<float, 128>(p, st) : attn_one<float, 256>(p, st);
+}
+
+cudaError_t launch_block_merge(const BlockParams& p, cudaStream_t st) {
+  const long long rows = (long long)p.B * p.Nkv * p.S * p.G;
+  const int chunks = p.stash ? (p.T + 4 * kMergeThreads - 1) / (4 * kMergeThreads) : 0;
+  const long long blocks = rows + (long long)p.B * p.Nkv * chunks;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (p.t_type == kF16)
+    block_merge_kernel<__half><<<(unsigned)blocks, kMergeThreads, 0, st>>>(p, rows, chunks);
+  else
+    block_merge_kernel<float><<<(unsigned)blocks, kMergeThreads, 0, st>>>(p, rows, chunks);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_block_weights(const BlockParams& p, cudaStream_t st) {
+  if (p.t_type == kF16)
+    return p.H <= 64 ? weights_one<__half, 64>(p, st) : p.H <= 128 ? weights_one<__half, 128>(p, st) : weights_one<__half, 256>(p, st);
+  return p.H <= 64 ? weights_one<float, 64>(p, st) : p.H <= 128 ? weights_one<float, 128>(p, st) : weights_one<float, 256>(p, st);
+}
+
+}  // namespace gqa

@@ -1,0 +1,94 @@
+// Internal interface of the multi-axis rotary, the block-scaled int8 cache and
+// its eviction: parameter blocks and launchers (block_api.cu fills them in).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gqa_internal.h"
+
+namespace gqa {
+
+constexpr int kRotaryChunks = 16;  // 8-pair chunks of a head (head size up to 256)
+
+struct RotaryAxesParams {
+  const void *q, *k;        // k null: queries only
+  void *qo, *ko;
+  const int* pos;           // [axes][tokens]
+  const void *cos_c, *sin_c;
+  const void *qw, *kw;      // norm weights or null
+  uint32_t* status;
+  long long tokens;         // B * S
+  int N, Nkv, H, pairs, table_rows;
+  int table_f32;            // table dtype: 1 fp32, 0 T
+  float eps;
+  unsigned axis_nibbles[kRotaryChunks];  // axes of pairs 8 l .. 8 l + 7, 4 bits each
+  unsigned char chunk_uniform[kRotaryChunks];  // the eight pairs share one axis
+};
+cudaError_t launch_rotary_axes(const RotaryAxesParams& p, int t_type, cudaStream_t st);
+
+struct BlockParams {
+  int B, S, N, Nkv, G, H;
+  int C, T;              // cache capacity, total_sequence_length
+  int bs_log2, nblk;     // log2 of the block size, blocks of a (b, g)
+  int t_type;
+  int window;            // -1: none
+  float scale, softcap;
+  int smooth;
+  const void *q, *k, *v;  // k / v null: nothing to append
+  void* out;
+  int8_t *kc, *vc;
+  float *ks, *vs;
+  const int *seqlens, *new_lens;
+  const void* sink;
+  const float* past_w;
+  float* present_w;      // null: no weights
+  uint32_t* status;
+  // split-KV kernel
+  int rt_rows, nrt;      // rows of a row tile, row tiles of a (b, g)
+  int workers;           // warps of the grid
+  float *part_o, *part_ml;
+  float* stash;          // log2-domain scores [B*Nkv][S*G][stash_ld] (one row tile), or null
+  int stash_ld;
+  float* lse;            // log2-domain log-sum-exp [B*Nkv][S*G], or null
+  // tensor-core prefill
+  long long wait_budget;
+  int withhold_tile;
+};
+
+// Lengths of one sequence; false when they break the contract.
+__host__ __device__ inline bool block_lengths(const BlockParams& p, int b, int* total, int* fresh) {
+  *total = p.seqlens[b] + 1;
+  *fresh = p.new_lens ? p.new_lens[b] : p.S;
+  return *total >= 0 && *total <= p.T && *fresh >= 0 && *fresh <= p.S && *fresh <= *total;
+}
+
+cudaError_t launch_block_append(const BlockParams& p, cudaStream_t st);
+// Split-KV attention on warp MMAs, every shape.
+constexpr int kBlockUnit = 32;      // keys per work unit
+constexpr int kBlockRangeCost = 2;  // work units a range's start and end are counted as
+int block_row_tile(int t_type);     // query rows per row tile
+int block_workers(const BlockParams& p);
+cudaError_t launch_block_attn(const BlockParams& p, cudaStream_t st);
+cudaError_t launch_block_merge(const BlockParams& p, cudaStream_t st);
+// Attention weights of the cache rows from the log-sum-exp of every query row.
+cudaError_t launch_block_weights(const BlockParams& p, cudaStream_t st);
+
+struct EvictParams {
+  int B, Nkv, H, C, Cto, T;
+  int bs_log2, nblk, nblk_to;
+  int keep, recent, first;
+  const int8_t *kc, *vc;
+  const float *ks, *vs;
+  int8_t *kc_to, *vc_to;
+  float *ks_to, *vs_to;
+  const float* w;
+  float* w_to;           // or null
+  const int* seqlens;
+  int *kept, *seqlens_to;
+  uint32_t* status;
+};
+cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t st);
+cudaError_t launch_evict_gather(const EvictParams& p, cudaStream_t st);
+
+}  // namespace gqa

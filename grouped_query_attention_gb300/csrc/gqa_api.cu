@@ -18,48 +18,25 @@
 #include <vector>
 
 #include "../../include/gqa.h"
+#include "gqa_host.h"
 #include "gqa_internal.h"
 
-struct gqa_handle {
-  gqa_attrs attrs;
-  long long wait_budget;    // bound of each pipeline wait of the tensor-core kernels (clock cycles)
-  int withhold_tile;        // >= 0: testing the timeout path (see gqa_set_wait_limit)
-  // per-launch profiling (gqa_profile_begin / gqa_profile_end)
-  bool profiling;
-  std::vector<cudaEvent_t> events;  // 2 per launch
-  std::vector<int> kinds;
-  int used;
-};
+using gqa::align_up;
+using gqa::check_aligned;
+using gqa::cuda_fail;
+using gqa::fail;
+using gqa::kAlign;
+using gqa::present;
+using gqa::shape_is;
+using gqa::timed_launch;
 
 namespace {
 
-thread_local std::string g_last_error;
+// Reason of the last failure on this thread (fixed storage: recording it cannot fail).
+thread_local char g_last_error[512];
 
-gqa_status fail(gqa_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-gqa_status fail(gqa_status s, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_last_error = buf;
-  return s;
-}
-
-constexpr size_t kAlign = 256;
 constexpr long long kDefaultWaitBudget = 4000000000LL;   // clock cycles, about 2 s at the maximum SM clock
 constexpr long long kDecodeTargetCtas = 152LL * 16;  // GB300: 152 SMs, ~16 split CTAs per SM
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-bool present(const gqa_tensor& t) { return t.data != nullptr; }
-
-bool shape_is(const gqa_tensor& t, int ndim, const int64_t* s) {
-  if (t.ndim != ndim) return false;
-  for (int i = 0; i < ndim; ++i)
-    if (t.shape[i] != s[i]) return false;
-  return true;
-}
 
 std::string shape_str(const gqa_tensor& t) {
   std::string r = "(";
@@ -81,12 +58,6 @@ struct Plan {
   bool bias_staged;  // tensor-core prefill with the bias staged by a small kernel and copied by TMA
   size_t part_rows;  // decode partial rows (part_o holds part_rows x H floats, part_ml part_rows x 2)
 };
-
-gqa_status check_aligned(const gqa_tensor& t, const char* name) {
-  if (present(t) && (reinterpret_cast<uintptr_t>(t.data) & 15u) != 0)
-    return fail(GQA_ERR_INVALID_ARGUMENT, "%s: data pointer is not 16-byte aligned", name);
-  return GQA_OK;
-}
 
 gqa_status plan_call(const gqa_handle* hd, const gqa_inputs* in, const gqa_outputs* out, Plan* pl) {
   if (!hd || !in || !out || !pl) return fail(GQA_ERR_INVALID_ARGUMENT, "NULL handle, inputs or outputs");
@@ -386,23 +357,6 @@ void bind_workspace(Plan* pl, void* ws) {
   }
 }
 
-gqa_status cuda_fail(cudaError_t e, const char* what) {
-  return fail(GQA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-// Launch through `fn`, bracketed by an event pair when the handle is profiling.
-template <typename F>
-cudaError_t timed_launch(gqa_handle* h, int kind, cudaStream_t st, F fn) {
-  const bool rec = h->profiling && h->used < (int)h->kinds.size();
-  if (rec) cudaEventRecord(h->events[2 * h->used], st);
-  cudaError_t e = fn();
-  if (rec) {
-    cudaEventRecord(h->events[2 * h->used + 1], st);
-    h->kinds[h->used++] = kind;
-  }
-  return e;
-}
-
 // The decode launch a plan selected.
 cudaError_t launch_decode_any(const Plan& pl, cudaStream_t st, const gqa::TmaMaps& maps) {
   if (!pl.tc_decode) return gqa::launch_decode(pl.P, st);
@@ -410,6 +364,18 @@ cudaError_t launch_decode_any(const Plan& pl, cudaStream_t st, const gqa::TmaMap
 }
 
 }  // namespace
+
+namespace gqa {
+
+gqa_status fail(gqa_status s, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
+  va_end(ap);
+  return s;
+}
+
+}  // namespace gqa
 
 extern "C" {
 
@@ -660,6 +626,6 @@ const char* gqa_status_string(gqa_status s) {
   return "GQA_ERR_UNKNOWN";
 }
 
-const char* gqa_last_error(void) { return g_last_error.c_str(); }
+const char* gqa_last_error(void) { return g_last_error; }
 
 }  // extern "C"

@@ -263,10 +263,160 @@ typedef struct gqa_plan_info {
 GQA_API gqa_status gqa_describe_plan(const gqa_handle* handle, const gqa_inputs* in, const gqa_outputs* out,
                                      gqa_plan_info* info);
 
+/* ---- Rotary embedding with several position axes -------------------------
+ * Adjacent to section Attributes, do_rotary, whose single position is a row's
+ * place in its sequence. Here every token has one position on each of
+ * num_axes axes (time, height, width, ...), and each rotated pair takes its
+ * angle from one of them:
+ *   y[d]     = x[d] c - x[d+D] s,   y[d+D] = x[d+D] c + x[d] s,   d < D,
+ *   c = cos_cache[p][d], s = sin_cache[p][d], p = positions[axis(d)][b][i],
+ * D = sum of sections (2 D <= head size; coordinates from 2 D on pass through).
+ * axis(d): interleaved == 0: the first sections[0] pairs take axis 0, the next
+ * sections[1] axis 1, and so on. interleaved == 1: pair d takes axis
+ * r = d % num_axes while d < num_axes * sections[r], else axis 0 (sections[0]
+ * is then the number of pairs left for axis 0).
+ * With norm weights x is first RMS normalised, x / sqrt(mean(x^2) + eps) * w
+ * (qk_norm_epsilon of the handle). Computed in fp32, rounded once; for head
+ * sizes 64, 128 and 256 the operation order is that of the rows gqa_forward
+ * stores (equal bytes at equal positions). Positions are explicit, so rows of
+ * a cache that gqa_block_evict has compacted keep their own.
+ *   query      T (B, S, N*H);  key T (B, S, N_kv*H) or absent
+ *   positions  int32 (num_axes, B, S), each in [0, R); a token with another
+ *              position is not written and sets GQA_DEVICE_BAD_ROTARY
+ *   cos/sin_cache  T or float32 (R, D)
+ *   q/k_norm_weight T (H): both or neither (without key: q only)
+ * Outputs have the inputs' shapes; each may be its input (in place) and may
+ * not overlap another tensor. D is a multiple of 8, num_axes 1 .. 8. */
+#define GQA_MAX_ROTARY_AXES 8
+typedef struct gqa_rotary_inputs {
+  gqa_tensor query, key;
+  gqa_tensor positions;
+  gqa_tensor cos_cache, sin_cache;
+  gqa_tensor q_norm_weight, k_norm_weight;
+  int32_t sections[GQA_MAX_ROTARY_AXES]; /* pairs of each axis (host values) */
+  int32_t num_axes;
+  int32_t interleaved;
+} gqa_rotary_inputs;
+
+typedef struct gqa_rotary_outputs {
+  gqa_tensor query, key;
+} gqa_rotary_outputs;
+
+/* One launch on `stream`. Of the handle's attributes only the head counts and
+ * qk_norm_epsilon apply. status: see gqa_block_forward. */
+GQA_API gqa_status gqa_rotary_axes(gqa_handle* handle, const gqa_rotary_inputs* in, const gqa_rotary_outputs* out,
+                                   void* status, void* stream);
+
+/* ---- int8 cache with a scale for each block of tokens and KV head ---------
+ * Beside the per-tensor and per-channel scales of section Inputs (k_scale,
+ * v_scale), which are fixed by the caller, these belong to the cache and
+ * follow the data. Row r of head g of sequence b is
+ *   value[d] = code[b][g][r][d] * scale[b][g][r / block_size].
+ *   key/value_codes   int8 (B, N_kv, C, H)
+ *   key/value_scales  float32 (B, N_kv, ceil(C / block_size))
+ *   block_size        16, 32, 64, 128 or 256 tokens */
+typedef struct gqa_block_cache {
+  gqa_tensor key_codes, value_codes;
+  gqa_tensor key_scales, value_scales;
+  int32_t block_size;
+} gqa_block_cache;
+
+/* Inputs of one step. total_b = seqlens_k[b] + 1 is the number of live cache
+ * rows of sequence b after the step; the last n_b = new_lens[b] (S without
+ * new_lens; 0 <= n_b <= min(S, total_b)) of them belong to the first n_b rows
+ * of query (key, value); rows n_b .. S-1 are padding. seqlens_k[b] may be -1
+ * with n_b = 0 (an empty slot).
+ *   query            T (B, S, N*H), prepared (see gqa_rotary_axes)
+ *   key, value       T (B, S, N_kv*H), or both absent: the rows are in the cache already
+ *   seqlens_k        int32 (B);  new_lens int32 (B) or absent
+ *   head_sink        T (N) or absent
+ *   past_weights     float32 (B, N_kv, C) or absent (read as zeros)
+ *   total_sequence_length  HOST scalar, at least the largest total_b, at most C */
+typedef struct gqa_block_inputs {
+  gqa_tensor query, key, value;
+  gqa_tensor seqlens_k, new_lens;
+  gqa_tensor head_sink;
+  gqa_tensor past_weights;
+  int32_t total_sequence_length;
+} gqa_block_inputs;
+
+/*   output           T (B, S, N*H); padding rows are written as 0
+ *   present_weights  float32 (B, N_kv, C) or absent; may be past_weights itself */
+typedef struct gqa_block_outputs {
+  gqa_tensor output;
+  gqa_tensor present_weights;
+} gqa_block_outputs;
+
+/* Bytes of workspace gqa_block_forward needs for these shapes (host-only; runs
+ * every host-side check). May be 0. */
+GQA_API gqa_status gqa_block_workspace_size(const gqa_handle* handle, const gqa_block_cache* cache,
+                                            const gqa_block_inputs* in, const gqa_block_outputs* out, size_t* bytes);
+
+/* One step over a block-scaled cache, on `stream`:
+ *   1. with key / value, store the new rows at cache rows total_b - n_b ..
+ *      total_b - 1. The scale of a block is max|x| over the rows stored in
+ *      it times fp32(1/127), rounded to fp32; a block that already holds rows keeps its
+ *      scale when the new rows need no larger one, else it takes the larger
+ *      one and its old codes are rounded anew. A code is the integer nearest
+ *      to the exact quotient x / scale, ties to even, within +-127. An
+ *      infinite x becomes +-127 and a NaN 0, and neither enters the scale.
+ *   2. output[b, i, h] = softmax over the visible rows j of scale * q . k_j
+ *      (softcap c: c tanh(s / c)), times the values; query row i stands at
+ *      cache row p = total_b - n_b + i and sees rows max(0, p - W) .. p, W =
+ *      local_window_size (all rows up to p without a window); query head h
+ *      reads KV head h / (N / N_kv). head_sink / smooth_softmax add a logit to
+ *      the denominator as in gqa_forward.
+ *   3. with present_weights: present_weights[b, g, j] = past_weights[b, g, j]
+ *      (0 for j >= total_b - n_b) + the sum over the n_b rows and the heads of
+ *      group g of the probability of row j, for j < total_b. Other entries
+ *      keep their values. No atomics: a call's result does not vary.
+ * Rows of the cache behind total_b keep their bytes. Attributes used:
+ * num_heads, kv_num_heads, local_window_size, scale, softcap, smooth_softmax;
+ * causal must be 1 and do_rotary, the quant types and sliding_window_cache off.
+ * workspace: at least gqa_block_workspace_size bytes, 256-byte aligned, not
+ * used concurrently by another call; its contents need not survive.
+ * status: one device uint32 (4-byte aligned) or NULL. Data errors (lengths out
+ * of range: that sequence is skipped, nothing of it is written) OR
+ * GQA_DEVICE_* bits into it; it is never cleared here: clear it once before
+ * its first use, and read and clear it with gqa_read_device_status. */
+GQA_API gqa_status gqa_block_forward(gqa_handle* handle, const gqa_block_cache* cache, const gqa_block_inputs* in,
+                                     const gqa_block_outputs* out, void* workspace, size_t workspace_bytes,
+                                     void* status, void* stream);
+
+/* Eviction from a block-scaled cache by accumulated attention weight: the live
+ * rows of every (sequence, KV head) are reduced to at most `keep`, copied in
+ * their order to rows 0 .. of another cache. Sequences with total_b <= keep
+ * keep all rows. Otherwise rows [0, first) and the `recent` last ones stay,
+ * and of the rows between them the keep - first - recent with the largest
+ * weights (equal weights: the lower row first; a NaN counts as the lowest).
+ *   from, into       caches of the same B, N_kv, H and block_size; into has
+ *                    C >= min(keep, total_sequence_length) and shares no memory with `from`
+ *   weights          float32 (B, N_kv, from C);  seqlens_k int32 (B)
+ *   into_weights     float32 (B, N_kv, into C) or absent: the kept rows' weights
+ *   kept             int32 (B, N_kv, keep): source row of each kept row, -1 behind the last
+ *   into_seqlens_k   int32 (B): min(total_b, keep) - 1
+ * A block of `into` takes the largest scale among its rows' source blocks;
+ * rows of a block with that scale keep their codes, the others are rounded
+ * anew (nearest, ties to even). Rows and blocks behind the last kept row keep
+ * their bytes. A sequence with total_b outside [0, min(C, total_sequence_length)]
+ * is skipped and sets GQA_DEVICE_BAD_SEQLEN.
+ * 0 <= first, 0 <= recent, 1 <= keep, first + recent <= keep. */
+typedef struct gqa_evict_args {
+  gqa_block_cache from, into;
+  gqa_tensor weights, seqlens_k;
+  gqa_tensor into_weights, kept, into_seqlens_k;
+  int32_t total_sequence_length;
+  int32_t keep, recent, first;
+} gqa_evict_args;
+
+/* Two launches on `stream`, no workspace; of the handle's attributes only
+ * kv_num_heads applies. */
+GQA_API gqa_status gqa_block_evict(gqa_handle* handle, const gqa_evict_args* args, void* status, void* stream);
+
 /* Per-launch timing for measurement tools. gqa_profile_begin creates
  * 2*max_launches CUDA events (host-side driver objects, no device memory);
- * while profiling is on, every gqa_forward / gqa_forward_noalloc call on this
- * handle records an event pair around each kernel it launches (up to
+ * while profiling is on, every call on this handle that launches kernels
+ * records an event pair around each kernel it launches (up to
  * max_launches launches in total). gqa_profile_end synchronises the events,
  * writes up to `capacity` (kind, milliseconds) pairs in launch order, sets
  * *count to the number of launches recorded, releases the events and turns
@@ -279,6 +429,14 @@ GQA_API gqa_status gqa_describe_plan(const gqa_handle* handle, const gqa_inputs*
 #define GQA_KERNEL_DECODE_TENSOR_CORE 6
 #define GQA_KERNEL_WINDOW_SHIFT 7
 #define GQA_KERNEL_BIAS_STAGE 8
+#define GQA_KERNEL_ROTARY_AXES 9
+#define GQA_KERNEL_BLOCK_APPEND 10
+#define GQA_KERNEL_BLOCK_ATTENTION 11
+#define GQA_KERNEL_BLOCK_MERGE 12
+#define GQA_KERNEL_BLOCK_PREFILL 13
+#define GQA_KERNEL_BLOCK_WEIGHTS 14
+#define GQA_KERNEL_EVICT_SELECT 15
+#define GQA_KERNEL_EVICT_GATHER 16
 GQA_API gqa_status gqa_profile_begin(gqa_handle* handle, int32_t max_launches);
 GQA_API gqa_status gqa_profile_end(gqa_handle* handle, int32_t* kinds, float* ms, int32_t capacity, int32_t* count);
 

@@ -115,7 +115,7 @@ gqa_status check_block_cache(const gqa_block_cache& c, const char* name, long lo
     if (t->dtype != GQA_F32 || !shape_is(*t, 3, ss))
       return fail(GQA_ERR_INVALID_ARGUMENT, "%s: scales must be float32 (B, kv_num_heads, ceil(C / block_size)) = (%lld,%lld,%lld)",
                   name, B, Nkv, (long long)ss[2]);
-  if (*C > (1LL << 30) || B * Nkv > 65535 || B * Nkv * *C > kElems / H)
+  if (*C > (1LL << 30) || B * Nkv > 65535 || B * Nkv * *C >= (1LL << 31))   // TMA rows are 32-bit
     return fail(GQA_ERR_UNSUPPORTED, "%s: tensor too large", name);
   return GQA_OK;
 }
@@ -207,7 +207,7 @@ gqa_status plan_block(const gqa_handle* h, const gqa_block_cache* cache, const g
   P.withhold_tile = h->withhold_tile;
 
   const long long rows = S * G;
-  P.rt_rows = gqa::block_row_tile(P.t_type);
+  P.rt_rows = gqa::block_row_tile(P.t_type, (int)H, rows);
   P.nrt = (int)((rows + P.rt_rows - 1) / P.rt_rows);
   P.workers = gqa::block_workers(P);
   const size_t slots = (size_t)P.workers + (size_t)(B * Nkv) * P.nrt;
@@ -217,7 +217,8 @@ gqa_status plan_block(const gqa_handle* h, const gqa_block_cache* cache, const g
   if (P.present_w) {
     if (P.nrt == 1) {
       P.stash_ld = (int)((T + gqa::kBlockUnit - 1) / gqa::kBlockUnit * gqa::kBlockUnit);
-      pl->stash = align_up((size_t)(B * Nkv * rows) * P.stash_ld * sizeof(float));
+      P.stash_rows = (int)((rows + 1) & ~1LL);
+      pl->stash = align_up((size_t)(B * Nkv) * P.stash_ld * P.stash_rows * sizeof(float));
     } else {
       pl->lse = align_up((size_t)(B * Nkv * rows) * sizeof(float));
     }

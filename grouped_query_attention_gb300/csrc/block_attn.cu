@@ -2,26 +2,31 @@
 // steps, short chunks, and every shape the tensor-core prefill does not take).
 //
 // Rows of a KV head (b, g): query rows (position, grouped head), in row tiles
-// of 16 (fp16) or 8 (fp32). One warp MMA (m16n8k16, fp16 in, fp32 sums) takes
-// the 16 rows against 8 keys (scores) or against 8 coordinates (output). The
-// codes are small integers, exact in fp16; the block's K scale multiplies the
-// scores, its V scale the probabilities (both are one number for 16 keys).
-// fp32 queries keep their precision as two fp16 parts: MMA rows 0..7 hold
-// hi = fp16(q 2^-e), rows 8..15 lo = fp16(q 2^-e - hi), 2^e from the row's
-// largest value, and the two halves of the accumulator are added; so are
-// P_hi and P_lo. That fills the rows an 8-row tile would leave idle.
+// of 8 or 16. A decode step has a few rows against many keys, so the keys are
+// the M side of the warp MMA (m16n8k16, fp16 in, fp32 sums): S^T = K Q^T takes
+// 16 keys against 8 rows, O^T += V^T P^T 16 coordinates against 8 rows, and a
+// row tile of 8 leaves nothing idle. P^T leaves the first product with keys
+// along the lanes and enters the second with rows along them: one 8 x 8
+// transpose (movmatrix) per 8 keys. The codes are small integers, exact in
+// fp16; the block's K scale multiplies the scores, its V scale the
+// probabilities (both are one number for 16 keys). fp32 queries and
+// probabilities keep their precision as two fp16 parts, hi = fp16(x) and
+// lo = fp16(x - hi) (queries brought to [1, 2) by a power of two per row).
 //
-// Bound: HBM, 2 H bytes per cache row. Every warp is a worker of its own: the
-// 32-key units of all ranges (b, g, row tile) are laid end to end, a worker
-// takes an equal share, copies its units through a private ring with
-// asynchronous 16-byte copies (chunks swizzled so that the fragment reads do
-// not conflict), and nothing waits for another warp. A worker's piece of a
-// range ends as a partial (m, l, O) in the workspace; a second launch merges
-// the pieces of each row and adds the attention weights of the cache rows.
+// Bound: HBM, 2 H bytes per cache row; the instructions that turn codes into
+// fp16 fragments (11 per 4-code word of K and of V) come next. Every warp is a
+// worker of its own: the 32-key units of all ranges (b, g, row tile) are laid
+// end to end, a worker takes an equal share, copies its units by TMA through a
+// private ring (128-byte swizzle, so the fragment reads do not conflict), and
+// nothing waits for another warp. A worker's piece of a range ends as a
+// partial (m, l, O) in the workspace; a second launch merges the pieces of
+// each row and adds the attention weights of the cache rows.
 #include <cuda_fp16.h>
 
 #include "block_internal.h"
 #include "common.cuh"
+#include "tcgen05.cuh"
+#include "tma_host.h"
 
 namespace gqa {
 namespace {
@@ -35,9 +40,13 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Transpose of an 8 x 8 matrix of fp16 pairs held by a warp (row lane / 4, columns 2 (lane % 4), + 1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
+
 // Four bytes, or zeros when !on.
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool on) {
   const int n = on ? 4 : 0;
@@ -68,11 +77,12 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
 }
 __device__ __forceinline__ float2 unpack(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
 
-// 16-byte chunk `c` of row `r` of a staged tile of HP-byte rows.
+// 16-byte chunk `c` of row `r` of a 32-row tile as TMA lands it: rows of 64
+// bytes (64-byte swizzle) or boxes of 128-byte rows (128-byte swizzle).
 template <int HP>
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   if constexpr (HP == 64) return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-  return (uint32_t)(r * HP + (((c & ~7) | ((c ^ r) & 7)) << 4));
+  return (uint32_t)((c >> 3) * (kBlockUnit * 128) + r * 128 + (((c ^ r) & 7) << 4));
 }
 
 // Key range of sequence b shared by its row tiles: units [t0, t0 + nt).
@@ -181,106 +191,95 @@ struct Walk {
   }
 };
 
+constexpr int kStages = 2;   // units in the ring: one being read, one landing
+
 template <int HP>
-struct RingShape {
-  static constexpr int kStages = HP == 64 ? 6 : 3;
-  static constexpr int kStageBytes = 2 * kBlockUnit * HP;   // K tile, V tile
+struct __align__(1024) WarpSmem {
+  uint8_t ring[kStages][2 * kBlockUnit * HP];   // K tile, V tile
+};
+struct WarpCtl {
+  float sc[kStages][4];    // K scales of the unit's two 16-key groups, V scales
+  uint64_t full[kStages];
 };
 
-template <typename T, int HP>
-struct __align__(16) WarpSmem {
-  uint8_t ring[RingShape<HP>::kStages][RingShape<HP>::kStageBytes];
-  float sc[RingShape<HP>::kStages][4];    // K scales of the unit's two 16-key groups, V scales
-  uint4 q[HP > 128 ? HP / 16 * 32 : 1];   // query fragments of the large head sizes
-};
-
-// Fragments of the row tile's queries: thread t of a quad holds coordinates
-// t HP/4 .. of its rows (the order of the contraction is free as long as the
-// keys use the same), four per MMA step. Returns the factor of the scores.
-template <typename T, int HP>
-__device__ float load_queries(const BlockParams& p, int b, int g, int rt, uint32_t (*qf)[4], uint4* qs) {
-  const int lane = threadIdx.x & 31, gq = lane >> 2, t = lane & 3;
-  const int nrows = p.S * p.G, r0 = rt * p.rt_rows;
-  constexpr bool kF16 = sizeof(T) == 2;
-  const T* row[2];
-#pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    const int r = r0 + gq + (kF16 ? 8 * hf : 0);
-    row[hf] = r < nrows ? static_cast<const T*>(p.q) +
-                              ((long long)(b * (long long)p.S + r / p.G) * p.N + g * p.G + r % p.G) * p.H
-                        : nullptr;
-  }
-  float up = 1.f, down = 1.f;
-  if constexpr (!kF16) {
-    float mx = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < HP / 16; ++ks) {
-      const int d = t * (HP / 4) + 4 * ks;
-      if (row[0] && d < p.H) {
-        const float4 v = *reinterpret_cast<const float4*>(row[0] + d);
-        mx = fmax3(mx, fabsf(v.x), fabsf(v.y));
-        mx = fmax3(mx, fabsf(v.z), fabsf(v.w));
-      }
-    }
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    const int ex = (__float_as_int(mx) >> 23) & 0xff;
-    const int e = ex == 0 ? 0 : min(ex, 253) - 127;
-    down = __int_as_float((127 - e) << 23);
-    up = __int_as_float((127 + e) << 23);
-  }
-#pragma unroll
-  for (int ks = 0; ks < HP / 16; ++ks) {
-    const int d = t * (HP / 4) + 4 * ks;
-    uint32_t a[4] = {0u, 0u, 0u, 0u};
-    if constexpr (kF16) {
-      if (row[0] && d < p.H) {
-        const uint2 v = *reinterpret_cast<const uint2*>(row[0] + d);
-        a[0] = v.x;
-        a[2] = v.y;
-      }
-      if (row[1] && d < p.H) {
-        const uint2 v = *reinterpret_cast<const uint2*>(row[1] + d);
-        a[1] = v.x;
-        a[3] = v.y;
-      }
-    } else if (row[0] && d < p.H) {
-      float4 v = *reinterpret_cast<const float4*>(row[0] + d);
-      v.x *= down;
-      v.y *= down;
-      v.z *= down;
-      v.w *= down;
-      a[0] = pack(v.x, v.y);
-      a[2] = pack(v.z, v.w);
-      const float2 h0 = unpack(a[0]), h1 = unpack(a[2]);
-      a[1] = pack(v.x - h0.x, v.y - h0.y);
-      a[3] = pack(v.z - h1.x, v.w - h1.y);
-    }
-    if constexpr (HP > 128) {
-      qs[ks * 32 + lane] = make_uint4(a[0], a[1], a[2], a[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) qf[ks][i] = a[i];
-    }
-  }
-  return up;
+// CTAs per SM the registers and the ring leave room for.
+template <int HP, int NT>
+constexpr int ctas_per_sm() {
+  return HP > 128 ? 1 : NT > 1 ? 2 : 3;
 }
 
-template <typename T, int HP>
-__global__ void __launch_bounds__(kWarps * 32, HP > 128 ? 1 : 2)
-block_attn_kernel(const BlockParams p) {
+// Query fragments of a row tile: thread t of a quad holds coordinates t HP/4
+// .. of row gq of every 8-row tile (the order of the contraction is free as
+// long as the keys use the same), four per MMA step. up[n]: the power of two
+// an fp32 row was divided by.
+template <typename T, int HP, int NT>
+__device__ void load_queries(const BlockParams& p, int b, int g, int rt, uint2 (*qf)[HP / 16], float* up) {
   constexpr bool kHalf = sizeof(T) == 2;
-  constexpr int kStages = RingShape<HP>::kStages;
-  constexpr int kTileBytes = kBlockUnit * HP;
-  constexpr int kSteps = HP / 16;           // MMA steps over the coordinates
-  constexpr int kNT = HP / 8;               // output tiles of 8 coordinates
-  constexpr float kGrow = 4.f;              // log2 growth of a maximum tolerated before rescaling
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  WarpSmem<T, HP>& sm = reinterpret_cast<WarpSmem<T, HP>*>(smem_raw)[threadIdx.x >> 5];
   const int lane = threadIdx.x & 31, gq = lane >> 2, t = lane & 3;
-  const long long worker = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int r = rt * p.rt_rows + 8 * n + gq;
+    const T* row = r < p.S * p.G ? static_cast<const T*>(p.q) +
+                                       ((b * (long long)p.S + r / p.G) * p.N + g * p.G + r % p.G) * p.H
+                                 : nullptr;
+    if constexpr (kHalf) {
+      up[n] = 1.f;
+#pragma unroll
+      for (int ks = 0; ks < HP / 16; ++ks) {
+        const int d = t * (HP / 4) + 4 * ks;
+        qf[n][ks] = row && d < p.H ? *reinterpret_cast<const uint2*>(row + d) : make_uint2(0u, 0u);
+      }
+    } else {
+      float4 v[HP / 16];
+      float mx = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < HP / 16; ++ks) {
+        const int d = t * (HP / 4) + 4 * ks;
+        v[ks] = row && d < p.H ? *reinterpret_cast<const float4*>(row + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        mx = fmax3(mx, fabsf(v[ks].x), fabsf(v[ks].y));
+        mx = fmax3(mx, fabsf(v[ks].z), fabsf(v[ks].w));
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int ex = (__float_as_int(mx) >> 23) & 0xff;
+      const int e = ex == 0 ? 0 : min(ex, 253) - 127;
+      const float down = __int_as_float((127 - e) << 23);
+      up[n] = __int_as_float((127 + e) << 23);
+#pragma unroll
+      for (int ks = 0; ks < HP / 16; ++ks) {   // hi parts in tile n, lo parts in tile NT + n
+        const float4 x = make_float4(v[ks].x * down, v[ks].y * down, v[ks].z * down, v[ks].w * down);
+        const uint2 hi = make_uint2(pack(x.x, x.y), pack(x.z, x.w));
+        const float2 h0 = unpack(hi.x), h1 = unpack(hi.y);
+        qf[n][ks] = hi;
+        qf[NT + n][ks] = make_uint2(pack(x.x - h0.x, x.y - h0.y), pack(x.z - h1.x, x.w - h1.y));
+      }
+    }
+  }
+}
 
-  if (blockIdx.x == 0 && threadIdx.x < 32 && p.status) {   // lengths out of range
+// NT: 8-row tiles of a row tile. PLAIN: no softcap and no score stash.
+template <typename T, int HP, int NT, bool PLAIN>
+__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<HP, NT>())
+block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+  constexpr bool kHalf = sizeof(T) == 2;
+  constexpr int kParts = kHalf ? 1 : 2;     // fp16 parts of queries and probabilities
+  constexpr int kTileBytes = kBlockUnit * HP;
+  constexpr int kSteps = HP / 16;           // MMA steps over the coordinates; output tiles of 16 coordinates
+  constexpr float kGrow = 4.f;              // log2 growth of a maximum tolerated before rescaling
+  extern __shared__ uint8_t smem_raw[];
+  WarpSmem<HP>* rings = reinterpret_cast<WarpSmem<HP>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ WarpCtl ctls[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, t = lane & 3;
+  WarpSmem<HP>& sm = rings[warp];
+  WarpCtl& ctl = ctls[warp];
+  const long long worker = (long long)blockIdx.x * kWarps + warp;
+
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) tc::mbar_init(&ctl.full[s], 1);
+    tc::mbar_fence_init();
+  }
+  __syncwarp();
+  if (blockIdx.x == 0 && warp == 0 && p.status) {   // lengths out of range
     bool bad = false;
     for (int b = lane; b < p.B; b += 32) {
       int a, f;
@@ -295,36 +294,27 @@ block_attn_kernel(const BlockParams p) {
   ld.start(p, u0, u1 - u0);
   cp = ld;
 
-  const int chunks = p.H / 16;
+  int fetched = 0;
   // Start the copies of the unit at `ld` into stage s and move on.
   auto fetch = [&](int s) {
-    if (ld.left > 0) {
-      const int j0 = (ld.t0 + ld.off) * kBlockUnit, rows = min(kBlockUnit, ld.total - j0);
-      const long long bg = (long long)ld.b * p.Nkv + ld.gr / p.nrt;
-      const int8_t* ksrc = p.kc + (bg * p.C + j0) * p.H;
-      const int8_t* vsrc = p.vc + (bg * p.C + j0) * p.H;
-      const uint32_t kd = (uint32_t)__cvta_generic_to_shared(sm.ring[s]), vd = kd + kTileBytes;
-      if (chunks == HP / 16) {
+    if (ld.left > 0 && (p.withhold_tile < 0 || fetched != p.withhold_tile)) {
+      ++fetched;
+      const int j0 = (ld.t0 + ld.off) * kBlockUnit;
+      const int bg = ld.b * p.Nkv + ld.gr / p.nrt;
+      if (lane == 0) {
+        const int row = bg * p.C + j0;   // below 2^31 (checked by the host)
+        tc::mbar_arrive_tx(&ctl.full[s], 2 * kTileBytes);
 #pragma unroll
-        for (int i = 0; i < kBlockUnit * HP / 512; ++i) {
-          const int x = i * 32 + lane, r = x / (HP / 16), c = x % (HP / 16);
-          if (r < rows) {
-            cp16(kd + chunk_at<HP>(r, c), ksrc + r * HP + 16 * c);
-            cp16(vd + chunk_at<HP>(r, c), vsrc + r * HP + 16 * c);
-          }
-        }
-      } else {
-        for (int x = lane; x < rows * chunks; x += 32) {
-          const int r = x / chunks, c = x - r * chunks;
-          cp16(kd + chunk_at<HP>(r, c), ksrc + r * p.H + 16 * c);
-          cp16(vd + chunk_at<HP>(r, c), vsrc + r * p.H + 16 * c);
+        for (int x = 0; x < (HP > 128 ? 2 : 1); ++x) {
+          tc::tma_load_2d(sm.ring[s] + x * kBlockUnit * 128, &tmk, 128 * x, row, &ctl.full[s]);
+          tc::tma_load_2d(sm.ring[s] + kTileBytes + x * kBlockUnit * 128, &tmv, 128 * x, row, &ctl.full[s]);
         }
       }
       if (lane < 4) {   // scales of the two 16-key groups; 0 behind the last row
         const int j = j0 + 16 * (lane & 1);
-        const float* src = (lane < 2 ? p.ks : p.vs) + bg * p.nblk;
+        const float* src = (lane < 2 ? p.ks : p.vs) + (long long)bg * p.nblk;
         const bool on = j < ld.total;
-        cp4((uint32_t)__cvta_generic_to_shared(&sm.sc[s][lane]), src + (on ? j >> p.bs_log2 : 0), on);
+        cp4((uint32_t)__cvta_generic_to_shared(&ctl.sc[s][lane]), src + (on ? j >> p.bs_log2 : 0), on);
       }
       ld.next(p);
     }
@@ -333,168 +323,189 @@ block_attn_kernel(const BlockParams p) {
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) fetch(s);
 
-  uint32_t qf[HP > 128 ? 1 : kSteps][4];
-  float o[kNT][4];
-  float m[2], l[2], mul[2];     // rows gq and gq + 8 (fp32: row gq only)
-  int pos[2];
+  uint2 qf[NT * kParts][kSteps];
+  float o[kSteps][NT][4];       // O^T: coordinates gq HP/8 + 2 i (0, 1) and + 1 (2, 3), rows 2 t (0, 2) and + 1 (1, 3)
+  float m[NT][2], l[NT][2], mul[NT][2];   // of rows 8 n + 2 t, + 1
   int wexp = -200;              // the V scales enter as vs 2^-wexp
   bool fresh_piece = true;
   int stage = 0;
+  uint32_t parity = 0;
   while (cp.left > 0) {
     const int b = cp.b, g = cp.gr / p.nrt, rt = cp.gr % p.nrt;
-    const int j0 = (cp.t0 + cp.off) * kBlockUnit, total = cp.total, past = cp.total - cp.fresh;
+    const int j0 = (cp.t0 + cp.off) * kBlockUnit, past = cp.total - cp.fresh;
+    __syncwarp();                                  // the other stage has been read by every lane
+    fetch(stage ^ 1);
     if (fresh_piece) {
       fresh_piece = false;
-      const float f = load_queries<T, HP>(p, b, g, rt, qf, sm.q) * p.scale;
+      float up[NT];
+      load_queries<T, HP, NT>(p, b, g, rt, qf, up);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        mul[h] = p.softcap > 0.f ? f : f * kLog2e;
-        m[h] = kNegBig;
-        l[h] = 0.f;
-        pos[h] = past + (rt * p.rt_rows + gq + (kHalf ? 8 * h : 0)) / p.G;
-      }
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < kNT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        for (int h = 0; h < 2; ++h) {
+          const float f = __shfl_sync(0xffffffffu, up[n], 4 * (2 * t + h)) * p.scale;
+          mul[n][h] = p.softcap > 0.f ? f : f * kLog2e;
+          m[n][h] = kNegBig;
+          l[n][h] = 0.f;
+        }
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
       wexp = -200;
     }
-    cp_wait<kStages - 2>();
-    __syncwarp();
-    fetch(stage == 0 ? kStages - 1 : stage - 1);   // the stage read one unit ago
+    cp_wait<kStages - 1>();
+    if (!__all_sync(0xffffffffu, tc::mbar_wait(&ctl.full[stage], parity, p.wait_budget))) {
+      if (lane == 0 && p.status) atomicOr(p.status, GQA_DEVICE_TIMEOUT_BIT);
+      tc::mbar_wait(&ctl.full[stage ^ 1], stage == 0 ? parity : parity ^ 1u, p.wait_budget);   // a copy still landing
+      break;
+    }
     const uint8_t* kt = sm.ring[stage];
     const uint8_t* vt = kt + kTileBytes;
 
-    // ---- scores of 32 keys: s[n] holds rows gq (0, 1) and gq + 8 (2, 3), keys 8 n + 2 t, + 1
-    float s[4][4];
+    // ---- scores: s[kk][n] holds keys 16 kk + gq (0, 1) and + 8 (2, 3), rows 2 t (0, 2) and + 1 (1, 3)
+    float s[2][NT][4];
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-      const int r = 8 * n + gq;
-      uint32_t kw[kSteps];
+    for (int kk = 0; kk < 2; ++kk) {
+      uint32_t kw[2][kSteps];
 #pragma unroll
-      for (int i = 0; i < kSteps / 4; ++i) {
-        const uint4 v = *reinterpret_cast<const uint4*>(kt + chunk_at<HP>(r, t * (HP / 64) + i));
-        kw[4 * i] = v.x ^ 0x80808080u;
-        kw[4 * i + 1] = v.y ^ 0x80808080u;
-        kw[4 * i + 2] = v.z ^ 0x80808080u;
-        kw[4 * i + 3] = v.w ^ 0x80808080u;
-      }
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < kSteps / 4; ++i) {
+          const uint4 v = *reinterpret_cast<const uint4*>(kt + chunk_at<HP>(16 * kk + 8 * h + gq, t * (HP / 64) + i));
+          kw[h][4 * i] = v.x ^ 0x80808080u;
+          kw[h][4 * i + 1] = v.y ^ 0x80808080u;
+          kw[h][4 * i + 2] = v.z ^ 0x80808080u;
+          kw[h][4 * i + 3] = v.w ^ 0x80808080u;
+        }
+      float c[NT * kParts][4];
+#pragma unroll
+      for (int n = 0; n < NT * kParts; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < kSteps; ++ks) {
-        if constexpr (HP > 128) {
-          const uint4 a = sm.q[ks * 32 + lane];
-          const uint32_t av[4] = {a.x, a.y, a.z, a.w};
-          mma16816(s[n], av, codes_lo(kw[ks]), codes_hi(kw[ks]));
-        } else {
-          mma16816(s[n], qf[ks], codes_lo(kw[ks]), codes_hi(kw[ks]));
-        }
+        const uint32_t a[4] = {codes_lo(kw[0][ks]), codes_lo(kw[1][ks]), codes_hi(kw[0][ks]), codes_hi(kw[1][ks])};
+#pragma unroll
+        for (int n = 0; n < NT * kParts; ++n) mma16816(c[n], a, qf[n][ks].x, qf[n][ks].y);
       }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[kk][n][e] = kHalf ? c[n][e] : c[n][e] + c[NT * (kParts - 1) + n][e];
     }
-    const float ksc[2] = {sm.sc[stage][0], sm.sc[stage][1]};
-    const float vsc[2] = {sm.sc[stage][2], sm.sc[stage][3]};
-    // Log2-domain scores; hi and lo parts of an fp32 row are added.
-    const bool edge = j0 + kBlockUnit - 1 > past + (rt * p.rt_rows) / p.G ||
-                      (p.window >= 0 && j0 < past + (rt * p.rt_rows + p.rt_rows - 1) / p.G - p.window);
+    const float4 sc = *reinterpret_cast<const float4*>(ctl.sc[stage]);
+    const float ksc[2] = {sc.x, sc.y}, vsc[2] = {sc.z, sc.w};
+    // Log2-domain scores.
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      if (!kHalf) {
-        s[n][0] += s[n][2];
-        s[n][1] += s[n][3];
-      }
+    for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-      for (int e = 0; e < (kHalf ? 4 : 2); ++e) {
-        float x = s[n][e] * (mul[e >> 1] * ksc[n >> 1]);
-        if (p.softcap > 0.f) x = p.softcap * kLog2e * tanhf(x / p.softcap);
-        if (edge) {
-          const int j = j0 + 8 * n + 2 * t + (e & 1);
-          if (j > pos[e >> 1] || (p.window >= 0 && j < pos[e >> 1] - p.window)) x = -INFINITY;
+      for (int n = 0; n < NT; ++n) {
+        const float f[2] = {mul[n][0] * ksc[kk], mul[n][1] * ksc[kk]};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[kk][n][e] *= f[e & 1];
+          if (!PLAIN && p.softcap > 0.f) s[kk][n][e] = p.softcap * kLog2e * tanhf(s[kk][n][e] / p.softcap);
         }
-        s[n][e] = x;
       }
+    const int r0 = rt * p.rt_rows;
+    if (j0 + kBlockUnit - 1 > past + r0 / p.G ||
+        (p.window >= 0 && j0 < past + (r0 + 8 * NT - 1) / p.G - p.window)) {   // a mask border crosses the unit
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int pos = past + (r0 + 8 * n + 2 * t + h) / p.G;
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int j = j0 + 16 * kk + 8 * x + gq;
+              if (j > pos || (p.window >= 0 && j < pos - p.window)) s[kk][n][2 * x + h] = -INFINITY;
+            }
+        }
     }
-    if (p.stash) {
+    if (!PLAIN && p.stash) {
+      float* dst = p.stash + (((long long)b * p.Nkv + g) * p.stash_ld + j0 + gq) * p.stash_rows + 2 * t;
 #pragma unroll
-      for (int h = 0; h < (kHalf ? 2 : 1); ++h) {
-        const int r = gq + 8 * h;
-        if (r < p.S * p.G) {
-          float* dst = p.stash + (((long long)b * p.Nkv + g) * p.S * p.G + r) * p.stash_ld + j0 + 2 * t;
+      for (int n = 0; n < NT; ++n)
+        if (8 * n + 2 * t < p.stash_rows) {
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
-            *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(s[n][2 * h], s[n][2 * h + 1]);
+          for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              *reinterpret_cast<float2*>(dst + (16 * kk + 8 * x) * p.stash_rows + 8 * n) =
+                  make_float2(s[kk][n][2 * x], s[kk][n][2 * x + 1]);
         }
-      }
     }
     // ---- running maximum; O is rescaled only when one grows by more than 2^4
     // or the V scales outgrow their reference.
-    float mx[2];
+    float mx[NT][2];
+    bool grow = false;
 #pragma unroll
-    for (int h = 0; h < (kHalf ? 2 : 1); ++h) {
-      mx[h] = fmaxf(fmax3(s[0][2 * h], s[0][2 * h + 1], s[1][2 * h]), fmax3(s[1][2 * h + 1], s[2][2 * h], s[2][2 * h + 1]));
-      mx[h] = fmax3(mx[h], s[3][2 * h], s[3][2 * h + 1]);
-      mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-      mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-    }
-    const bool grow0 = mx[0] > m[0] + kGrow, grow1 = kHalf && mx[kHalf ? 1 : 0] > m[1] + kGrow;
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x = fmaxf(fmax3(s[0][n][h], s[0][n][2 + h], s[1][n][h]), s[1][n][2 + h]);
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        mx[n][h] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        grow |= mx[n][h] > m[n][h] + kGrow;
+      }
     // P enters the MMA as p vs 2^-wexp, at most 2^14: vs 2^-wexp in [2^9, 2^10)
     // for the block that set it, and fp16 keeps its 11 bits down to 2^-14.
     const int vexp = (__float_as_int(fmaxf(vsc[0], vsc[1])) >> 23) - 127 - 9;
-    if (__any_sync(0xffffffffu, grow0 || grow1) || vexp > wexp) {
+    if (__any_sync(0xffffffffu, grow) || vexp > wexp) {
       const int dw = vexp > wexp ? max(wexp - vexp, -126) : 0;
       if (vexp > wexp) wexp = max(vexp, -110);
       const float fw = __int_as_float((127 + dw) << 23);
-      float f[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool grow = h == 0 ? grow0 : grow1;
-        const float mn = grow ? mx[kHalf ? h : 0] : m[h];
-        const float e = grow ? ex2(m[h] - mn) : 1.f;
-        m[h] = mn;
-        l[h] *= e;
-        f[h] = e * fw;
-      }
-      if (!kHalf) f[1] = f[0];
+      for (int n = 0; n < NT; ++n) {
+        float f[2];
 #pragma unroll
-      for (int i = 0; i < kNT; ++i) {
-        o[i][0] *= f[0];
-        o[i][1] *= f[0];
-        o[i][2] *= f[1];
-        o[i][3] *= f[1];
-      }
-    }
-    const float down = __int_as_float((127 - wexp < 1 ? 1 : 127 - wexp > 254 ? 254 : 127 - wexp) << 23);
-    const float vm[2] = {vsc[0] * down, vsc[1] * down};
-    // ---- P, and O += P V, 16 keys per step
+        for (int h = 0; h < 2; ++h) {
+          const float mn = mx[n][h] > m[n][h] + kGrow ? mx[n][h] : m[n][h];
+          const float e = ex2(m[n][h] - mn);
+          m[n][h] = mn;
+          l[n][h] *= e;
+          f[h] = e * fw;
+        }
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      uint32_t a[4];
-      if constexpr (kHalf) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float p0 = ex2(s[2 * kk + u][2 * h] - m[h]), p1 = ex2(s[2 * kk + u][2 * h + 1] - m[h]);
-            l[h] += p0 + p1;
-            a[2 * u + h] = pack(p0 * vm[kk], p1 * vm[kk]);
-          }
-      } else {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float p0 = ex2(s[2 * kk + u][0] - m[0]), p1 = ex2(s[2 * kk + u][1] - m[0]);
-          l[0] += p0 + p1;
-          const float x0 = p0 * vm[kk], x1 = p1 * vm[kk];
-          a[2 * u] = pack(x0, x1);
-          const float2 hi = unpack(a[2 * u]);
-          a[2 * u + 1] = pack(x0 - hi.x, x1 - hi.y);
+        for (int i = 0; i < kSteps; ++i) {
+          o[i][n][0] *= f[0];
+          o[i][n][1] *= f[1];
+          o[i][n][2] *= f[0];
+          o[i][n][3] *= f[1];
         }
       }
-      // Keys 16 kk + 2 t, + 1, + 8, + 9; output tile i, column n = gq: coordinate gq HP/8 + i.
-      const int k0 = 16 * kk + 2 * t;
+    }
+    const float down = __int_as_float((127 - wexp) << 23);   // wexp is in [-110, 119] here
+    // ---- P, and O^T += V^T P^T, 16 keys per step
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const float vm = vsc[kk] * down;
+      uint32_t pb[NT * kParts][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float p0 = ex2(s[kk][n][2 * x] - m[n][0]), p1 = ex2(s[kk][n][2 * x + 1] - m[n][1]);
+          l[n][0] += p0;
+          l[n][1] += p1;
+          const float x0 = p0 * vm, x1 = p1 * vm;
+          const uint32_t hi = pack(x0, x1);
+          pb[n][x] = transpose8(hi);
+          if constexpr (!kHalf) {
+            const float2 h2 = unpack(hi);
+            pb[NT + n][x] = transpose8(pack(x0 - h2.x, x1 - h2.y));
+          }
+        }
+      // Keys 16 kk + 2 t, + 1, + 8, + 9 of thread t; coordinates gq HP/8 .. of quad gq.
       constexpr int kWords = HP / 32 < 4 ? HP / 32 : 4;   // 4-coordinate words per pass
 #pragma unroll
       for (int hf = 0; hf < HP / 32 / kWords; ++hf) {
         uint32_t w[4][kWords];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int r = k0 + (x & 1) + 8 * (x >> 1);
+          const int r = 16 * kk + 2 * t + (x & 1) + 8 * (x >> 1);
           const int byte = gq * (HP / 8) + 16 * hf;
           const uint8_t* src = vt + chunk_at<HP>(r, byte >> 4) + (byte & 15);
           if constexpr (kWords == 4) {
@@ -513,15 +524,19 @@ block_attn_kernel(const BlockParams p) {
         for (int y = 0; y < kWords; ++y) {
           const uint32_t alo = __byte_perm(w[0][y], w[1][y], 0x5140u), ahi = __byte_perm(w[0][y], w[1][y], 0x7362u);
           const uint32_t blo = __byte_perm(w[2][y], w[3][y], 0x5140u), bhi = __byte_perm(w[2][y], w[3][y], 0x7362u);
-          const int i = 16 * hf + 4 * y;
-          mma16816(o[i], a, codes_lo(alo), codes_lo(blo));
-          mma16816(o[i + 1], a, codes_hi(alo), codes_hi(blo));
-          mma16816(o[i + 2], a, codes_lo(ahi), codes_lo(bhi));
-          mma16816(o[i + 3], a, codes_hi(ahi), codes_hi(bhi));
+          const uint32_t a0[4] = {codes_lo(alo), codes_hi(alo), codes_lo(blo), codes_hi(blo)};
+          const uint32_t a1[4] = {codes_lo(ahi), codes_hi(ahi), codes_lo(bhi), codes_hi(bhi)};
+          const int i = 8 * hf + 2 * y;
+#pragma unroll
+          for (int n = 0; n < NT * kParts; ++n) {
+            mma16816(o[i][n % NT], a0, pb[n][0], pb[n][1]);
+            mma16816(o[i + 1][n % NT], a1, pb[n][0], pb[n][1]);
+          }
         }
       }
     }
-    stage = stage + 1 == kStages ? 0 : stage + 1;
+    stage ^= 1;
+    if (stage == 0) parity ^= 1;
     const int range = cp.b * p.Nkv * p.nrt + cp.gr;
     cp.next(p);
     if (cp.left > 0 && cp.b * p.Nkv * p.nrt + cp.gr == range) continue;
@@ -529,34 +544,27 @@ block_attn_kernel(const BlockParams p) {
     // ---- the piece ends: (m, l) and O of its rows into slot worker + range
     fresh_piece = true;
     const long long slot = worker + range;
-    const float upw = __int_as_float((127 + max(wexp, -126)) << 23);   // O in units of 2^wexp (no V scale seen: O is 0)
+    const float upw = __int_as_float((127 + wexp) << 23);   // O is in units of 2^wexp
 #pragma unroll
-    for (int h = 0; h < (kHalf ? 2 : 1); ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      const int row = gq + 8 * h;
-      if (rt * p.rt_rows + row < p.S * p.G) {
-        if (t == 0)
-          *reinterpret_cast<float2*>(p.part_ml + (slot * p.rt_rows + row) * 2) = make_float2(m[h], l[h]);
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float sum = l[n][h];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int row = 8 * n + 2 * t + h;
+        if (r0 + row >= p.S * p.G) continue;
+        if (gq == 0) *reinterpret_cast<float2*>(p.part_ml + (slot * p.rt_rows + row) * 2) = make_float2(m[n][h], sum);
         float* dst = p.part_o + (slot * p.rt_rows + row) * p.H;
 #pragma unroll
-        for (int col = 0; col < 2; ++col)
-#pragma unroll
-          for (int i = 0; i < kNT; i += 4) {
-            const int d = (2 * t + col) * (HP / 8) + i;
-            if (d >= p.H) continue;
-            float4 v;
-            if constexpr (kHalf) {
-              v = make_float4(o[i][2 * h + col] * upw, o[i + 1][2 * h + col] * upw, o[i + 2][2 * h + col] * upw,
-                              o[i + 3][2 * h + col] * upw);
-            } else {
-              v = make_float4((o[i][col] + o[i][2 + col]) * upw, (o[i + 1][col] + o[i + 1][2 + col]) * upw,
-                              (o[i + 2][col] + o[i + 2][2 + col]) * upw, (o[i + 3][col] + o[i + 3][2 + col]) * upw);
-            }
-            *reinterpret_cast<float4*>(dst + d) = v;
-          }
+        for (int i = 0; i < kSteps; i += 2) {
+          const int d = gq * (HP / 8) + 2 * i;
+          if (d < p.H)
+            *reinterpret_cast<float4*>(dst + d) = make_float4(o[i][n][h] * upw, o[i][n][2 + h] * upw,
+                                                              o[i + 1][n][h] * upw, o[i + 1][n][2 + h] * upw);
+        }
       }
-    }
   }
   cp_wait<0>();
 }
@@ -720,7 +728,7 @@ block_merge_kernel(const BlockParams p, long long row_blocks, int weight_chunks)
     float w = 0.f;
     if (j >= t0 * kBlockUnit)
       for (int r = 0; r < nrows; ++r)
-        w += ex2(p.stash[((long long)bg * p.S * p.G + r) * p.stash_ld + j] - lse[r]);
+        w += ex2(p.stash[((long long)bg * p.stash_ld + j) * p.stash_rows + r] - lse[r]);
     if (p.past_w && j < total - fresh) w += p.past_w[at];
     p.present_w[at] = w;
   }
@@ -883,14 +891,32 @@ cudaError_t allow_smem(K kern, int bytes, bool* done) {
   return cudaSuccess;
 }
 
-template <typename T, int HP>
+template <typename T, int HP, int NT, bool PLAIN>
 cudaError_t attn_one(const BlockParams& p, cudaStream_t st) {
   static bool done[kMaxDevices];
-  const int smem = kWarps * (int)sizeof(WarpSmem<T, HP>);
-  cudaError_t e = allow_smem(block_attn_kernel<T, HP>, smem, done);
+  const int smem = kWarps * (int)sizeof(WarpSmem<HP>) + 1024;
+  cudaError_t e = allow_smem(block_attn_kernel<T, HP, NT, PLAIN>, smem, done);
   if (e != cudaSuccess) return e;
-  block_attn_kernel<T, HP><<<(unsigned)(p.workers / kWarps), kWarps * 32, smem, st>>>(p);
+  CUtensorMap mk, mv;
+  const uint64_t rows = (uint64_t)p.B * p.Nkv * p.C;
+  if ((e = encode_codes(&mk, p.kc, rows, p.H, HP, kBlockUnit)) != cudaSuccess) return e;
+  if ((e = encode_codes(&mv, p.vc, rows, p.H, HP, kBlockUnit)) != cudaSuccess) return e;
+  block_attn_kernel<T, HP, NT, PLAIN><<<(unsigned)(p.workers / kWarps), kWarps * 32, smem, st>>>(p, mk, mv);
   return cudaGetLastError();
+}
+
+template <typename T, int HP, int NT>
+cudaError_t attn_nt(const BlockParams& p, cudaStream_t st) {
+  return p.softcap > 0.f || p.stash ? attn_one<T, HP, NT, false>(p, st) : attn_one<T, HP, NT, true>(p, st);
+}
+
+template <int HP>
+cudaError_t attn_hp(const BlockParams& p, cudaStream_t st) {
+  if (p.t_type == kF32) return attn_nt<float, HP, 1>(p, st);
+  if constexpr (HP <= 128) {
+    if (p.rt_rows == 16) return attn_nt<__half, HP, 2>(p, st);
+  }
+  return attn_nt<__half, HP, 1>(p, st);
 }
 
 template <typename T, int HP>
@@ -905,12 +931,15 @@ cudaError_t weights_one(const BlockParams& p, cudaStream_t st) {
 
 }  // namespace
 
-int block_row_tile(int t_type) { return t_type == kF16 ? 16 : 8; }
+// fp32 rows come as two fp16 parts: a tile of 8 rows is two MMA tiles. Up to 8
+// fp16 rows take one, more take tiles of 16 (the codes are converted half as
+// often), but for head sizes above 128, whose output tiles fill the registers.
+int block_row_tile(int t_type, int H, long long rows) { return t_type == kF16 && H <= 128 && rows > 8 ? 16 : 8; }
 
-// One worker per warp, two CTAs of four per SM (one for head sizes above 128);
-// fewer when there are not four units for each.
+// One worker per warp, as many CTAs of four as an SM holds; fewer when there
+// are not four units for each.
 int block_workers(const BlockParams& p) {
-  const long long most = 152LL * kWarps * (p.H > 128 ? 1 : 2);
+  const long long most = 152LL * kWarps * (p.H > 128 ? 1 : p.rt_rows > 8 ? 2 : 3);
   const int keys = p.window >= 0 && (long long)p.window + p.S < p.T ? p.window + p.S + kBlockUnit : p.T;
   const long long units =
       (long long)p.B * p.Nkv * p.nrt * ((keys + kBlockUnit - 1) / kBlockUnit + kBlockRangeCost);
@@ -920,9 +949,7 @@ int block_workers(const BlockParams& p) {
 }
 
 cudaError_t launch_block_attn(const BlockParams& p, cudaStream_t st) {
-  if (p.t_type == kF16)
-    return p.H <= 64 ? attn_one<__half, 64>(p, st) : p.H <= 128 ? attn_one<__half, 128>(p, st) : attn_one<__half, 256>(p, st);
-  return p.H <= 64 ? attn_one<float, 64>(p, st) : p.H <= 128 ? attn_one<float, 128>(p, st) : attn_one<float, 256>(p, st);
+  return p.H <= 64 ? attn_hp<64>(p, st) : p.H <= 128 ? attn_hp<128>(p, st) : attn_hp<256>(p, st);
 }
 
 cudaError_t launch_block_merge(const BlockParams& p, cudaStream_t st) {

@@ -48,8 +48,8 @@ struct BlockParams {
   int rt_rows, nrt;      // rows of a row tile, row tiles of a (b, g)
   int workers;           // warps of the grid
   float *part_o, *part_ml;
-  float* stash;          // log2-domain scores [B*Nkv][S*G][stash_ld] (one row tile), or null
-  int stash_ld;
+  float* stash;          // log2-domain scores [B*Nkv][stash_ld keys][stash_rows] (one row tile), or null
+  int stash_ld, stash_rows;
   float* lse;            // log2-domain log-sum-exp [B*Nkv][S*G], or null
   // tensor-core prefill
   long long wait_budget;
@@ -67,7 +67,7 @@ cudaError_t launch_block_append(const BlockParams& p, cudaStream_t st);
 // Split-KV attention on warp MMAs, every shape.
 constexpr int kBlockUnit = 32;      // keys per work unit
 constexpr int kBlockRangeCost = 2;  // work units a range's start and end are counted as
-int block_row_tile(int t_type);     // query rows per row tile
+int block_row_tile(int t_type, int H, long long rows);   // query rows per row tile, of `rows` of a (b, g)
 int block_workers(const BlockParams& p);
 cudaError_t launch_block_attn(const BlockParams& p, cudaStream_t st);
 cudaError_t launch_block_merge(const BlockParams& p, cudaStream_t st);

@@ -40,6 +40,13 @@ cudaError_t encode_u8_2d(CUtensorMap* map, const void* base, uint64_t rows, uint
 cudaError_t encode_u8_2d_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                                uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows);
 
+// 2D map of a row-major [rows][cols] byte matrix (cols a multiple of 16) for
+// tiles of box_rows rows padded to `padded` = 64, 128 or 256 columns: boxes of
+// 64 bytes with the 64-byte swizzle, else of 128 bytes with the 128-byte one
+// (two boxes for 256). Columns and rows past the matrix read as zero.
+cudaError_t encode_codes(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, int padded,
+                         uint32_t box_rows);
+
 // 2D map of a row-major [rows][cols] fp32 matrix without swizzle: boxes of
 // box_cols (<= 256) x box_rows elements land as box_rows rows of box_cols
 // consecutive floats; elements past the matrix are read as zero.

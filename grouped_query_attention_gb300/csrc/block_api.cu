@@ -122,6 +122,7 @@ gqa_status check_block_cache(const gqa_block_cache& c, const char* name, long lo
 
 struct BlockPlan {
   BlockParams P;
+  bool prefill;                                // tensor-core prefill instead of the split over the keys
   size_t part_o, part_ml, stash, lse, total;   // bytes of each section
 };
 
@@ -207,15 +208,22 @@ gqa_status plan_block(const gqa_handle* h, const gqa_block_cache* cache, const g
   P.withhold_tile = h->withhold_tile;
 
   const long long rows = S * G;
-  P.rt_rows = gqa::block_row_tile(P.t_type, (int)H, rows);
-  P.nrt = (int)((rows + P.rt_rows - 1) / P.rt_rows);
-  P.workers = gqa::block_workers(P);
-  const size_t slots = (size_t)P.workers + (size_t)(B * Nkv) * P.nrt;
-  pl->part_o = align_up(slots * P.rt_rows * H * sizeof(float));
-  pl->part_ml = align_up(slots * P.rt_rows * 2 * sizeof(float));
-  pl->stash = pl->lse = 0;
+  pl->prefill = H == 128 && 128 % G == 0 && rows > 16;
+  pl->part_o = pl->part_ml = pl->stash = pl->lse = 0;
+  if (pl->prefill) {
+    const long long nqb = (rows + 255) / 256;
+    if (nqb > 65535) return fail(GQA_ERR_UNSUPPORTED, "query too large");
+    P.qb_major = 2 * S >= T;   // key ranges differ by query block more than by sequence
+  } else {
+    P.rt_rows = gqa::block_row_tile(P.t_type, (int)H, rows);
+    P.nrt = (int)((rows + P.rt_rows - 1) / P.rt_rows);
+    P.workers = gqa::block_workers(P);
+    const size_t slots = (size_t)P.workers + (size_t)(B * Nkv) * P.nrt;
+    pl->part_o = align_up(slots * P.rt_rows * H * sizeof(float));
+    pl->part_ml = align_up(slots * P.rt_rows * 2 * sizeof(float));
+  }
   if (P.present_w) {
-    if (P.nrt == 1) {
+    if (!pl->prefill && P.nrt == 1) {
       P.stash_ld = (int)((T + gqa::kBlockUnit - 1) / gqa::kBlockUnit * gqa::kBlockUnit);
       P.stash_rows = (int)((rows + 1) & ~1LL);
       pl->stash = align_up((size_t)(B * Nkv) * P.stash_ld * P.stash_rows * sizeof(float));
@@ -359,10 +367,15 @@ gqa_status gqa_block_forward(gqa_handle* h, const gqa_block_cache* cache, const 
     e = timed_launch(h, GQA_KERNEL_BLOCK_APPEND, st, [&] { return gqa::launch_block_append(P, st); });
     if (e != cudaSuccess) return cuda_fail(e, "append launch");
   }
-  e = timed_launch(h, GQA_KERNEL_BLOCK_ATTENTION, st, [&] { return gqa::launch_block_attn(P, st); });
-  if (e != cudaSuccess) return cuda_fail(e, "attention launch");
-  e = timed_launch(h, GQA_KERNEL_BLOCK_MERGE, st, [&] { return gqa::launch_block_merge(P, st); });
-  if (e != cudaSuccess) return cuda_fail(e, "merge launch");
+  if (pl.prefill) {
+    e = timed_launch(h, GQA_KERNEL_BLOCK_PREFILL, st, [&] { return gqa::launch_block_prefill(P, st); });
+    if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
+  } else {
+    e = timed_launch(h, GQA_KERNEL_BLOCK_ATTENTION, st, [&] { return gqa::launch_block_attn(P, st); });
+    if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+    e = timed_launch(h, GQA_KERNEL_BLOCK_MERGE, st, [&] { return gqa::launch_block_merge(P, st); });
+    if (e != cudaSuccess) return cuda_fail(e, "merge launch");
+  }
   if (P.lse) {
     e = timed_launch(h, GQA_KERNEL_BLOCK_WEIGHTS, st, [&] { return gqa::launch_block_weights(P, st); });
     if (e != cudaSuccess) return cuda_fail(e, "weights launch");

@@ -52,6 +52,7 @@ struct BlockParams {
   int stash_ld, stash_rows;
   float* lse;            // log2-domain log-sum-exp [B*Nkv][S*G], or null
   // tensor-core prefill
+  int qb_major;          // grid with the query block on the slow axis
   long long wait_budget;
   int withhold_tile;
 };
@@ -71,6 +72,8 @@ int block_row_tile(int t_type, int H, long long rows);   // query rows per row t
 int block_workers(const BlockParams& p);
 cudaError_t launch_block_attn(const BlockParams& p, cudaStream_t st);
 cudaError_t launch_block_merge(const BlockParams& p, cudaStream_t st);
+// Tensor-core prefill: head size 128, group size dividing 128.
+cudaError_t launch_block_prefill(const BlockParams& p, cudaStream_t st);
 // Attention weights of the cache rows from the log-sum-exp of every query row.
 cudaError_t launch_block_weights(const BlockParams& p, cudaStream_t st);
 

@@ -13,11 +13,17 @@
 // and its 11 bits down to v' p = 2^-20. fp32 queries and P are split into two
 // fp16 parts as in the prefill over per-channel caches: twice the MMAs.
 //
-// Warps: 0 TMA of the query tiles; 1 MMA issue, tensor memory; 2..9 softmax,
-// one thread per row, epilogue; 10..13 converters: codes of the next K or V
-// tile from global memory into registers while the current one is converted.
-// S0 | S1 | O0 | O1 in tensor memory; the order of the MMAs is the other
-// prefills'. Every barrier wait is bounded.
+// Warps: 0 TMA of the query tiles, then of the code tiles into a two-tile
+// ring; 1 MMA issue, tensor memory; 2 the scales of a tile, two tiles ahead;
+// 4..11 softmax, one thread per row, epilogue; 12..15 converters: code tile to
+// fp16 operand tile (3 idle: register shares go by warpgroup). Converters that
+// loaded the next codes themselves waited for them at every proxy fence:
+// 2400 cycles a tile pair, which set the pace (4700 against 2400 of MMAs).
+// Steps of 64 keys: S of a step is 64 tensor-memory columns, so each query
+// tile has two S buffers beside its O (2 x (2 x 64 + 128) = 512 columns) and
+// S of the step after next is issued behind P.V of this one: a softmax never
+// waits for its own P.V. With S over 128 keys (one buffer) it did: 1800 of
+// 3700 cycles per 128 keys. Every barrier wait is bounded.
 #include <cuda_fp16.h>
 
 #include "block_internal.h"
@@ -34,8 +40,13 @@ constexpr int kBM = 128;                       // rows per query tile
 constexpr int kBN = 128;                       // keys per K/V tile
 constexpr int kHD = 128;                       // head size
 constexpr int kGroups = kBN / 16;              // 16-key groups of a tile, one scale each
-constexpr int kThreads = 448;
-constexpr int kConvWarp0 = 10;
+constexpr int kThreads = 512;
+constexpr int kSoftWarp0 = 4;
+constexpr int kConvWarp0 = 12;
+// Registers per thread of each warpgroup after the split (launched with 128):
+// TMA + MMA, two softmax groups, converters; the sum is what was launched.
+constexpr int kRegsIssue = 80, kRegsSoft = 176, kRegsConv = 80;
+static_assert(kRegsIssue + 2 * kRegsSoft + kRegsConv == 4 * 128, "register split");
 constexpr int kConvWarps = 4;
 constexpr int kConvRows = kBN / kConvWarps;
 constexpr int kScStages = 4;                   // scale slots: a tile's are read until both its softmaxes end
@@ -43,24 +54,28 @@ constexpr uint32_t kBox = 128u * 128u;         // 128 rows x 128 bytes
 constexpr uint32_t kTile = 2u * kBox;          // fp16 operand tile
 constexpr float kLazy = 8.0f;                  // log2 growth tolerated before rescaling O
 constexpr float kLift = 6.0f;
-constexpr uint32_t kIdS = idesc_f16(128, 128, 0, 0);
+constexpr int kStep = 64;                      // keys per step
+constexpr uint32_t kIdS = idesc_f16(128, kStep, 0, 0);
 constexpr uint32_t kIdO = idesc_f16(128, 128, 0, 1);
 
-// F32: hi and lo query tiles (the raw fp32 tile before), one V buffer; fp16: one tile, two V buffers.
+// F32: hi and lo query tiles (the raw fp32 tile before) and one operand tile each of K and V; fp16: two each.
 template <bool F32>
 struct __align__(1024) PfSmem {
   static constexpr uint32_t kQ = F32 ? 4 * kBox : 2 * kBox;
-  static constexpr int kVB = F32 ? 1 : 2;
+  static constexpr int kNB = F32 ? 1 : 2;
   uint8_t q[2][kQ];
-  uint8_t kf[2][kTile];
-  uint8_t vf[kVB][kTile];
+  uint8_t kf[kNB][kTile];
+  uint8_t vf[kNB][kTile];
+  uint8_t raw[2][kBox];          // code tiles as copied
   float rho[2][kBM];             // fp32 rows: 2^e
   float ks[kScStages][kGroups];  // K scales
   float lv[kScStages][kGroups];  // kLift + log2 v'
   float iv[kScStages][kGroups];  // 2^-kLift / v'
+  uint64_t sc_full[kScStages], sc_empty[kScStages];
+  uint64_t raw_full[2], raw_empty[2];
   uint64_t q_land[2], q_ready[2];
   uint64_t kf_full[2], kf_empty[2], vf_full[2], vf_empty[2];
-  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t s_full[2][2], p_full[2][2], o_done[2];   // [query tile][buffer]
   uint64_t drain;
   uint32_t tmem;
   unsigned vmax;                 // bits of the largest V scale
@@ -93,6 +108,11 @@ __device__ __forceinline__ void codes16(uint4 w, uint32_t* h) {
   }
 }
 
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // All bits of `v` over the 128 threads of softmax group q (named barrier 1 + q).
 __device__ __forceinline__ bool group_all(bool v, int q) {
   uint32_t r;
@@ -103,20 +123,38 @@ __device__ __forceinline__ bool group_all(bool v, int q) {
   return r != 0;
 }
 
-// c tanh(u) log2(e) on |u| <= 5/8 as u Q(u^2), Q the degree-5 least-squares fit
-// of tanh(u) / u in u^2 (relative error 5e-8 in fp32 Horner); a warp's half
-// with a larger |u| takes c (1 - 2 / (e^2u + 1)) for those values, whose own
-// size keeps the cancellation harmless. As packed pairs: 8 instructions for
-// two scores against four special-function ones.
-constexpr float kCapZ = 0.625f * 0.625f;
-__device__ __forceinline__ float2 cap_poly(float2 u, float2 z, const float* q) {
-  float2 y = make_float2(q[5], q[5]);
+// Softcap in the log2 domain, c2 tanh(u), c2 = softcap log2(e), as u Q(u^2)
+// with Q the least-squares fit of tanh(u) / u in u^2: degree 3 on |u| <= 0.35,
+// degree 7 on |u| <= 1 (relative error 9e-8 each in fp32 Horner). Beyond,
+// c2 (1 - 2 / (e^2u + 1)), whose cancellation the value's own size keeps
+// harmless. A pair of scores costs 6 or 10 packed instructions on the FMA pipe.
+constexpr float kCapLow = 0.35f, kCapHigh = 1.0f;
+__device__ constexpr float kFit3[4] = {0.9999999403953552f, -0.3333241641521454f, 0.13295666873455048f, -0.04895104840397835f};
+__device__ constexpr float kFit7[8] = {1.0f, -0.33333274722099304f, 0.13332107663154602f, -0.05386783555150032f,
+                                       0.021456174552440643f, -0.00790493842214346f, 0.0022732384968549013f,
+                                       -0.0003508012741804123f};
+template <int DEG>
+__device__ __forceinline__ float2 cap_fit(float2 z) {
+  constexpr const float* q = DEG == 3 ? kFit3 : kFit7;
+  float2 y = make_float2(q[DEG], q[DEG]);
 #pragma unroll
-  for (int i = 4; i >= 0; --i) y = ffma2(y, z, make_float2(q[i], q[i]));
-  return ffma2(u, y, make_float2(0.f, 0.f));
+  for (int i = DEG - 1; i >= 0; --i) y = ffma2(y, z, make_float2(q[i], q[i]));
+  return y;
 }
-__device__ __forceinline__ float cap_exp(float u, float c2) {
-  return fmaf(__frcp_rn(ex2(u * (2.f * kLog2e)) + 1.f), -2.f * c2, c2);
+__device__ __forceinline__ float cap_far(float u, float c2) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(u * (2.f * kLog2e)) + 1.f));
+  return fmaf(r, -2.f * c2, c2);
+}
+// Both forms computed, one selected (no branch).
+__device__ __forceinline__ float2 cap_any(float2 u, float c2) {
+  const float2 z = ffma2(u, u, make_float2(0.f, 0.f));
+  const float2 y = ffma2(u, cap_fit<7>(z), make_float2(0.f, 0.f));
+  const float fx = cap_far(u.x, c2), fy = cap_far(u.y, c2);
+  float2 r;
+  asm("{ .reg .pred p; setp.le.f32 p, %1, %2; selp.f32 %0, %3, %4, p; }" : "=f"(r.x) : "f"(z.x), "f"(kCapHigh), "f"(y.x * c2), "f"(fx));
+  asm("{ .reg .pred p; setp.le.f32 p, %1, %2; selp.f32 %0, %3, %4, p; }" : "=f"(r.y) : "f"(z.y), "f"(kCapHigh), "f"(y.y * c2), "f"(fy));
+  return r;
 }
 
 // fp32 query tiles, in place, by the 256 softmax threads (wt = 0 .. 255), 8
@@ -178,10 +216,11 @@ __device__ void split_rows(const BlockParams& p, PfSmem<true>& sm, int wt) {
 template <bool F32, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
 block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmq,
-                     const __grid_constant__ CUtensorMap tmo) {
+                     const __grid_constant__ CUtensorMap tmo, const __grid_constant__ CUtensorMap tmk,
+                     const __grid_constant__ CUtensorMap tmv) {
   using SM = PfSmem<F32>;
   using T = typename std::conditional<F32, float, __half>::type;
-  constexpr int kVB = SM::kVB;
+  constexpr int kNB = SM::kNB;
   constexpr int kBoxes = F32 ? 4 : 2, kBoxDims = kHD / kBoxes;
   extern __shared__ uint8_t smem_raw[];
   SM& sm = *reinterpret_cast<SM*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -212,20 +251,29 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
   }
   const int kmax = past + i_hi + 1;
   const int kmin = p.window >= 0 ? max(0, past + i_lo - p.window) & ~15 : 0;   // scales change at multiples of 16
-  const int ntiles = (kmax - kmin + kBN - 1) / kBN;
+  const int nsteps = (kmax - kmin + kStep - 1) / kStep;
+  const int ntiles = (nsteps + 1) / 2;
 
   if (warp == 1) tmem_alloc(&sm.tmem, 512);
   if (tid == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sm.q_land[t], 1);
       mbar_init(&sm.q_ready[t], 8);
-      mbar_init(&sm.s_full[t], 1);
-      mbar_init(&sm.p_full[t], kBM);
+      for (int u = 0; u < 2; ++u) {
+        mbar_init(&sm.s_full[t][u], 1);
+        mbar_init(&sm.p_full[t][u], 4);   // warps of a softmax group
+      }
       mbar_init(&sm.o_done[t], 1);
       mbar_init(&sm.kf_full[t], kConvWarps);
       mbar_init(&sm.kf_empty[t], 1);
       mbar_init(&sm.vf_full[t], kConvWarps);
       mbar_init(&sm.vf_empty[t], 1);
+      mbar_init(&sm.raw_full[t], 1);
+      mbar_init(&sm.raw_empty[t], kConvWarps);
+    }
+    for (int t = 0; t < kScStages; ++t) {
+      mbar_init(&sm.sc_full[t], 1);
+      mbar_init(&sm.sc_empty[t], 8);   // softmax warps
     }
     mbar_init(&sm.drain, 1);
     sm.abort = 0;
@@ -254,100 +302,149 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
   __syncthreads();
   const uint32_t tmem = sm.tmem;
   const int wexp = min(max((int)(sm.vmax >> 23) - 126, -100), 120);
-  const long long krow0 = (long long)bg * p.C + kmin;
+  const int krow0 = bg * p.C + kmin;   // below 2^31 (checked by the host)
+  // Order of the code tiles: K(0), then K(t+1) (operand tile free once
+  // S_1(t+1 - kNB) is done) and V(t).
+  const int nconv = 2 * ntiles;
+  auto item = [&](int n, bool& is_k) -> int {
+    if (n == 0) {
+      is_k = true;
+      return 0;
+    }
+    const int t = (n - 1) >> 1;
+    // With one operand tile of each kind V(t) goes first: K(t+1) has to wait for S_1(t).
+    const bool first = ((n - 1) & 1) == 0;
+    is_k = (kNB == 1 ? !first : first) && t + 1 < ntiles;
+    return is_k ? t + 1 : t;
+  };
 
+  if (warp < kSoftWarp0) {
+  regs_down<kRegsIssue>();
   if (warp == 0) {
+    // ================================================================ TMA of the code tiles
+    bool ok = true;
+    int n = 0;
+    for (; n < nconv && ok; ++n) {
+      bool is_k;
+      const int u = item(n, is_k);
+      if (u == p.withhold_tile) break;   // testing: this tile is never copied, the waits for it expire
+      ok = __all_sync(0xffffffffu, mbar_wait(&sm.raw_empty[n & 1], ((uint32_t)(n >> 1) & 1u) ^ 1u, p.wait_budget) && !aborted(sm));
+      if (ok && elect_one()) {
+        mbar_arrive_tx(&sm.raw_full[n & 1], kBox);
+        tma_load_2d(sm.raw[n & 1], is_k ? &tmk : &tmv, 0, krow0 + u * kBN, &sm.raw_full[n & 1]);
+      }
+      __syncwarp();
+    }
+    if (!ok && lane == 0) set_abort(p, sm);
+    if (!ok) --n;
     // No copy of this CTA may still be landing when it exits.
     mbar_wait(&sm.q_land[0], 0, p.wait_budget);
     mbar_wait(&sm.q_land[1], 0, p.wait_budget);
+    for (int x = n > 2 ? n - 2 : 0; x < n; ++x) mbar_wait(&sm.raw_full[x & 1], (uint32_t)(x >> 1) & 1u, p.wait_budget);
+  } else if (warp == 2) {
+    // ================================================================ scales
+    // Lanes 0..7: K scale of a 16-key group, 8..15: V scale. Keys behind the
+    // sequence are masked: any finite scale serves.
+    auto load = [&](int u) -> float {
+      const int j = kmin + u * kBN + 16 * (lane & (kGroups - 1));
+      const float* src = (lane < kGroups ? p.ks : p.vs) + (long long)bg * p.nblk;
+      return lane < 2 * kGroups && u < ntiles && j < total ? __ldg(src + (j >> p.bs_log2)) : 1.f;
+    };
+    float next = load(0), after = load(1);
+    bool ok = true;
+    for (int u = 0; u < ntiles && ok; ++u) {
+      const int slot = u & (kScStages - 1);
+      const float scale = next;
+      next = after;
+      after = load(u + 2);
+      ok = __all_sync(0xffffffffu, mbar_wait(&sm.sc_empty[slot], ((uint32_t)(u / kScStages) & 1u) ^ 1u, p.wait_budget) && !aborted(sm));
+      if (!ok) break;
+      if (lane < kGroups) {
+        sm.ks[slot][lane] = fmaxf(scale, 1e-30f);   // positive: a mask of -inf stays -inf
+      } else if (lane < 2 * kGroups) {
+        // v' at least 2^-60: a zero block's V adds nothing that counts, but its keys' P must reach l
+        const float v = fminf(fmaxf(scale * __int_as_float((127 - wexp) << 23), 0x1p-60f), 1.f);
+        sm.lv[slot][lane - kGroups] = kLift + log2f(v);
+        sm.iv[slot][lane - kGroups] = __fdiv_rn(0x1p-6f, v);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.sc_full[slot]);
+    }
+    if (!ok && lane == 0) set_abort(p, sm);
   } else if (warp == 1) {
     // ================================================================ MMA issuer
-    uint64_t dk[2], dq[2], dv[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      dk[i] = desc_kmajor_sw128(smem_addr(sm.kf[i]));
-      dq[i] = desc_kmajor_sw128(smem_addr(sm.q[i]));
-      dv[i] = desc_mnmajor_sw128(smem_addr(sm.vf[i % kVB]), kBox, 1024);
-    }
-    auto issue_s = [&](int q, int kb) {
-      const uint32_t d = tmem + q * 128;
+    // Descriptors of buffer 0; a buffer further is a constant away (16-byte units).
+    const uint64_t dk0 = desc_kmajor_sw128(smem_addr(sm.kf[0])), dq0 = desc_kmajor_sw128(smem_addr(sm.q[0]));
+    const uint64_t dv0 = desc_mnmajor_sw128(smem_addr(sm.vf[0]), kBox, 1024);
+    // S_q of step h into buffer h & 1 of query tile q: keys 64 (h & 1) .. of K tile h / 2.
+    auto issue_s = [&](int q, int h) {
+      const uint32_t d = tmem + q * 128 + (h & 1) * kStep;
+      const uint64_t b0 = dk0 + (uint64_t)(((h >> 1) % kNB) * (int)(kTile >> 4) + (h & 1) * (kStep * 128 >> 4));
 #pragma unroll
       for (int part = 0; part < (F32 ? 2 : 1); ++part) {   // the lo tile starts 32 KB after the hi tile
-        const uint64_t a0 = dq[q] + (uint64_t)(part * (int)((2 * kBox) >> 4));
+        const uint64_t a0 = dq0 + (uint64_t)(q * (int)(SM::kQ >> 4) + part * (int)((2 * kBox) >> 4));
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
           const uint64_t off = (uint64_t)((ks >> 2) * 1024 + (ks & 3) * 2);
-          mma_f16_ss(d, a0 + off, dk[kb] + off, kIdS, part > 0 || ks > 0);
+          mma_f16_ss(d, a0 + off, b0 + off, kIdS, part > 0 || ks > 0);
         }
       }
-      mma_commit(&sm.s_full[q]);
+      mma_commit(&sm.s_full[q][h & 1]);
     };
-    // Keys 64 h .. of P: hi pairs in columns 64 h .. + 31 of S_q (lo pairs in the next 32).
-    auto issue_pv = [&](int q, int vb, bool acc) {
+    // O_q += P V of step h: hi pairs in columns 0 .. 31 of the S buffer (lo pairs in the next 32).
+    auto issue_pv = [&](int q, int h) {
       const uint32_t d = tmem + 256 + q * 128;
-      const uint32_t pa = tmem + q * 128;
+      const uint32_t pa = tmem + q * 128 + (h & 1) * kStep;
+      const uint64_t b0 = dv0 + (uint64_t)(((h >> 1) % kNB) * (int)(kTile >> 4) + (h & 1) * (kStep * 128 >> 4));
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        const uint32_t col = (uint32_t)((ks >> 2) * 64 + (ks & 3) * 8);
-        const uint64_t bv = dv[vb] + (uint64_t)(ks * 128);
-        mma_f16_ts(d, pa + col, bv, kIdO, acc || ks > 0);
-        if constexpr (F32) mma_f16_ts(d, pa + col + 32, bv, kIdO, true);
+      for (int ks = 0; ks < 4; ++ks) {
+        const uint64_t bv = b0 + (uint64_t)(ks * 128);
+        mma_f16_ts(d, pa + 8 * ks, bv, kIdO, h > 0 || ks > 0);
+        if constexpr (F32) mma_f16_ts(d, pa + 32 + 8 * ks, bv, kIdO, true);
       }
       mma_commit(&sm.o_done[q]);
     };
     auto wait1 = [&](uint64_t* bar, uint32_t par) {
       return __all_sync(0xffffffffu, mbar_wait(bar, par, p.wait_budget)) != 0;
     };
+    // S of step h for query tile q; the K tile is released behind its last use.
+    auto next_s = [&](int q, int h) {
+      if (elect_one()) {
+        issue_s(q, h);
+        if (q == 1 && ((h & 1) || h + 1 == nsteps)) mma_commit(&sm.kf_empty[(h >> 1) % kNB]);
+      }
+      __syncwarp();
+    };
     uint64_t* q_ok = F32 ? sm.q_ready : sm.q_land;
-    bool ok = wait1(&q_ok[0], 0) && wait1(&sm.kf_full[0], 0);
-    if (ok && elect_one()) {
+    bool ok = wait1(&sm.kf_full[0], 0);
+    for (int q = 0; q < 2 && ok; ++q) {
+      ok = wait1(&q_ok[q], 0);
+      if (!ok) break;
       tc_fence_after();
-      issue_s(0, 0);
+      next_s(q, 0);
     }
-    __syncwarp();
-    if (ok) ok = wait1(&q_ok[1], 0);
-    if (ok && elect_one()) {
-      tc_fence_after();
-      issue_s(1, 0);
-      mma_commit(&sm.kf_empty[0]);
-    }
-    __syncwarp();
-    for (int t = 0; t < ntiles && ok; ++t) {
-      const uint32_t tp = (uint32_t)t & 1u;
-      const bool more = t + 1 < ntiles;
-      const int kb1 = (t + 1) & 1, vb = t % kVB;
-      if (!wait1(&sm.vf_full[vb], (uint32_t)(t / kVB) & 1u) || !wait1(&sm.p_full[0], tp)) {
-        ok = false;
-        break;
-      }
-      if (elect_one()) {
+    for (int q = 0; q < 2 && ok && nsteps > 1; ++q) next_s(q, 1);
+    for (int h = 0; h < nsteps && ok; ++h) {
+      const int t = h >> 1;
+      if ((h & 1) == 0) ok = wait1(&sm.vf_full[t % kNB], (uint32_t)(t / kNB) & 1u);
+      for (int q = 0; q < 2 && ok; ++q) {
+        ok = wait1(&sm.p_full[q][h & 1], (uint32_t)t & 1u);
+        if (!ok) break;
         tc_fence_after();
-        issue_pv(0, vb, t > 0);
-      }
-      __syncwarp();
-      if (more && !wait1(&sm.kf_full[kb1], (uint32_t)((t + 1) >> 1) & 1u)) {
-        ok = false;
-        break;
-      }
-      if (more && elect_one()) {
-        tc_fence_after();
-        issue_s(0, kb1);
-      }
-      __syncwarp();
-      if (!wait1(&sm.p_full[1], tp)) {
-        ok = false;
-        break;
-      }
-      if (elect_one()) {
-        tc_fence_after();
-        issue_pv(1, vb, t > 0);
-        mma_commit(&sm.vf_empty[vb]);
-        if (more) {
-          issue_s(1, kb1);
-          mma_commit(&sm.kf_empty[kb1]);
+        if (elect_one()) {
+          issue_pv(q, h);
+          if (q == 1 && ((h & 1) || h + 1 == nsteps)) mma_commit(&sm.vf_empty[t % kNB]);
+        }
+        __syncwarp();
+        if (h + 2 < nsteps) {
+          if (q == 0 && (h & 1) == 0) {
+            ok = wait1(&sm.kf_full[(t + 1) % kNB], (uint32_t)((t + 1) / kNB) & 1u);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          next_s(q, h + 2);
         }
       }
-      __syncwarp();
       if (__any_sync(0xffffffffu, aborted(sm))) ok = false;
     }
     if (!ok && lane == 0) set_abort(p, sm);
@@ -357,52 +454,26 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
       mbar_wait(&sm.drain, 0, p.wait_budget);
     }
     __syncwarp();
+  }
   } else if (warp >= kConvWarp0) {
+    regs_down<kRegsConv>();
     // ================================================================ converters
-    // Order: K(0), then K(t+1) (its buffer is free once S_1(t-1) is done) and
-    // V(t). The scales of a tile (both kinds) go out with its K.
     constexpr int kSteps = kConvRows * 8 / 32;
     const int row0 = (warp - kConvWarp0) * kConvRows;
-    const long long ncache = (long long)p.B * p.Nkv * p.C;
-    const int nconv = 2 * ntiles;
-    auto item = [&](int n, bool& is_k) -> int {
-      if (n == 0) {
-        is_k = true;
-        return 0;
-      }
-      const int t = (n - 1) >> 1;
-      is_k = ((n - 1) & 1) == 0 && t + 1 < ntiles;
-      return is_k ? t + 1 : t;
-    };
-    auto load = [&](int n, uint4* w, float& scale) {
+    bool ok = true;
+    for (int n = 0; n < nconv && ok; ++n) {
       bool is_k;
       const int u = item(n, is_k);
-      const int8_t* cache = is_k ? p.kc : p.vc;
-      const long long grow0 = krow0 + (long long)u * kBN + row0;
+      ok = __all_sync(0xffffffffu, mbar_wait(&sm.raw_full[n & 1], (uint32_t)(n >> 1) & 1u, p.wait_budget) && !aborted(sm));
+      if (!ok) break;
+      uint4 w[kSteps];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int x = s * 32 + lane;
-        const long long gr = grow0 + (x >> 3);
-        w[s] = gr < ncache ? __ldg(reinterpret_cast<const uint4*>(cache + gr * kHD + (x & 7) * 16)) : make_uint4(0u, 0u, 0u, 0u);
-      }
-      if (is_k && warp == kConvWarp0 && lane < 2 * kGroups) {
-        const int j = kmin + u * kBN + 16 * (lane & (kGroups - 1));
-        const float* src = (lane < kGroups ? p.ks : p.vs) + (long long)bg * p.nblk;
-        scale = j < total ? __ldg(src + (j >> p.bs_log2)) : 1.f;   // masked keys: any finite scale
-      }
-    };
-    bool withheld = false;
-    auto convert = [&](int n, const uint4* w, float scale) -> bool {
-      bool is_k;
-      const int u = item(n, is_k);
-      if (u == p.withhold_tile) {   // testing: this tile is never converted, the waits for it expire
-        withheld = true;
-        return false;
-      }
-      uint64_t* empty = is_k ? &sm.kf_empty[u & 1] : &sm.vf_empty[u % kVB];
-      const uint32_t pe = (is_k ? (uint32_t)(u >> 1) : (uint32_t)(u / kVB)) & 1u;
-      if (!__all_sync(0xffffffffu, mbar_wait(empty, pe ^ 1u, p.wait_budget)) || aborted(sm)) return false;
-      uint8_t* dst = is_k ? sm.kf[u & 1] : sm.vf[u % kVB];
+      for (int s = 0; s < kSteps; ++s)   // step s: rows row0 + 4 s .., lane = 16-byte chunk in order
+        w[s] = *reinterpret_cast<const uint4*>(sm.raw[n & 1] + row0 * kHD + (s * 32 + lane) * 16);
+      ok = __all_sync(0xffffffffu, mbar_wait(is_k ? &sm.kf_empty[u % kNB] : &sm.vf_empty[u % kNB],
+                                             ((uint32_t)(u / kNB) & 1u) ^ 1u, p.wait_budget) && !aborted(sm));
+      if (!ok) break;
+      uint8_t* dst = is_k ? sm.kf[u % kNB] : sm.vf[u % kNB];
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         const int x = s * 32 + lane, row = row0 + (x >> 3), j = x & 7;
@@ -412,37 +483,18 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
         *reinterpret_cast<uint4*>(bx + sw128_offset(row, 2 * (j & 3))) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4*>(bx + sw128_offset(row, 2 * (j & 3) + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
       }
-      if (is_k && warp == kConvWarp0 && lane < 2 * kGroups) {
-        const int slot = u & (kScStages - 1), grp = lane & (kGroups - 1);
-        if (lane < kGroups) {
-          sm.ks[slot][grp] = fmaxf(scale, 1e-30f);   // positive: a mask of -inf stays -inf
-        } else {
-          // v' at least 2^-60: a zero block's V adds nothing that counts, but its keys' P must reach l
-          const float v = fminf(fmaxf(scale * __int_as_float((127 - wexp) << 23), 0x1p-60f), 1.f);
-          sm.lv[slot][grp] = kLift + log2f(v);
-          sm.iv[slot][grp] = __fdiv_rn(0x1p-6f, v);
-        }
-      }
       fence_async_smem();   // fp16 tile (generic stores) -> async proxy: the MMAs may read it
       __syncwarp();
-      if (lane == 0) mbar_arrive(is_k ? &sm.kf_full[u & 1] : &sm.vf_full[u % kVB]);
-      return true;
-    };
-    uint4 wa[kSteps], wb[kSteps];
-    float sa = 1.f, sb = 1.f;
-    bool ok = true;
-    load(0, wa, sa);
-    for (int n = 0; n < nconv && ok; n += 2) {
-      if (n + 1 < nconv) load(n + 1, wb, sb);
-      ok = convert(n, wa, sa);
-      if (!ok || n + 1 >= nconv) break;
-      if (n + 2 < nconv) load(n + 2, wa, sa);
-      ok = convert(n + 1, wb, sb);
+      if (lane == 0) {
+        mbar_arrive(&sm.raw_empty[n & 1]);
+        mbar_arrive(is_k ? &sm.kf_full[u % kNB] : &sm.vf_full[u % kNB]);
+      }
     }
-    if (!ok && !withheld && lane == 0) set_abort(p, sm);
+    if (!ok && lane == 0) set_abort(p, sm);
   } else {
     // ================================================================ softmax groups
-    const int q = (warp - 2) >> 2;            // query tile of this group
+    regs_up<kRegsSoft>();
+    const int q = (warp - kSoftWarp0) >> 2;   // query tile of this group
     const int quarter = warp & 3;             // tensor-memory lane quarter of this warp
     const int rl = quarter * 32 + lane;
     const int r = r0 + q * kBM + rl;
@@ -459,146 +511,138 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
     bool ok = true;
     float rho = 1.f;
     if constexpr (F32) {
-      split_rows(p, sm, tid - 64);
+      split_rows(p, sm, tid - 32 * kSoftWarp0);
       ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_ready[q], 0, p.wait_budget));   // rho of every row written
       rho = sm.rho[q][rl];
     }
     const float k_row = rho * p.scale * (CAP ? 1.f / p.softcap : kLog2e);
-    float cq[6];
     const float c2 = p.softcap * kLog2e;
-    if constexpr (CAP) {
-      const float fit[6] = {1.0f, -0.3333325982093811f, 0.13331091403961182f, -0.053718484938144684f,
-                            0.020583488047122955f, -0.005652355030179024f};
-#pragma unroll
-      for (int e = 0; e < 6; ++e) cq[e] = fit[e] * c2;
-    }
     float m_run = kNegBig, l_run = 0.f;
-    for (int t = 0; t < ntiles && ok; ++t) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_full[q], (uint32_t)t & 1u, p.wait_budget) && !aborted(sm))) {
+    for (int st = 0; st < nsteps && ok; ++st) {
+      const int t = st >> 1, hf = st & 1, slot = t & (kScStages - 1);
+      bool got = mbar_wait(&sm.s_full[q][hf], (uint32_t)t & 1u, p.wait_budget) && !aborted(sm);
+      if (hf == 0) got = got && mbar_wait(&sm.sc_full[slot], (uint32_t)(t / kScStages) & 1u, p.wait_budget);
+      if (!__all_sync(0xffffffffu, got)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const int slot = t & (kScStages - 1);
-      const int j0 = kmin + t * kBN;
-      const int lo = max(lo_key - j0, 0), hi = min(hi_key - j0, kBN);   // visible columns [lo, hi)
-      const bool full = __all_sync(0xffffffffu, lo == 0 && hi == kBN);
-      // Pass 1: row max, 64 columns at a time; masked (and softcapped) scores are written back.
-      float mt = kNegBig;
+      const uint32_t s_buf = s_addr + hf * kStep;
+      uint32_t x[64];
+      tmem_ld32(s_buf, x);
+      tmem_ld32(s_buf + 32, x + 32);
+      const float4 kg = *reinterpret_cast<const float4*>(&sm.ks[slot][4 * hf]);
+      const float kkg[4] = {kg.x * k_row, kg.y * k_row, kg.z * k_row, kg.w * k_row};
+      const int j0 = kmin + st * kStep;
+      const int lo = max(lo_key - j0, 0), hi = min(hi_key - j0, kStep);   // visible columns [lo, hi)
+      const bool full = __all_sync(0xffffffffu, lo == 0 && hi == kStep);
+      tmem_ld_wait();
+      // Row max (a softcap is monotone); a softcap also takes the largest
+      // |score|. Masked columns then hold what the exponent turns into -inf:
+      // -inf, or +inf under a softcap's fit (its last coefficient is negative,
+      // so u Q(u^2) is -inf there).
+      float ua = 0.f;
+      if constexpr (CAP) {
+        if (!full) {
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t x[64];
-        tmem_ld32(s_addr + hf * 64, x);
-        tmem_ld32(s_addr + hf * 64 + 32, x + 32);
-        tmem_ld_wait();
-        const float4 kg = *reinterpret_cast<const float4*>(&sm.ks[slot][4 * hf]);
-        const float ksg[4] = {kg.x, kg.y, kg.z, kg.w};
-        if constexpr (CAP) {
-          float zmax = 0.f;
-#pragma unroll
-          for (int gi = 0; gi < 4; ++gi) {
-            const float f = ksg[gi] * k_row;
-            const float2 f2 = make_float2(f, f);
-#pragma unroll
-            for (int e = 16 * gi; e < 16 * gi + 16; e += 2) {
-              const float2 u = ffma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), f2, make_float2(0.f, 0.f));
-              const float2 z = ffma2(u, u, make_float2(0.f, 0.f));
-              zmax = fmax3(zmax, z.x, z.y);
-              const float2 y = cap_poly(u, z, cq);
-              x[e] = __float_as_uint(y.x);
-              x[e + 1] = __float_as_uint(y.y);
-            }
-          }
-          if (__any_sync(0xffffffffu, !(zmax <= kCapZ))) {   // large scores: the raw products once more
-#pragma unroll 1
-            for (int gi = 0; gi < 4; ++gi) {
-              const float f = sm.ks[slot][4 * hf + gi] * k_row;
-              uint32_t raw[16];
-              tmem_ld16(s_addr + hf * 64 + 16 * gi, raw);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const float2 u = make_float2(__uint_as_float(raw[e]) * f, __uint_as_float(raw[e + 1]) * f);
-                const float2 z = make_float2(u.x * u.x, u.y * u.y);
-                const float2 y = cap_poly(u, z, cq);
-                raw[e] = __float_as_uint(z.x <= kCapZ ? y.x : cap_exp(u.x, c2));
-                raw[e + 1] = __float_as_uint(z.y <= kCapZ ? y.y : cap_exp(u.y, c2));
-              }
-              tmem_st16(s_addr + hf * 64 + 16 * gi, raw);
-            }
-            tmem_st_wait();
-            tmem_ld32(s_addr + hf * 64, x);
-            tmem_ld32(s_addr + hf * 64 + 32, x + 32);
-            tmem_ld_wait();
-          }
-        }
-        if (CAP || !full) {
-          if (!full) {
-#pragma unroll
-            for (int e = 0; e < 64; ++e) {
-              const int col = hf * 64 + e;
-              x[e] = (col >= lo && col < hi) ? x[e] : 0xff800000u;   // -inf
-            }
-          }
-          tmem_st32(s_addr + hf * 64, x);
-          tmem_st32(s_addr + hf * 64 + 32, x + 32);
+          for (int e = 0; e < 64; ++e) x[e] = (e >= lo && e < hi) ? x[e] : 0u;
         }
 #pragma unroll
         for (int gi = 0; gi < 4; ++gi) {
-          float a = fmax3(__uint_as_float(x[16 * gi]), __uint_as_float(x[16 * gi + 1]), __uint_as_float(x[16 * gi + 2]));
-          float c = fmax3(__uint_as_float(x[16 * gi + 3]), __uint_as_float(x[16 * gi + 4]), __uint_as_float(x[16 * gi + 5]));
+          float a = 0.f, c = 0.f;
 #pragma unroll
-          for (int e = 6; e < 16; e += 4) {
-            a = fmax3(a, __uint_as_float(x[16 * gi + e]), __uint_as_float(x[16 * gi + e + 1]));
-            if (e + 2 < 16) c = fmax3(c, __uint_as_float(x[16 * gi + e + 2]), __uint_as_float(x[16 * gi + e + 3]));
+          for (int e = 16 * gi; e < 16 * gi + 16; e += 4) {
+            a = fmax3(a, fabsf(__uint_as_float(x[e])), fabsf(__uint_as_float(x[e + 1])));
+            c = fmax3(c, fabsf(__uint_as_float(x[e + 2])), fabsf(__uint_as_float(x[e + 3])));
           }
-          const float mg = fmaxf(a, c);
-          mt = fmaxf(mt, CAP ? mg : mg * (ksg[gi] * k_row));
+          ua = fmaxf(ua, fmaxf(a, c) * kkg[gi]);
         }
       }
-      if (CAP || !full) tmem_st_wait();
-      // Lazy rescale: O_q is complete up to tile t-1 (its MMAs precede S_q(t)).
+      if (!full) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e) x[e] = (e >= lo && e < hi) ? x[e] : 0xff800000u;   // -inf
+      }
+      float mt = -INFINITY;
+#pragma unroll
+      for (int gi = 0; gi < 4; ++gi) {
+        float a = __uint_as_float(x[16 * gi]), c = __uint_as_float(x[16 * gi + 1]);
+#pragma unroll
+        for (int e = 16 * gi + 2; e < 16 * gi + 14; e += 4) {
+          a = fmax3(a, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+          c = fmax3(c, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+        }
+        a = fmax3(a, __uint_as_float(x[16 * gi + 14]), __uint_as_float(x[16 * gi + 15]));
+        mt = fmaxf(mt, fmaxf(a, c) * kkg[gi]);
+      }
+      if constexpr (CAP) {
+        if (mt > kNegBig) mt = cap_any(make_float2(mt, mt), c2).x;
+        if (!full) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e) x[e] = x[e] == 0xff800000u ? 0x7f800000u : x[e];   // +inf
+        }
+      }
+      // Lazy rescale: O_q holds P.V up to the last step once that is done.
       const bool grow = mt > m_run + kLazy;
-      const float m_new = grow ? mt : m_run;
-      if (t > 0 && __any_sync(0xffffffffu, grow)) {
-        const float f = grow ? ex2(m_run - m_new) : 1.0f;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float m_new = grow ? mt : m_run;
+        if (st > 0) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&sm.o_done[q], (uint32_t)(st - 1) & 1u, p.wait_budget))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const float f = grow ? ex2(m_run - m_new) : 1.0f;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t raw[32];
-          tmem_ld32(o_addr + c * 32, raw);
-          tmem_ld_wait();
+          for (int c = 0; c < 8; ++c) {   // 16 columns at a time: the step's scores stay live
+            uint32_t raw[16];
+            tmem_ld16(o_addr + c * 16, raw);
+            tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * f);
-          tmem_st32(o_addr + c * 32, raw);
+            for (int e = 0; e < 16; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * f);
+            tmem_st16(o_addr + c * 16, raw);
+          }
+          l_run *= f;
         }
-        l_run *= f;
+        m_run = m_new;
       }
-      m_run = m_new;
-      // Pass 2: P' per 16 keys; keys 64 hf ..: hi pairs over columns 64 hf ..
-      // + 31, lo pairs over the next 32 (only columns of the half just read).
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t x[64];
-        tmem_ld32(s_addr + hf * 64, x);
-        tmem_ld32(s_addr + hf * 64 + 32, x + 32);
-        const float4 kg = *reinterpret_cast<const float4*>(&sm.ks[slot][4 * hf]);
-        const float4 lg = *reinterpret_cast<const float4*>(&sm.lv[slot][4 * hf]);
-        const float4 ig = *reinterpret_cast<const float4*>(&sm.iv[slot][4 * hf]);
-        const float ksg[4] = {kg.x, kg.y, kg.z, kg.w}, lvg[4] = {lg.x, lg.y, lg.z, lg.w}, ivg[4] = {ig.x, ig.y, ig.z, ig.w};
-        tmem_ld_wait();
+      const float4 lg = *reinterpret_cast<const float4*>(&sm.lv[slot][4 * hf]);
+      const float4 ig = *reinterpret_cast<const float4*>(&sm.iv[slot][4 * hf]);
+      const float ccg[4] = {lg.x - m_run, lg.y - m_run, lg.z - m_run, lg.w - m_run}, ivg[4] = {ig.x, ig.y, ig.z, ig.w};
+      // P' of the step: hi pairs over the buffer's first 32 columns, lo pairs over the next.
+      // MODE 0: no softcap; 3, 7: its fit of that degree; 9: any size.
+      auto exponents = [&](auto mode) {
+        constexpr int MODE = decltype(mode)::value;
 #pragma unroll
         for (int qq = 0; qq < 2; ++qq) {
-          uint32_t ph[16], pl[F32 ? 16 : 1];
+          uint32_t ph[16];
+          [[maybe_unused]] uint32_t pl[F32 ? 16 : 1];
 #pragma unroll
           for (int gi = 0; gi < 2; ++gi) {
             const int gr = 2 * qq + gi;
-            const float kk = CAP ? 1.f : ksg[gr] * k_row, cc = lvg[gr] - m_run;
-            const float2 kk2 = make_float2(kk, kk), cc2 = make_float2(cc, cc);
+            const float2 kk2 = make_float2(kkg[gr], kkg[gr]), cc2 = make_float2(ccg[gr], ccg[gr]);
             float2 ls = make_float2(0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const int e = 16 * gr + 2 * k;
-              const float2 arg = ffma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), kk2, cc2);
+              const float2 x2 = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+              float2 arg;
+              if constexpr (MODE == 0) {
+                arg = ffma2(x2, kk2, cc2);
+              } else {
+                const float2 u = ffma2(x2, kk2, make_float2(0.f, 0.f));
+                if constexpr (MODE == 9) {
+                  const float2 y = cap_any(u, c2);
+                  arg = make_float2(y.x + ccg[gr], y.y + ccg[gr]);
+                  if (!full) {
+                    arg.x = x[e] == 0x7f800000u ? -INFINITY : arg.x;
+                    arg.y = x[e + 1] == 0x7f800000u ? -INFINITY : arg.y;
+                  }
+                } else {
+                  const float2 z = ffma2(u, u, make_float2(0.f, 0.f));
+                  const float2 uc = ffma2(u, make_float2(c2, c2), make_float2(0.f, 0.f));
+                  arg = ffma2(uc, cap_fit<MODE>(z), cc2);
+                }
+              }
               const float pa = ex2(arg.x), pb = ex2(arg.y);
               ls = ffma2(make_float2(pa, pb), make_float2(1.f, 1.f), ls);
               const __half2 hp = __floats2half2_rn(pa, pb);
@@ -611,18 +655,39 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
             }
             l_run = fmaf(ls.x + ls.y, ivg[gr], l_run);
           }
-          tmem_st16(s_addr + hf * 64 + 16 * qq, ph);
-          if constexpr (F32) tmem_st16(s_addr + hf * 64 + 32 + 16 * qq, pl);
+          tmem_st16(s_buf + 16 * qq, ph);
+          if constexpr (F32) tmem_st16(s_buf + 32 + 16 * qq, pl);
         }
+      };
+      if constexpr (CAP) {
+        if (__all_sync(0xffffffffu, !(ua > kCapLow)))
+          exponents(std::integral_constant<int, 3>());
+        else if (__all_sync(0xffffffffu, !(ua > kCapHigh)))
+          exponents(std::integral_constant<int, 7>());
+        else
+          exponents(std::integral_constant<int, 9>());
+      } else {
+        exponents(std::integral_constant<int, 0>());
       }
       tmem_st_wait();
+      // The epilogue waits for the last P.V by its phase parity: the one before
+      // must be over by then (it may still run here).
+      if (st > 0 && st + 1 == nsteps &&
+          !__all_sync(0xffffffffu, mbar_wait(&sm.o_done[q], (uint32_t)(st - 1) & 1u, p.wait_budget))) {
+        ok = false;
+        break;
+      }
       tc_fence_before();
-      mbar_arrive(&sm.p_full[q]);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sm.p_full[q][hf]);
+        if (hf == 1 || st + 1 == nsteps) mbar_arrive(&sm.sc_empty[slot]);
+      }
     }
     // ---- epilogue: O / l (+ sink) in units of 2^(wexp - kLift), staged in the
     // group's query tile (free once its last P.V is done) and written with
     // tensor stores (rows past S are skipped).
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_done[q], (uint32_t)(ntiles - 1) & 1u, p.wait_budget) && !aborted(sm));
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_done[q], (uint32_t)(nsteps - 1) & 1u, p.wait_budget) && !aborted(sm));
     if (ok) {
       tc_fence_after();
       float mf = m_run, extra = 0.f;
@@ -665,7 +730,7 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
     }
     if (!group_all(ok, q)) {
       if (lane == 0) set_abort(p, sm);
-    } else if (quarter == 2 && elect_one()) {   // warp 2 (group 0) or 6 (group 1)
+    } else if (quarter == 0 && elect_one()) {   // one thread of the group
       for (int k = 0; k < kBoxes; ++k)
         tma_store_4d(&tmo, sm.q[q] + k * kBox, kBoxDims * k, g * p.G, (r0 + q * kBM) / p.G, b);
       bulk_commit();
@@ -692,12 +757,15 @@ cudaError_t launch_one(const BlockParams& p, cudaStream_t st) {
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
     done[dev] = true;
   }
-  CUtensorMap mq, mo;
+  CUtensorMap mq, mo, mk, mv;
+  const uint64_t crows = (uint64_t)p.B * p.Nkv * p.C;
+  if ((e = encode_u8_2d(&mk, p.kc, crows, kHD, kHD, kHD, kBN)) != cudaSuccess) return e;
+  if ((e = encode_u8_2d(&mv, p.vc, crows, kHD, kHD, kHD, kBN)) != cudaSuccess) return e;
   auto encode = F32 ? encode_f32_query_sw128 : encode_fp16_query_sw128;
   if ((e = encode(&mq, p.q, p.B, p.S, p.N, (uint32_t)p.G)) != cudaSuccess) return e;
   if ((e = encode(&mo, p.out, p.B, p.S, p.N, (uint32_t)p.G)) != cudaSuccess) return e;
   const unsigned nqb = (unsigned)((p.S * p.G + 2 * kBM - 1) / (2 * kBM)), nbg = (unsigned)(p.B * p.Nkv);
-  kern<<<p.qb_major ? dim3(nbg, nqb) : dim3(nqb, nbg), kThreads, smem, st>>>(p, mq, mo);
+  kern<<<p.qb_major ? dim3(nbg, nqb) : dim3(nqb, nbg), kThreads, smem, st>>>(p, mq, mo, mk, mv);
   return cudaGetLastError();
 }
 

@@ -212,7 +212,7 @@ gqa_status plan_block(const gqa_handle* h, const gqa_block_cache* cache, const g
   pl->part_o = pl->part_ml = pl->stash = pl->lse = 0;
   if (pl->prefill) {
     const long long nqb = (rows + 255) / 256;
-    if (nqb > 65535) return fail(GQA_ERR_UNSUPPORTED, "query too large");
+    if (nqb > 65535 || (T + 127) / 128 > 65535) return fail(GQA_ERR_UNSUPPORTED, "query too large");
     P.qb_major = 2 * S >= T;   // key ranges differ by query block more than by sequence
   } else {
     P.rt_rows = gqa::block_row_tile(P.t_type, (int)H, rows);
@@ -377,7 +377,9 @@ gqa_status gqa_block_forward(gqa_handle* h, const gqa_block_cache* cache, const 
     if (e != cudaSuccess) return cuda_fail(e, "merge launch");
   }
   if (P.lse) {
-    e = timed_launch(h, GQA_KERNEL_BLOCK_WEIGHTS, st, [&] { return gqa::launch_block_weights(P, st); });
+    e = timed_launch(h, GQA_KERNEL_BLOCK_WEIGHTS, st, [&] {
+      return pl.prefill && P.t_type == gqa::kF16 ? gqa::launch_block_weights_tc(P, st) : gqa::launch_block_weights(P, st);
+    });
     if (e != cudaSuccess) return cuda_fail(e, "weights launch");
   }
   return GQA_OK;

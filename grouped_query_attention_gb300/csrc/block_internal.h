@@ -76,6 +76,8 @@ cudaError_t launch_block_merge(const BlockParams& p, cudaStream_t st);
 cudaError_t launch_block_prefill(const BlockParams& p, cudaStream_t st);
 // Attention weights of the cache rows from the log-sum-exp of every query row.
 cudaError_t launch_block_weights(const BlockParams& p, cudaStream_t st);
+// ... on the tensor cores: where the tensor-core prefill runs with fp16 queries.
+cudaError_t launch_block_weights_tc(const BlockParams& p, cudaStream_t st);
 
 struct EvictParams {
   int B, Nkv, H, C, Cto, T;

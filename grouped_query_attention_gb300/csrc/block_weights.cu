@@ -1,0 +1,302 @@
+// Attention weights of the cache rows after a tensor-core prefill (head size
+// 128, group size dividing 128, fp16): w[j] = sum over the query rows r that
+// see key j of exp2(s_rj - lse_r), lse_r the row's log-sum-exp that the
+// prefill left in the workspace (log2 domain).
+//
+// CTA = 128 keys of one KV head. Keys are the M side of S^T = K Q^T (128 keys
+// x 128 query rows a tile), so a key is a tensor-memory lane and its sum stays
+// in one thread: no reduction across threads, no atomics, and the K scale is
+// one number per thread. Query tiles arrive by TMA (two stages); two softmax
+// groups take alternate tiles, each with its own tensor-memory buffer.
+//
+// Bound: exp2, one per visible pair (16 a clock and SM: 1024 cycles a tile
+// against 512 of MMAs). Two CTAs share an SM (256 tensor-memory columns each).
+// Causal: key tile 0 meets every query row, the last few; the longest start first.
+#include <cuda_fp16.h>
+
+#include "block_internal.h"
+#include "block_tc.cuh"
+#include "common.cuh"
+#include "tcgen05.cuh"
+#include "tma_host.h"
+
+namespace gqa {
+namespace {
+
+using namespace tc;
+
+constexpr int kKeys = 128;                     // keys of a CTA
+constexpr int kRows = 128;                     // query rows of a tile
+constexpr int kHD = 128;
+constexpr int kThreads = 384;
+constexpr int kSoftWarp0 = 4;
+constexpr uint32_t kBox = 128u * 128u;
+constexpr uint32_t kTile = 2u * kBox;
+constexpr uint32_t kIdS = idesc_f16(128, 128, 0, 0);
+
+struct __align__(1024) WtSmem {
+  uint8_t k[kTile];                            // fp16 codes, K-major
+  uint8_t q[2][kTile];
+  float nl[2][kRows];                          // -lse of the tile's rows
+  float part[kKeys];                           // the second group's sums
+  uint64_t q_full[2], q_empty[2], nl_full[2], nl_empty[2], s_full[2], s_empty[2];
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+};
+static_assert(2 * (sizeof(WtSmem) + 1024 + 1024) <= 233472, "two CTAs per SM");
+
+__device__ __forceinline__ bool aborted(const WtSmem& sm) {
+  return *reinterpret_cast<const volatile int*>(&sm.abort) != 0;
+}
+__device__ __forceinline__ void set_abort(const BlockParams& p, WtSmem& sm) {
+  *reinterpret_cast<volatile int*>(&sm.abort) = 1;
+  if (p.status) atomicOr(p.status, GQA_DEVICE_TIMEOUT_BIT);
+}
+
+template <bool CAP>
+__global__ void __launch_bounds__(kThreads, 2)
+block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmq) {
+  extern __shared__ uint8_t smem_raw[];
+  WtSmem& sm = *reinterpret_cast<WtSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int bg = blockIdx.x, b = bg / p.Nkv, g = bg % p.Nkv;
+  int total, fresh;
+  if (!block_lengths(p, b, &total, &fresh)) return;
+  const int j0 = (int)blockIdx.y * kKeys;
+  if (j0 >= total) return;
+  const int past = total - fresh;
+  // Positions of the step that see a key of this block, and their rows in tiles of 128.
+  const int i_lo = max(0, j0 - past);
+  const int i_hi = p.window >= 0 ? min(fresh, j0 + kKeys + p.window - past) : fresh;
+  const int rows0 = i_lo * p.G, rows1 = i_hi * p.G;
+  const int ntiles = rows1 > rows0 ? (rows1 - rows0 + kRows - 1) / kRows : 0;
+
+  if (warp == 1) tmem_alloc(&sm.tmem, 256);
+  if (tid == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sm.q_full[t], 1);
+      mbar_init(&sm.q_empty[t], 1);
+      mbar_init(&sm.nl_full[t], 1);
+      mbar_init(&sm.nl_empty[t], 4);
+      mbar_init(&sm.s_full[t], 1);
+      mbar_init(&sm.s_empty[t], 4);
+    }
+    mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    mbar_fence_init();
+  }
+  // The key tile: rows behind the sequence are left as zeros.
+  for (int x = tid; x < kKeys * 8; x += kThreads) {
+    const int row = x >> 3, j = x & 7;
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (j0 + row < total)
+      w = *reinterpret_cast<const uint4*>(p.kc + ((long long)bg * p.C + j0 + row) * kHD + 16 * j);
+    uint32_t h[8];
+    codes16(w, h);
+    uint8_t* bx = sm.k + (j >> 2) * kBox;
+    *reinterpret_cast<uint4*>(bx + sw128_offset(row, 2 * (j & 3))) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(bx + sw128_offset(row, 2 * (j & 3) + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+  }
+  fence_async_smem();   // key tile (generic stores) -> async proxy: the MMAs read it
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  if (warp == 0) {
+    // ================================================================ TMA: query tiles
+    bool ok = true;
+    int n = 0;
+    for (; n < ntiles && ok; ++n) {
+      if (n == p.withhold_tile) break;   // testing: this tile is never copied, the waits for it expire
+      ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_empty[n & 1], ((uint32_t)(n >> 1) & 1u) ^ 1u, p.wait_budget) && !aborted(sm));
+      if (ok && elect_one()) {
+        mbar_arrive_tx(&sm.q_full[n & 1], kTile);
+        for (int k = 0; k < 2; ++k)
+          tma_load_4d(sm.q[n & 1] + k * kBox, &tmq, 64 * k, g * p.G, i_lo + n * (kRows / p.G), b, &sm.q_full[n & 1]);
+      }
+      __syncwarp();
+    }
+    if (!ok && lane == 0) set_abort(p, sm);
+    if (!ok) --n;
+    // No copy of this CTA may still be landing when it exits.
+    for (int x = n > 2 ? n - 2 : 0; x < n; ++x) mbar_wait(&sm.q_full[x & 1], (uint32_t)(x >> 1) & 1u, p.wait_budget);
+  } else if (warp == 1) {
+    // ================================================================ MMA issuer
+    const uint64_t dk = desc_kmajor_sw128(smem_addr(sm.k)), dq = desc_kmajor_sw128(smem_addr(sm.q[0]));
+    bool ok = true;
+    for (int n = 0; n < ntiles && ok; ++n) {
+      const int bf = n & 1;
+      const uint32_t par = (uint32_t)(n >> 1) & 1u;
+      ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full[bf], par, p.wait_budget) &&
+                                       mbar_wait(&sm.s_empty[bf], par ^ 1u, p.wait_budget) && !aborted(sm));
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t b0 = dq + (uint64_t)(bf * (int)(kTile >> 4));
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          const uint64_t off = (uint64_t)((ks >> 2) * 1024 + (ks & 3) * 2);
+          mma_f16_ss(tmem + bf * 128, dk + off, b0 + off, kIdS, ks > 0);
+        }
+        mma_commit(&sm.q_empty[bf]);
+        mma_commit(&sm.s_full[bf]);
+      }
+      __syncwarp();
+    }
+    if (!ok && lane == 0) set_abort(p, sm);
+    if (elect_one()) {   // every MMA has finished before tensor memory is freed
+      mma_commit(&sm.drain);
+      mbar_wait(&sm.drain, 0, p.wait_budget);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ================================================================ -lse of the rows, a tile ahead
+    const float* lse = p.lse + (long long)bg * p.S * p.G;
+    auto load = [&](int n, float* v) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = rows0 + n * kRows + 4 * lane + i;
+        v[i] = r < rows1 ? -lse[r] : 0.f;   // rows from rows1 on are masked
+      }
+    };
+    float next[4];
+    load(0, next);
+    bool ok = true;
+    for (int n = 0; n < ntiles && ok; ++n) {
+      float v[4] = {next[0], next[1], next[2], next[3]};
+      if (n + 1 < ntiles) load(n + 1, next);
+      ok = __all_sync(0xffffffffu, mbar_wait(&sm.nl_empty[n & 1], ((uint32_t)(n >> 1) & 1u) ^ 1u, p.wait_budget) && !aborted(sm));
+      if (!ok) break;
+      *reinterpret_cast<float4*>(&sm.nl[n & 1][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.nl_full[n & 1]);
+    }
+    if (!ok && lane == 0) set_abort(p, sm);
+  }
+  float sum = 0.f;
+  const int key = (warp & 3) * 32 + lane, j = j0 + key;   // softmax threads: tensor-memory lane = key
+  if (warp >= kSoftWarp0) {
+    // ================================================================ sums of one key
+    const int grp = (warp - kSoftWarp0) >> 2;
+    const uint32_t s_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16) + grp * 128;
+    const float ks = j < total ? p.ks[(long long)bg * p.nblk + (j >> p.bs_log2)] : 0.f;
+    const float kk = ks * p.scale * (CAP ? 1.f / p.softcap : kLog2e), c2 = p.softcap * kLog2e;
+    const float2 kk2 = make_float2(kk, kk);
+    // Rows [r_lo, r_hi) see the key.
+    const int r_lo = max(0, j - past) * p.G;
+    const int r_hi = j < total ? (p.window >= 0 ? min(rows1, (int)min((long long)(j - past) + p.window + 1, (long long)fresh) * p.G) : rows1) : 0;
+    bool ok = true;
+    for (int n = grp; n < ntiles && ok; n += 2) {
+      const uint32_t par = (uint32_t)(n >> 1) & 1u;
+      ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[grp], par, p.wait_budget) &&
+                                       mbar_wait(&sm.nl_full[grp], par, p.wait_budget) && !aborted(sm));
+      if (!ok) break;
+      tc_fence_after();
+      const int r0 = rows0 + n * kRows;
+      const int lo = r_lo - r0, hi = r_hi - r0;   // visible columns [lo, hi)
+      const bool full = __all_sync(0xffffffffu, lo <= 0 && hi >= kRows);
+      float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < kRows / 32; ++c) {
+        uint32_t x[32];
+        tmem_ld32(s_addr + 32 * c, x);
+        tmem_ld_wait();
+        int mode = 0;
+        if constexpr (CAP) {
+          float a = 0.f;
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) a = fmax3(a, fabsf(__uint_as_float(x[e])), fabsf(__uint_as_float(x[e + 1])));
+          a *= kk;
+          mode = __all_sync(0xffffffffu, !(a > kCapLow)) ? 3 : __all_sync(0xffffffffu, !(a > kCapHigh)) ? 7 : 9;
+        }
+        auto add = [&](auto m) {
+          constexpr int MODE = decltype(m)::value;
+#pragma unroll
+          for (int e4 = 0; e4 < 32; e4 += 4) {
+            const float4 nl = *reinterpret_cast<const float4*>(&sm.nl[grp][32 * c + e4]);
+            const float nv[4] = {nl.x, nl.y, nl.z, nl.w};
+#pragma unroll
+            for (int e = e4; e < e4 + 4; e += 2) {
+              const float2 x2 = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+              const float2 n2 = make_float2(nv[e - e4], nv[e - e4 + 1]);
+              float2 arg;
+              if constexpr (MODE == 0) {
+                arg = ffma2(x2, kk2, n2);
+              } else {
+                const float2 u = ffma2(x2, kk2, make_float2(0.f, 0.f));
+                if constexpr (MODE == 9) {
+                  const float2 y = cap_any(u, c2);
+                  arg = make_float2(y.x + n2.x, y.y + n2.y);
+                } else {
+                  const float2 z = ffma2(u, u, make_float2(0.f, 0.f));
+                  const float2 uc = ffma2(u, make_float2(c2, c2), make_float2(0.f, 0.f));
+                  arg = ffma2(uc, cap_fit<MODE>(z), n2);
+                }
+              }
+              if (!full) {
+                arg.x = 32 * c + e >= lo && 32 * c + e < hi ? arg.x : -INFINITY;
+                arg.y = 32 * c + e + 1 >= lo && 32 * c + e + 1 < hi ? arg.y : -INFINITY;
+              }
+              acc = ffma2(make_float2(ex2(arg.x), ex2(arg.y)), make_float2(1.f, 1.f), acc);
+            }
+          }
+        };
+        if constexpr (CAP) {
+          if (mode == 3) add(std::integral_constant<int, 3>());
+          else if (mode == 7) add(std::integral_constant<int, 7>());
+          else add(std::integral_constant<int, 9>());
+        } else {
+          add(std::integral_constant<int, 0>());
+        }
+      }
+      sum += acc.x + acc.y;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sm.s_empty[grp]);
+        mbar_arrive(&sm.nl_empty[grp]);
+      }
+    }
+    if (!ok && lane == 0) set_abort(p, sm);
+    if (grp == 1) sm.part[key] = sum;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 256);
+  if (warp >= kSoftWarp0 && warp < kSoftWarp0 + 4 && j < total && !aborted(sm)) {
+    const long long at = (long long)bg * p.C + j;
+    p.present_w[at] = sum + sm.part[key] + (p.past_w && j < past ? p.past_w[at] : 0.f);
+  }
+}
+
+constexpr int kMaxDevices = 64;
+
+template <bool CAP>
+cudaError_t launch_one(const BlockParams& p, cudaStream_t st) {
+  static bool done[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  const int smem = (int)sizeof(WtSmem) + 1024;
+  if (!done[dev]) {
+    if ((e = cudaFuncSetAttribute(block_weights_tc_kernel<CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+      return e;
+    done[dev] = true;
+  }
+  CUtensorMap mq;
+  if ((e = encode_fp16_query_sw128(&mq, p.q, p.B, p.S, p.N, (uint32_t)p.G)) != cudaSuccess) return e;
+  const dim3 grid((unsigned)(p.B * p.Nkv), (unsigned)((p.T + kKeys - 1) / kKeys));
+  block_weights_tc_kernel<CAP><<<grid, kThreads, smem, st>>>(p, mq);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_block_weights_tc(const BlockParams& p, cudaStream_t st) {
+  return p.softcap > 0.f ? launch_one<true>(p, st) : launch_one<false>(p, st);
+}
+
+}  // namespace gqa

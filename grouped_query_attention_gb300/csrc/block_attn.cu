@@ -287,7 +287,9 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.status, GQA_DEVICE_BAD_SEQLEN_BIT);
   }
-  const long long units = all_units(p);
+  const long long units = all_units(p);   // lengths are older than the kernel ahead
+  dep_wait();
+  dep_launch();
   const long long u0 = units * worker / p.workers, u1 = units * (worker + 1) / p.workers;
   if (u0 >= u1) return;
   Walk ld, cp;
@@ -571,8 +573,6 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
 
 // ------------------------------------------------------------------ merge
 
-constexpr int kMergeThreads = 128;
-
 // Slots of the pieces of range (b, g, rt) in the split above: [first, first + n).
 __device__ __forceinline__ int pieces_of(const BlockParams& p, long long units, int b, int gr, int total, int fresh,
                                          int t0, int nt, long long before, long long* first) {
@@ -583,30 +583,6 @@ __device__ __forceinline__ int pieces_of(const BlockParams& p, long long units, 
   const long long w0 = ((base + lo + 1) * p.workers - 1) / units, w1 = ((base + hi) * p.workers - 1) / units;
   *first = w0 + (long long)b * p.Nkv * p.nrt + gr;
   return (int)(w1 - w0) + 1;
-}
-
-// Log2-domain maximum and sum of one row over its pieces and the sink.
-__device__ __forceinline__ void row_stats(const BlockParams& p, long long slot0, int n, int row, int head, float* m,
-                                          float* l) {
-  // one warp: lanes over the pieces
-  const int lane = threadIdx.x & 31;
-  float mm = kNegBig;
-  for (int i = lane; i < n; i += 32) mm = fmaxf(mm, p.part_ml[((slot0 + i) * p.rt_rows + row) * 2]);
-  for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-  float sink = kNegBig;
-  if (p.sink || p.smooth) {
-    sink = (p.sink ? load_t(p.sink, head, p.t_type) : 0.f) * kLog2e;
-    mm = fmaxf(mm, sink);
-  }
-  float ll = 0.f;
-  for (int i = lane; i < n; i += 32) {
-    const float2 v = *reinterpret_cast<const float2*>(p.part_ml + ((slot0 + i) * p.rt_rows + row) * 2);
-    ll += v.y * ex2(v.x - mm);
-  }
-  for (int o = 16; o; o >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, o);
-  if (p.sink || p.smooth) ll += ex2(sink - mm);
-  *m = mm;
-  *l = ll;
 }
 
 struct RangeInfo {
@@ -636,45 +612,81 @@ __device__ RangeInfo range_info(const BlockParams& p, int b, int gr) {
   return r;
 }
 
-// Blocks of kMergeThreads; blocks [0, rows) merge one query row each, the
-// others add the weights of 4 * kMergeThreads cache rows of one (b, g).
-template <typename T>
-__global__ void __launch_bounds__(kMergeThreads)
+constexpr int kMaxPieces = 152 * kWarps * 3 + 1;   // workers, at most
+
+// Maximum / sum of v over the THREADS threads of the block.
+template <int THREADS, bool MAX>
+__device__ __forceinline__ float block_reduce(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float x = __shfl_xor_sync(0xffffffffu, v, o);
+    v = MAX ? fmaxf(v, x) : v + x;
+  }
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = red[0];
+#pragma unroll
+  for (int i = 1; i < THREADS / 32; ++i) v = MAX ? fmaxf(v, red[i]) : v + red[i];
+  return v;
+}
+
+constexpr int kWeightKeys = 2048;   // cache rows of a weight block
+
+// Blocks [0, row_blocks) merge one query row each, the others add the weights
+// of kWeightKeys cache rows of one (b, g).
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS)
 block_merge_kernel(const BlockParams p, long long row_blocks, int weight_chunks) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  __shared__ float s_m, s_l;
-  __shared__ float4 acc[kMergeThreads];
+  __shared__ float red[THREADS / 32];
+  __shared__ float fac[kMaxPieces];
+  __shared__ float4 acc[THREADS];
+  // Every block waits for the attention kernel, also one without work: what
+  // follows on the stream waits for this kernel alone.
   if (blockIdx.x < row_blocks) {
     const int nrows = p.S * p.G;
     const int bg = (int)(blockIdx.x / nrows), r = (int)(blockIdx.x % nrows), b = bg / p.Nkv, g = bg % p.Nkv;
     int total, fresh;
-    if (!block_lengths(p, b, &total, &fresh)) return;
+    if (!block_lengths(p, b, &total, &fresh)) {
+      dep_wait();
+      return;
+    }
     const int i = r / p.G, h = g * p.G + r % p.G, rt = r / p.rt_rows, row = r % p.rt_rows;
     T* out = static_cast<T*>(p.out) + (((long long)b * p.S + i) * p.N + h) * p.H;
     const int q4 = p.H / 4;            // float4 columns, 4 .. 64
     if (i >= fresh) {
-      for (int d = tid; d < p.H; d += kMergeThreads) out[d] = T(0.f);
+      dep_wait();
+      for (int d = tid; d < p.H; d += THREADS) out[d] = T(0.f);
       return;
     }
     const RangeInfo ri = range_info(p, b, g * p.nrt + rt);
-    if (warp == 0) {
-      float m, l;
-      row_stats(p, ri.slot0, ri.n, row, h, &m, &l);
-      if (lane == 0) {
-        s_m = m;
-        s_l = l;
-        if (p.lse) p.lse[(long long)bg * nrows + r] = l > 0.f ? m + log2f(l) : INFINITY;
-      }
+    const bool has_sink = p.sink || p.smooth;
+    const float sink = has_sink ? (p.sink ? load_t(p.sink, h, p.t_type) : 0.f) * kLog2e : kNegBig;
+    dep_wait();
+    float m = sink;
+    for (int x = tid; x < ri.n; x += THREADS) {
+      fac[x] = p.part_ml[((ri.slot0 + x) * p.rt_rows + row) * 2];
+      m = fmaxf(m, fac[x]);
     }
-    __syncthreads();
-    const float m = s_m, l = s_l;
-    const int groups = kMergeThreads / q4, grp = tid / q4, c = tid % q4;
+    m = block_reduce<THREADS, true>(m, red);
+    float l = 0.f;
+    for (int x = tid; x < ri.n; x += THREADS) {
+      const float f = ex2(fac[x] - m);
+      fac[x] = f;
+      l = fmaf(p.part_ml[((ri.slot0 + x) * p.rt_rows + row) * 2 + 1], f, l);
+    }
+    l = block_reduce<THREADS, false>(l, red) + (has_sink ? ex2(sink - m) : 0.f);   // (fac is complete behind it)
+    if (p.lse && tid == 0) p.lse[(long long)bg * nrows + r] = l > 0.f ? m + log2f(l) : INFINITY;
+    const int groups = THREADS / q4, grp = tid / q4, c = tid % q4;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     if (grp < groups) {
+      const float* src = p.part_o + (ri.slot0 * p.rt_rows + row) * p.H + 4 * c;
+      const long long ld = (long long)p.rt_rows * p.H;
+#pragma unroll 4
       for (int x = grp; x < ri.n; x += groups) {
-        const long long slot = (ri.slot0 + x) * p.rt_rows + row;
-        const float f = ex2(p.part_ml[slot * 2] - m);
-        const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot * p.H + 4 * c);
+        const float f = fac[x];
+        const float4 v = *reinterpret_cast<const float4*>(src + x * ld);
         a.x = fmaf(v.x, f, a.x);
         a.y = fmaf(v.y, f, a.y);
         a.z = fmaf(v.z, f, a.z);
@@ -705,32 +717,52 @@ block_merge_kernel(const BlockParams p, long long row_blocks, int weight_chunks)
   const long long x = blockIdx.x - row_blocks;
   const int bg = (int)(x / weight_chunks), chunk = (int)(x % weight_chunks), b = bg / p.Nkv, g = bg % p.Nkv;
   int total, fresh;
-  if (!block_lengths(p, b, &total, &fresh)) return;
-  const int j0 = chunk * 4 * kMergeThreads;
-  if (j0 >= total) return;
-  __shared__ float lse[16];
-  const int nrows = fresh * p.G;   // live rows (at most one row tile)
-  if (nrows > 0) {
-    const RangeInfo ri = range_info(p, b, g);
-    for (int r = warp; r < nrows; r += kMergeThreads / 32) {
-      float m, l;
-      row_stats(p, ri.slot0, ri.n, r, g * p.G + r % p.G, &m, &l);
-      if (lane == 0) lse[r] = m + log2f(l);
+  const int j0 = chunk * kWeightKeys;
+  if (!block_lengths(p, b, &total, &fresh) || j0 >= total) {
+    dep_wait();
+    return;
+  }
+  __shared__ float nl[16];                       // -lse of the rows
+  const int nrows = fresh * p.G, rs = p.stash_rows;   // live rows (at most one row tile)
+  const RangeInfo ri = range_info(p, b, g);
+  dep_wait();
+  for (int r = warp; r < nrows; r += THREADS / 32) {   // a warp per row, lanes over the pieces
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + ri.slot0 * p.rt_rows + r;
+    const bool has_sink = p.sink || p.smooth;
+    const float sink = has_sink ? (p.sink ? load_t(p.sink, g * p.G + r % p.G, p.t_type) : 0.f) * kLog2e : kNegBig;
+    float m = sink, l = 0.f;
+    for (int i = lane; i < ri.n; i += 32) m = fmaxf(m, ml[(long long)i * p.rt_rows].x);
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int i = lane; i < ri.n; i += 32) {
+      const float2 v = ml[(long long)i * p.rt_rows];
+      l = fmaf(v.y, ex2(v.x - m), l);
     }
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (has_sink) l += ex2(sink - m);
+    if (lane == 0) nl[r] = -(m + log2f(l));
   }
   __syncthreads();
   int t0, nt;
   units_of(p, total, fresh, &t0, &nt);
-  for (int k = 0; k < 4; ++k) {
-    const int j = j0 + k * kMergeThreads + tid;
+  const long long at0 = (long long)bg * p.C;
+  const float* st = p.stash + (long long)bg * p.stash_ld * rs;
+#pragma unroll 4
+  for (int k = 0; k < kWeightKeys / THREADS; ++k) {
+    const int j = j0 + k * THREADS + tid;
     if (j >= total) break;
-    const long long at = (long long)bg * p.C + j;
-    float w = 0.f;
-    if (j >= t0 * kBlockUnit)
-      for (int r = 0; r < nrows; ++r)
-        w += ex2(p.stash[((long long)bg * p.stash_ld + j) * p.stash_rows + r] - lse[r]);
-    if (p.past_w && j < total - fresh) w += p.past_w[at];
-    p.present_w[at] = w;
+    float w = p.past_w && j < total - fresh ? p.past_w[at0 + j] : 0.f;
+    if (j >= t0 * kBlockUnit) {
+      const float* sj = st + (long long)j * rs;
+      int r = 0;
+      if ((rs & 3) == 0) {
+        for (; r + 4 <= nrows; r += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(sj + r);
+          w += (ex2(v.x + nl[r]) + ex2(v.y + nl[r + 1])) + (ex2(v.z + nl[r + 2]) + ex2(v.w + nl[r + 3]));
+        }
+      }
+      for (; r < nrows; ++r) w += ex2(sj[r] + nl[r]);
+    }
+    p.present_w[at0 + j] = w;
   }
 }
 
@@ -901,8 +933,8 @@ cudaError_t attn_one(const BlockParams& p, cudaStream_t st) {
   const uint64_t rows = (uint64_t)p.B * p.Nkv * p.C;
   if ((e = encode_codes(&mk, p.kc, rows, p.H, HP, kBlockUnit)) != cudaSuccess) return e;
   if ((e = encode_codes(&mv, p.vc, rows, p.H, HP, kBlockUnit)) != cudaSuccess) return e;
-  block_attn_kernel<T, HP, NT, PLAIN><<<(unsigned)(p.workers / kWarps), kWarps * 32, smem, st>>>(p, mk, mv);
-  return cudaGetLastError();
+  return launch_dependent(p.k != nullptr, block_attn_kernel<T, HP, NT, PLAIN>, dim3((unsigned)(p.workers / kWarps)),
+                          kWarps * 32, (size_t)smem, st, p, mk, mv);
 }
 
 template <typename T, int HP, int NT>
@@ -954,14 +986,17 @@ cudaError_t launch_block_attn(const BlockParams& p, cudaStream_t st) {
 
 cudaError_t launch_block_merge(const BlockParams& p, cudaStream_t st) {
   const long long rows = (long long)p.B * p.Nkv * p.S * p.G;
-  const int chunks = p.stash ? (p.T + 4 * kMergeThreads - 1) / (4 * kMergeThreads) : 0;
+  const int chunks = p.stash ? (p.T + kWeightKeys - 1) / kWeightKeys : 0;
   const long long blocks = rows + (long long)p.B * p.Nkv * chunks;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  // A row of a long split has many pieces: more threads read them at once.
+  const bool many = p.workers / ((long long)p.B * p.Nkv * p.nrt) >= 64;
+  const dim3 grid((unsigned)blocks);
   if (p.t_type == kF16)
-    block_merge_kernel<__half><<<(unsigned)blocks, kMergeThreads, 0, st>>>(p, rows, chunks);
-  else
-    block_merge_kernel<float><<<(unsigned)blocks, kMergeThreads, 0, st>>>(p, rows, chunks);
-  return cudaGetLastError();
+    return many ? launch_dependent(true, block_merge_kernel<__half, 512>, grid, 512, 0, st, p, rows, chunks)
+                : launch_dependent(true, block_merge_kernel<__half, 128>, grid, 128, 0, st, p, rows, chunks);
+  return many ? launch_dependent(true, block_merge_kernel<float, 512>, grid, 512, 0, st, p, rows, chunks)
+              : launch_dependent(true, block_merge_kernel<float, 128>, grid, 128, 0, st, p, rows, chunks);
 }
 
 cudaError_t launch_block_weights(const BlockParams& p, cudaStream_t st) {

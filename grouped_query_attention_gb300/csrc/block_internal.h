@@ -64,6 +64,25 @@ __host__ __device__ inline bool block_lengths(const BlockParams& p, int b, int* 
   return *total >= 0 && *total <= p.T && *fresh >= 0 && *fresh <= p.S && *fresh <= *total;
 }
 
+// Launch that may start before the kernel ahead of it on the stream has
+// finished (`early`): it calls dep_wait() before it touches what that one
+// writes. What the kernels before those two wrote is complete by then, as the
+// one ahead began after them or waited for them before it let this one start.
+template <typename K, typename... A>
+cudaError_t launch_dependent(bool early, K kern, dim3 grid, unsigned threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 cudaError_t launch_block_append(const BlockParams& p, cudaStream_t st);
 // Split-KV attention on warp MMAs, every shape.
 constexpr int kBlockUnit = 32;      // keys per work unit

@@ -189,6 +189,7 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
   // ---- block-uniform checks before any barrier or tensor memory
   int total, fresh;
   if (!block_lengths(p, b, &total, &fresh)) {
+    dep_wait();   // also without work: what follows on the stream waits for this kernel alone
     if (qb == nqb - 1 && g == 0 && tid == 0 && p.status) atomicOr(p.status, GQA_DEVICE_BAD_SEQLEN_BIT);
     return;
   }
@@ -197,6 +198,7 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
   const int i_lo = r0 / p.G;
   const int i_hi = min((min(r0 + 2 * kBM, nrows) - 1) / p.G, fresh - 1);
   if (i_lo > i_hi) {   // padding rows only
+    dep_wait();
     for (int x = tid; x < 2 * kBM * kHD; x += kThreads) {
       const int r = r0 + x / kHD, d = x % kHD;
       if (r < nrows)
@@ -246,6 +248,8 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
     }
   }
   __syncwarp();
+  dep_wait();   // the cache is complete (queries and lengths are older than the kernel ahead)
+  dep_launch();
   {   // the largest V scale of the keys
     const float* vs = p.vs + (long long)bg * p.nblk;
     const int b1 = (kmax - 1) >> p.bs_log2;
@@ -751,8 +755,8 @@ cudaError_t launch_one(const BlockParams& p, cudaStream_t st) {
   if ((e = encode(&mq, p.q, p.B, p.S, p.N, (uint32_t)p.G)) != cudaSuccess) return e;
   if ((e = encode(&mo, p.out, p.B, p.S, p.N, (uint32_t)p.G)) != cudaSuccess) return e;
   const unsigned nqb = (unsigned)((p.S * p.G + 2 * kBM - 1) / (2 * kBM)), nbg = (unsigned)(p.B * p.Nkv);
-  kern<<<p.qb_major ? dim3(nbg, nqb) : dim3(nqb, nbg), kThreads, smem, st>>>(p, mq, mo, mk, mv);
-  return cudaGetLastError();
+  return launch_dependent(p.k != nullptr, kern, p.qb_major ? dim3(nbg, nqb) : dim3(nqb, nbg), kThreads, (size_t)smem, st,
+                          p, mq, mo, mk, mv);
 }
 
 }  // namespace

@@ -62,6 +62,7 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int bg = blockIdx.x, b = bg / p.Nkv, g = bg % p.Nkv;
   int total, fresh;
+  dep_wait();   // every block: what follows on the stream waits for this kernel alone
   if (!block_lengths(p, b, &total, &fresh)) return;
   const int j0 = (int)blockIdx.y * kKeys;
   if (j0 >= total) return;
@@ -289,8 +290,7 @@ cudaError_t launch_one(const BlockParams& p, cudaStream_t st) {
   CUtensorMap mq;
   if ((e = encode_fp16_query_sw128(&mq, p.q, p.B, p.S, p.N, (uint32_t)p.G)) != cudaSuccess) return e;
   const dim3 grid((unsigned)(p.B * p.Nkv), (unsigned)((p.T + kKeys - 1) / kKeys));
-  block_weights_tc_kernel<CAP><<<grid, kThreads, smem, st>>>(p, mq);
-  return cudaGetLastError();
+  return launch_dependent(true, block_weights_tc_kernel<CAP>, grid, kThreads, (size_t)smem, st, p, mq);
 }
 
 }  // namespace

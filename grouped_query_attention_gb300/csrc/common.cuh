@@ -25,6 +25,11 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Programmatic dependent launch: wait until the kernel ahead on the stream has
+// completed (and its writes are visible); allow the next one to start.
+__device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ void flag_status(const Params& p, unsigned int bit) {
   atomicOr(p.status, bit);
 }

@@ -631,13 +631,11 @@ __device__ __forceinline__ float block_reduce(float v, float* red) {
   return v;
 }
 
-constexpr int kWeightKeys = 2048;   // cache rows of a weight block
-
 // Blocks [0, row_blocks) merge one query row each, the others add the weights
-// of kWeightKeys cache rows of one (b, g).
+// of `keys` cache rows of one (b, g).
 template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS)
-block_merge_kernel(const BlockParams p, long long row_blocks, int weight_chunks) {
+block_merge_kernel(const BlockParams p, long long row_blocks, int weight_chunks, int keys) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   __shared__ float red[THREADS / 32];
   __shared__ float fac[kMaxPieces];
@@ -717,7 +715,7 @@ block_merge_kernel(const BlockParams p, long long row_blocks, int weight_chunks)
   const long long x = blockIdx.x - row_blocks;
   const int bg = (int)(x / weight_chunks), chunk = (int)(x % weight_chunks), b = bg / p.Nkv, g = bg % p.Nkv;
   int total, fresh;
-  const int j0 = chunk * kWeightKeys;
+  const int j0 = chunk * keys;
   if (!block_lengths(p, b, &total, &fresh) || j0 >= total) {
     dep_wait();
     return;
@@ -747,7 +745,7 @@ block_merge_kernel(const BlockParams p, long long row_blocks, int weight_chunks)
   const long long at0 = (long long)bg * p.C;
   const float* st = p.stash + (long long)bg * p.stash_ld * rs;
 #pragma unroll 4
-  for (int k = 0; k < kWeightKeys / THREADS; ++k) {
+  for (int k = 0; k < keys / THREADS; ++k) {
     const int j = j0 + k * THREADS + tid;
     if (j >= total) break;
     float w = p.past_w && j < total - fresh ? p.past_w[at0 + j] : 0.f;
@@ -986,17 +984,20 @@ cudaError_t launch_block_attn(const BlockParams& p, cudaStream_t st) {
 
 cudaError_t launch_block_merge(const BlockParams& p, cudaStream_t st) {
   const long long rows = (long long)p.B * p.Nkv * p.S * p.G;
-  const int chunks = p.stash ? (p.T + kWeightKeys - 1) / kWeightKeys : 0;
+  // Cache rows of a weight block: every block first adds up the rows' sums, so
+  // 2048 where that still leaves the SMs several blocks each, else 512.
+  const int keys = (long long)p.B * p.Nkv * p.T >= 152LL * 4 * 2048 ? 2048 : 512;
+  const int chunks = p.stash ? (p.T + keys - 1) / keys : 0;
   const long long blocks = rows + (long long)p.B * p.Nkv * chunks;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   // A row of a long split has many pieces: more threads read them at once.
   const bool many = p.workers / ((long long)p.B * p.Nkv * p.nrt) >= 64;
   const dim3 grid((unsigned)blocks);
   if (p.t_type == kF16)
-    return many ? launch_dependent(true, block_merge_kernel<__half, 512>, grid, 512, 0, st, p, rows, chunks)
-                : launch_dependent(true, block_merge_kernel<__half, 128>, grid, 128, 0, st, p, rows, chunks);
-  return many ? launch_dependent(true, block_merge_kernel<float, 512>, grid, 512, 0, st, p, rows, chunks)
-              : launch_dependent(true, block_merge_kernel<float, 128>, grid, 128, 0, st, p, rows, chunks);
+    return many ? launch_dependent(true, block_merge_kernel<__half, 512>, grid, 512, 0, st, p, rows, chunks, keys)
+                : launch_dependent(true, block_merge_kernel<__half, 128>, grid, 128, 0, st, p, rows, chunks, keys);
+  return many ? launch_dependent(true, block_merge_kernel<float, 512>, grid, 512, 0, st, p, rows, chunks, keys)
+              : launch_dependent(true, block_merge_kernel<float, 128>, grid, 128, 0, st, p, rows, chunks, keys);
 }
 
 cudaError_t launch_block_weights(const BlockParams& p, cudaStream_t st) {

@@ -187,7 +187,8 @@ __device__ __forceinline__ unsigned weight_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-constexpr int kSelCache = 8192;   // rows of a CTA whose keys stay in shared memory
+constexpr int kSelCache = 16384;   // rows of a CTA whose keys stay in shared memory
+constexpr int kSelRows = 4096;     // rows a CTA is given before the cluster grows
 
 // One (b, g) per cluster of CL CTAs, each with an equal slice of the rows
 // between `first` and `recent`. A radix selection (four passes of eight bits
@@ -240,10 +241,16 @@ evict_select_kernel(const EvictParams p, int CL) {
       const int i = i0 + tid;
       const unsigned key = i < n ? key_at(i) : 0u;
       const bool in = i < n && (key & mask) == prefix;
-      // lanes with the same digit count as one (the top digits of attention weights hardly differ)
-      const unsigned digit = in ? (key >> shift) & 255u : 256u;
-      const unsigned same = __match_any_sync(0xffffffffu, digit);
-      if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+      const unsigned digit = (key >> shift) & 255u;
+      const unsigned ins = __ballot_sync(0xffffffffu, in);
+      if (ins == 0) continue;
+      // a warp whose digits are all the same (top digits, ties) counts them as one
+      const unsigned first = __shfl_sync(0xffffffffu, digit, __ffs(ins) - 1);
+      if (__all_sync(0xffffffffu, !in || digit == first)) {
+        if (lane == 0) atomicAdd(&hist[first], __popc(ins));
+      } else if (in) {
+        atomicAdd(&hist[digit], 1);
+      }
     }
     if (CL > 1) cluster.sync(); else __syncthreads();
     if (tid < 256) {
@@ -344,12 +351,14 @@ evict_select_kernel(const EvictParams p, int CL) {
 
 // ------------------------------------------------------------------ eviction: the copy
 
-constexpr int kGatherThreads = 256;
+constexpr int kGatherThreads = 128;
+constexpr int kGatherAhead = 4;   // 16-byte chunks a thread has in flight before the scales are known
 
 // One block of tokens of one (b, g) of the new cache, K (z = 0) or V (z = 1):
 // the largest source scale of its rows, then every row's codes, 16 at a time,
 // rounded anew where the row's own scale is smaller. One read and one write of
-// each kept row; the bound is HBM.
+// each kept row; the bound is HBM, latency first: a thread's first code chunks
+// are requested together with the scales, not behind them.
 __global__ void __launch_bounds__(kGatherThreads)
 evict_gather_kernel(const EvictParams p) {
   const int bg = blockIdx.y, b = bg / p.Nkv, tid = threadIdx.x;
@@ -363,15 +372,23 @@ evict_gather_kernel(const EvictParams p) {
   const int8_t* from = (isv ? p.vc : p.kc) + (long long)bg * p.C * p.H;
   const float* sc = (isv ? p.vs : p.ks) + (long long)bg * p.nblk;
   int8_t* to = (isv ? p.vc_to : p.kc_to) + ((long long)bg * p.Cto + first) * p.H;
-  __shared__ int row[256];
   __shared__ float rs[256];
   __shared__ float red[kGatherThreads / 32];
+  const int* rows = p.kept + (long long)bg * p.keep + first;
+  const int chunks = p.H / 16;
+  uint4 ahead[kGatherAhead];
+#pragma unroll
+  for (int k = 0; k < kGatherAhead; ++k) {
+    const int i = k * kGatherThreads + tid;
+    if (i < n * chunks)
+      ahead[k] = *reinterpret_cast<const uint4*>(from + (long long)rows[i / chunks] * p.H + 16 * (i % chunks));
+  }
   float top = 0.f;
-  if (tid < n) {
-    const int r = p.kept[(long long)bg * p.keep + first + tid];
-    row[tid] = r;
-    rs[tid] = top = sc[r >> p.bs_log2];
-    if (!isv && p.w_to) p.w_to[(long long)bg * p.Cto + first + tid] = p.w[(long long)bg * p.C + r];
+  for (int i = tid; i < n; i += kGatherThreads) {
+    const int r = rows[i];
+    rs[i] = sc[r >> p.bs_log2];
+    top = fmaxf(top, rs[i]);
+    if (!isv && p.w_to) p.w_to[(long long)bg * p.Cto + first + i] = p.w[(long long)bg * p.C + r];
   }
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if ((tid & 31) == 0) red[tid >> 5] = top;
@@ -379,10 +396,8 @@ evict_gather_kernel(const EvictParams p) {
   top = red[0];
   for (int i = 1; i < kGatherThreads / 32; ++i) top = fmaxf(top, red[i]);
   if (tid == 0) (isv ? p.vs_to : p.ks_to)[(long long)bg * p.nblk_to + blockIdx.x] = top;
-  const int chunks = p.H / 16;
-  for (int i = tid; i < n * chunks; i += kGatherThreads) {
+  auto put = [&](int i, uint4 w) {
     const int r = i / chunks, c = i - r * chunks;
-    uint4 w = *reinterpret_cast<const uint4*>(from + (long long)row[r] * p.H + 16 * c);
     const float s = rs[r];
     if (s != top) {
       const float ratio = top > 0.f ? __fdiv_rn(s, top) : 0.f;
@@ -390,7 +405,14 @@ evict_gather_kernel(const EvictParams p) {
                      recode4(w.w, s, top, ratio));
     }
     *reinterpret_cast<uint4*>(to + (long long)r * p.H + 16 * c) = w;
+  };
+#pragma unroll
+  for (int k = 0; k < kGatherAhead; ++k) {
+    const int i = k * kGatherThreads + tid;
+    if (i < n * chunks) put(i, ahead[k]);
   }
+  for (int i = kGatherAhead * kGatherThreads + tid; i < n * chunks; i += kGatherThreads)
+    put(i, *reinterpret_cast<const uint4*>(from + (long long)rows[i / chunks] * p.H + 16 * (i % chunks)));
 }
 
 }  // namespace
@@ -406,10 +428,21 @@ cudaError_t launch_block_append(const BlockParams& p, cudaStream_t st) {
 }
 
 cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t st) {
-  // A CTA for every kSelCache rows, up to the portable cluster size.
+  // A CTA for every kSelRows rows, up to the portable cluster size.
   int CL = 1;
-  while (CL < 8 && (long long)CL * kSelCache < p.T) CL *= 2;
-  const size_t smem = kSelCache * sizeof(unsigned);   // 32 KB: within the default limit
+  while (CL < 8 && (long long)CL * kSelRows < p.T) CL *= 2;
+  const long long per = ((p.T + CL - 1) / CL + 31) & ~31LL;
+  const size_t smem = (size_t)(per < kSelCache ? per : kSelCache) * sizeof(unsigned);
+  static bool done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!done[dev]) {
+    e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCache * (int)sizeof(unsigned));
+    if (e != cudaSuccess) return e;
+    done[dev] = true;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.B * p.Nkv * CL));
   cfg.blockDim = dim3(kSelThreads);

@@ -559,7 +559,7 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
       mt *= k_row;
       ua *= k_row;
       if constexpr (CAP) {
-        if (mt > kNegBig) mt = cap_any(make_float2(mt, mt), c2).x;
+        if (mt > kNegBig) mt = cap_far(mt, c2);   // a reference: any rounding serves
       }
       // Lazy rescale: O_q holds P.V up to the last step once that is done.
       const bool grow = mt > m_run + kLazy;
@@ -628,8 +628,7 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
                     }
                   } else {
                     const float2 z = ffma2(u, u, make_float2(0.f, 0.f));
-                    const float2 uc = ffma2(u, make_float2(c2, c2), make_float2(0.f, 0.f));
-                    arg = ffma2(uc, cap_fit<MODE>(z), cc2);
+                    arg = ffma2(u, cap_fit<MODE>(z, c2), cc2);
                   }
                 }
                 const float pa = ex2(arg.x), pb = ex2(arg.y);
@@ -650,9 +649,10 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
         }
       };
       if constexpr (CAP) {
-        if (__all_sync(0xffffffffu, !(ua > kCapLow)))
+        const unsigned um = __reduce_max_sync(0xffffffffu, __float_as_uint(ua));   // ua >= 0: ordered as integers
+        if (um <= __float_as_uint(kCapLow))
           exponents(std::integral_constant<int, 3>());
-        else if (__all_sync(0xffffffffu, !(ua > kCapHigh)))
+        else if (um <= __float_as_uint(kCapHigh))
           exponents(std::integral_constant<int, 7>());
         else
           exponents(std::integral_constant<int, 9>());

@@ -33,12 +33,13 @@ __device__ constexpr float kFit3[4] = {0.9999999403953552f, -0.3333241641521454f
 __device__ constexpr float kFit7[8] = {1.0f, -0.33333274722099304f, 0.13332107663154602f, -0.05386783555150032f,
                                        0.021456174552440643f, -0.00790493842214346f, 0.0022732384968549013f,
                                        -0.0003508012741804123f};
+// c2 Q(z): the coefficients times c2 are loop constants of the caller.
 template <int DEG>
-__device__ __forceinline__ float2 cap_fit(float2 z) {
+__device__ __forceinline__ float2 cap_fit(float2 z, float c2) {
   constexpr const float* q = DEG == 3 ? kFit3 : kFit7;
-  float2 y = make_float2(q[DEG], q[DEG]);
+  float2 y = make_float2(q[DEG] * c2, q[DEG] * c2);
 #pragma unroll
-  for (int i = DEG - 1; i >= 0; --i) y = ffma2(y, z, make_float2(q[i], q[i]));
+  for (int i = DEG - 1; i >= 0; --i) y = ffma2(y, z, make_float2(q[i] * c2, q[i] * c2));
   return y;
 }
 __device__ __forceinline__ float cap_far(float u, float c2) {
@@ -49,11 +50,11 @@ __device__ __forceinline__ float cap_far(float u, float c2) {
 // Both forms computed, one selected (no branch).
 __device__ __forceinline__ float2 cap_any(float2 u, float c2) {
   const float2 z = ffma2(u, u, make_float2(0.f, 0.f));
-  const float2 y = ffma2(u, cap_fit<7>(z), make_float2(0.f, 0.f));
+  const float2 y = ffma2(u, cap_fit<7>(z, c2), make_float2(0.f, 0.f));
   const float fx = cap_far(u.x, c2), fy = cap_far(u.y, c2);
   float2 r;
-  asm("{ .reg .pred p; setp.le.f32 p, %1, %2; selp.f32 %0, %3, %4, p; }" : "=f"(r.x) : "f"(z.x), "f"(kCapHigh), "f"(y.x * c2), "f"(fx));
-  asm("{ .reg .pred p; setp.le.f32 p, %1, %2; selp.f32 %0, %3, %4, p; }" : "=f"(r.y) : "f"(z.y), "f"(kCapHigh), "f"(y.y * c2), "f"(fy));
+  asm("{ .reg .pred p; setp.le.f32 p, %1, %2; selp.f32 %0, %3, %4, p; }" : "=f"(r.x) : "f"(z.x), "f"(kCapHigh), "f"(y.x), "f"(fx));
+  asm("{ .reg .pred p; setp.le.f32 p, %1, %2; selp.f32 %0, %3, %4, p; }" : "=f"(r.y) : "f"(z.y), "f"(kCapHigh), "f"(y.y), "f"(fy));
   return r;
 }
 

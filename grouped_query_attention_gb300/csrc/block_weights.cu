@@ -232,8 +232,7 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
                   arg = make_float2(y.x + n2.x, y.y + n2.y);
                 } else {
                   const float2 z = ffma2(u, u, make_float2(0.f, 0.f));
-                  const float2 uc = ffma2(u, make_float2(c2, c2), make_float2(0.f, 0.f));
-                  arg = ffma2(uc, cap_fit<MODE>(z), n2);
+                  arg = ffma2(u, cap_fit<MODE>(z, c2), n2);
                 }
               }
               if (!full) {

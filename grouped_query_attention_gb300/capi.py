@@ -245,7 +245,9 @@ def gqa_set_wait_limit(handle, cycles: int, withhold_copy: int = -1) -> None:
 
 
 def gqa_rotary_axes(handle, inputs: GqaRotaryInputs, outputs: GqaRotaryOutputs, status: int, stream: int) -> None:
-    _check(load_library().gqa_rotary_axes(handle, inputs, outputs, status, stream))
+    st = (_lib or load_library()).gqa_rotary_axes(handle, inputs, outputs, status, stream)
+    if st != GQA_OK:
+        _check(st)
 
 
 def gqa_block_workspace_size(handle, cache: GqaBlockCache, inputs: GqaBlockInputs, outputs: GqaBlockOutputs) -> int:
@@ -256,11 +258,15 @@ def gqa_block_workspace_size(handle, cache: GqaBlockCache, inputs: GqaBlockInput
 
 def gqa_block_forward(handle, cache: GqaBlockCache, inputs: GqaBlockInputs, outputs: GqaBlockOutputs, workspace: int,
                       workspace_bytes: int, status: int, stream: int) -> None:
-    _check(load_library().gqa_block_forward(handle, cache, inputs, outputs, workspace, workspace_bytes, status, stream))
+    st = (_lib or load_library()).gqa_block_forward(handle, cache, inputs, outputs, workspace, workspace_bytes, status, stream)
+    if st != GQA_OK:
+        _check(st)
 
 
 def gqa_block_evict(handle, args: GqaEvictArgs, status: int, stream: int) -> None:
-    _check(load_library().gqa_block_evict(handle, args, status, stream))
+    st = (_lib or load_library()).gqa_block_evict(handle, args, status, stream)
+    if st != GQA_OK:
+        _check(st)
 
 
 def gqa_destroy(handle) -> None:

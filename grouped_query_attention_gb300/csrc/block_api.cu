@@ -220,7 +220,7 @@ gqa_status plan_block(const gqa_handle* h, const gqa_block_cache* cache, const g
     P.workers = gqa::block_workers(P);
     const size_t slots = (size_t)P.workers + (size_t)(B * Nkv) * P.nrt;
     pl->part_o = align_up(slots * P.rt_rows * H * sizeof(float));
-    pl->part_ml = align_up(slots * P.rt_rows * 2 * sizeof(float));
+    pl->part_ml = align_up(slots * P.rt_rows * 4 * sizeof(float));   // m, l, l of the rounded probabilities, -
   }
   if (P.present_w) {
     if (!pl->prefill && P.nrt == 1) {

@@ -328,6 +328,7 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
   uint2 qf[NT * kParts][kSteps];
   float o[kSteps][NT][4];       // O^T: coordinates gq HP/8 + 2 i (0, 1) and + 1 (2, 3), rows 2 t (0, 2) and + 1 (1, 3)
   float m[NT][2], l[NT][2], mul[NT][2];   // of rows 8 n + 2 t, + 1
+  float lr[kHalf ? NT : 1][2];            // fp16: the sum of the probabilities as the product with V has them
   int wexp = -200;              // the V scales enter as vs 2^-wexp
   bool fresh_piece = true;
   int stage = 0;
@@ -349,6 +350,7 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
           mul[n][h] = p.softcap > 0.f ? f : f * kLog2e;
           m[n][h] = kNegBig;
           l[n][h] = 0.f;
+          if (kHalf) lr[n][h] = 0.f;
         }
 #pragma unroll
       for (int i = 0; i < kSteps; ++i)
@@ -468,6 +470,7 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
           const float e = ex2(m[n][h] - mn);
           m[n][h] = mn;
           l[n][h] *= e;
+          if (kHalf) lr[n][h] *= e;
           f[h] = e * fw;
         }
 #pragma unroll
@@ -484,6 +487,12 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       const float vm = vsc[kk] * down;
+      // fp16: dividing the output by the sum of the rounded probabilities takes
+      // the common part of their roundings out (the dominant key's own most of
+      // all). Blocks of far smaller values keep the exact ones: theirs may
+      // round to nothing.
+      const bool rounded = kHalf && vm > 0.125f;
+      const float ivm = rounded ? __frcp_rn(vm) : 1.f;
       uint32_t pb[NT * kParts][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -495,7 +504,11 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
           const float x0 = p0 * vm, x1 = p1 * vm;
           const uint32_t hi = pack(x0, x1);
           pb[n][x] = transpose8(hi);
-          if constexpr (!kHalf) {
+          if constexpr (kHalf) {
+            const float2 r = unpack(hi);
+            lr[n][0] = fmaf(rounded ? r.x : p0, ivm, lr[n][0]);
+            lr[n][1] = fmaf(rounded ? r.y : p1, ivm, lr[n][1]);
+          } else {
             const float2 h2 = unpack(hi);
             pb[NT + n][x] = transpose8(pack(x0 - h2.x, x1 - h2.y));
           }
@@ -551,13 +564,16 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float sum = l[n][h];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        float sum = l[n][h], sr = kHalf ? lr[n][h] : 0.f;
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          sum += __shfl_xor_sync(0xffffffffu, sum, x);
+          if (kHalf) sr += __shfl_xor_sync(0xffffffffu, sr, x);
+        }
         const int row = 8 * n + 2 * t + h;
         if (r0 + row >= p.S * p.G) continue;
-        if (gq == 0) *reinterpret_cast<float2*>(p.part_ml + (slot * p.rt_rows + row) * 2) = make_float2(m[n][h], sum);
+        if (gq == 0)
+          *reinterpret_cast<float4*>(p.part_ml + (slot * p.rt_rows + row) * 4) = make_float4(m[n][h], sum, kHalf ? sr : sum, 0.f);
         float* dst = p.part_o + (slot * p.rt_rows + row) * p.H;
 #pragma unroll
         for (int i = 0; i < kSteps; i += 2) {
@@ -664,18 +680,24 @@ block_merge_kernel(const BlockParams p, long long row_blocks, int weight_chunks,
     dep_wait();
     float m = sink;
     for (int x = tid; x < ri.n; x += THREADS) {
-      fac[x] = p.part_ml[((ri.slot0 + x) * p.rt_rows + row) * 2];
+      fac[x] = p.part_ml[((ri.slot0 + x) * p.rt_rows + row) * 4];
       m = fmaxf(m, fac[x]);
     }
     m = block_reduce<THREADS, true>(m, red);
-    float l = 0.f;
+    float l = 0.f, lr = 0.f;
     for (int x = tid; x < ri.n; x += THREADS) {
       const float f = ex2(fac[x] - m);
       fac[x] = f;
-      l = fmaf(p.part_ml[((ri.slot0 + x) * p.rt_rows + row) * 2 + 1], f, l);
+      const float4 v = *reinterpret_cast<const float4*>(p.part_ml + ((ri.slot0 + x) * p.rt_rows + row) * 4);
+      l = fmaf(v.y, f, l);
+      lr = fmaf(v.z, f, lr);
     }
-    l = block_reduce<THREADS, false>(l, red) + (has_sink ? ex2(sink - m) : 0.f);   // (fac is complete behind it)
-    if (p.lse && tid == 0) p.lse[(long long)bg * nrows + r] = l > 0.f ? m + log2f(l) : INFINITY;
+    const float extra = has_sink ? ex2(sink - m) : 0.f;
+    if (p.lse) {
+      l = block_reduce<THREADS, false>(l, red) + extra;
+      if (tid == 0) p.lse[(long long)bg * nrows + r] = l > 0.f ? m + log2f(l) : INFINITY;
+    }
+    l = block_reduce<THREADS, false>(lr, red) + extra;   // (fac is complete behind it)
     const int groups = THREADS / q4, grp = tid / q4, c = tid % q4;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     if (grp < groups) {
@@ -725,14 +747,14 @@ block_merge_kernel(const BlockParams p, long long row_blocks, int weight_chunks,
   const RangeInfo ri = range_info(p, b, g);
   dep_wait();
   for (int r = warp; r < nrows; r += THREADS / 32) {   // a warp per row, lanes over the pieces
-    const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + ri.slot0 * p.rt_rows + r;
+    const float4* ml = reinterpret_cast<const float4*>(p.part_ml) + ri.slot0 * p.rt_rows + r;   // (m, l, ..)
     const bool has_sink = p.sink || p.smooth;
     const float sink = has_sink ? (p.sink ? load_t(p.sink, g * p.G + r % p.G, p.t_type) : 0.f) * kLog2e : kNegBig;
     float m = sink, l = 0.f;
     for (int i = lane; i < ri.n; i += 32) m = fmaxf(m, ml[(long long)i * p.rt_rows].x);
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     for (int i = lane; i < ri.n; i += 32) {
-      const float2 v = ml[(long long)i * p.rt_rows];
+      const float4 v = ml[(long long)i * p.rt_rows];
       l = fmaf(v.y, ex2(v.x - m), l);
     }
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -780,7 +802,7 @@ block_weights_kernel(const BlockParams p) {
   constexpr int kParts = kHalf ? 1 : 2;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   uint2* qs = reinterpret_cast<uint2*>(smem_raw);              // [row tile of 8][step][part][lane]
-  float4* rp = reinterpret_cast<float4*>(smem_raw + kWRows * HP * 2 * kParts);  // per row: factor, lse, position
+  float4* rp = reinterpret_cast<float4*>(smem_raw + kWRows * HP * 2 * kParts);  // per row: -, lse, position
   float* up = reinterpret_cast<float*>(rp + kWRows);                              // per row: 2^e of an fp32 row
   const int bg = blockIdx.y, b = bg / p.Nkv, g = bg % p.Nkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, t = lane & 3;
@@ -813,7 +835,6 @@ block_weights_kernel(const BlockParams p) {
       const int r = r0 + x;
       float4 v = make_float4(0.f, INFINITY, 0.f, 0.f);   // a row that does not count: exp2(0 - inf) = 0
       if (r < i_hi * p.G) {
-        v.x = p.softcap > 0.f ? p.scale : p.scale * kLog2e;
         v.y = p.lse[(long long)bg * p.S * p.G + r];
         v.z = __int_as_float(past + r / p.G);
       }
@@ -866,19 +887,25 @@ block_weights_kernel(const BlockParams p) {
     __syncthreads();
     if (jw < total) {
       for (int x = 0; x < kWRows / 8; ++x) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        // The attention kernel's scores bit for bit (same products, order and
+        // factors): their own error then cancels against the log-sum-exp's.
+        float c2[kParts][4] = {};
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
 #pragma unroll
           for (int part = 0; part < kParts; ++part) {
             const uint2 q = qs[((x * kSteps + i) * kParts + part) * 32 + lane];
-            mma16816(c, a[i], q.x, q.y);
+            mma16816(c2[part], a[i], q.x, q.y);
           }
+        float c[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] = kHalf ? c2[0][e] : c2[0][e] + c2[kParts - 1][e];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {   // rows 8 x + 2 t + u
           const float4 v = rp[8 * x + 2 * t + u];
           const int pos = __float_as_int(v.z);
-          const float f = v.x * ks * (kHalf ? 1.f : up[8 * x + 2 * t + u]);
+          const float us = (kHalf ? 1.f : up[8 * x + 2 * t + u]) * p.scale;
+          const float f = (p.softcap > 0.f ? us : us * kLog2e) * ks;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int j = jw + gq + 8 * h;

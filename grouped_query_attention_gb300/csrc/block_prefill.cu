@@ -341,12 +341,14 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
       const uint32_t d = tmem + q * 128 + bf * STEP;
       const uint64_t b0 = dk0 + (uint64_t)((t % kNB) * (int)(kTile >> 4) + bf * (STEP * 128 >> 4));
 #pragma unroll
-      for (int part = 0; part < (F32 ? 2 : 1); ++part) {   // the lo tile starts 32 KB after the hi tile
+      for (int part = F32 ? 1 : 0; part >= 0; --part) {
+        // The lo tile (32 KB behind the hi tile) goes first: the accumulator's
+        // roundings are relative to its size, which the hi products bring.
         const uint64_t a0 = dq0 + (uint64_t)(q * (int)(SM::kQ >> 4) + part * (int)((2 * kBox) >> 4));
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
           const uint64_t off = (uint64_t)((ks >> 2) * 1024 + (ks & 3) * 2);
-          mma_f16_ss(d, a0 + off, b0 + off, kIdS, part > 0 || ks > 0);
+          mma_f16_ss(d, a0 + off, b0 + off, kIdS, (F32 && part == 0) || ks > 0);
         }
       }
       mma_commit(&sm.s_full[q][bf]);

@@ -123,7 +123,7 @@ gqa_status check_block_cache(const gqa_block_cache& c, const char* name, long lo
 struct BlockPlan {
   BlockParams P;
   bool prefill;                                // tensor-core prefill instead of the split over the keys
-  size_t part_o, part_ml, stash, lse, total;   // bytes of each section
+  size_t part_o, part_ml, stash, lse, o_acc, total;   // bytes of each section
 };
 
 gqa_status plan_block(const gqa_handle* h, const gqa_block_cache* cache, const gqa_block_inputs* in,
@@ -209,14 +209,17 @@ gqa_status plan_block(const gqa_handle* h, const gqa_block_cache* cache, const g
 
   const long long rows = S * G;
   pl->prefill = H == 128 && 128 % G == 0 && rows > 16;
-  pl->part_o = pl->part_ml = pl->stash = pl->lse = 0;
+  pl->part_o = pl->part_ml = pl->stash = pl->lse = pl->o_acc = 0;
   if (pl->prefill) {
     const long long nqb = (rows + 255) / 256;
     if (nqb > 65535 || (T + 127) / 128 > 65535) return fail(GQA_ERR_UNSUPPORTED, "query too large");
+    if (P.t_type == gqa::kF32 && T > gqa::kPrefillFlush)
+      pl->o_acc = align_up((size_t)(B * Nkv) * nqb * 2 * 128 * 128 * sizeof(float));
     P.qb_major = 2 * S >= T;   // key ranges differ by query block more than by sequence
   } else {
     P.rt_rows = gqa::block_row_tile(P.t_type, (int)H, rows);
     P.nrt = (int)((rows + P.rt_rows - 1) / P.rt_rows);
+    P.flush = P.t_type == gqa::kF32 && P.nrt > 1;
     P.workers = gqa::block_workers(P);
     const size_t slots = (size_t)P.workers + (size_t)(B * Nkv) * P.nrt;
     pl->part_o = align_up(slots * P.rt_rows * H * sizeof(float));
@@ -231,7 +234,7 @@ gqa_status plan_block(const gqa_handle* h, const gqa_block_cache* cache, const g
       pl->lse = align_up((size_t)(B * Nkv * rows) * sizeof(float));
     }
   }
-  pl->total = pl->part_o + pl->part_ml + pl->stash + pl->lse;
+  pl->total = pl->part_o + pl->part_ml + pl->stash + pl->lse + pl->o_acc;
   return GQA_OK;
 }
 
@@ -360,6 +363,7 @@ gqa_status gqa_block_forward(gqa_handle* h, const gqa_block_cache* cache, const 
   P.part_ml = reinterpret_cast<float*>(w + pl.part_o);
   if (pl.stash) P.stash = reinterpret_cast<float*>(w + pl.part_o + pl.part_ml);
   if (pl.lse) P.lse = reinterpret_cast<float*>(w + pl.part_o + pl.part_ml);
+  if (pl.o_acc) P.o_acc = reinterpret_cast<float*>(w + pl.part_o + pl.part_ml + pl.lse);
   P.status = static_cast<uint32_t*>(status);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;

@@ -203,9 +203,9 @@ struct WarpCtl {
 };
 
 // CTAs per SM the registers and the ring leave room for.
-template <int HP, int NT>
+template <int HP, int NT, bool FLUSH>
 constexpr int ctas_per_sm() {
-  return HP > 128 ? 1 : NT > 1 ? 2 : 3;
+  return HP > 128 ? 1 : NT > 1 || FLUSH ? 2 : 3;
 }
 
 // Query fragments of a row tile: thread t of a quad holds coordinates t HP/4
@@ -257,9 +257,14 @@ __device__ void load_queries(const BlockParams& p, int b, int g, int rt, uint2 (
   }
 }
 
-// NT: 8-row tiles of a row tile. PLAIN: no softcap and no score stash.
-template <typename T, int HP, int NT, bool PLAIN>
-__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<HP, NT>())
+// NT: 8-row tiles of a row tile. PLAIN: no softcap and no score stash. FLUSH:
+// the MMA accumulator drops what does not fit (it rounds towards zero), so over
+// a thousand keys its error grows past the other fp32 roundings; every 8 units
+// O moves into sums that round to nearest. For fp32 prompts, where a worker
+// meets whole ranges (1.8e-6 against 0.6e-6 at 1500 keys); a decode step's
+// pieces are short and its registers go to a third CTA.
+template <typename T, int HP, int NT, bool PLAIN, bool FLUSH>
+__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<HP, NT, FLUSH>())
 block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
   constexpr bool kHalf = sizeof(T) == 2;
   constexpr int kParts = kHalf ? 1 : 2;     // fp16 parts of queries and probabilities
@@ -328,6 +333,8 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
   uint2 qf[NT * kParts][kSteps];
   float o[kSteps][NT][4];       // O^T: coordinates gq HP/8 + 2 i (0, 1) and + 1 (2, 3), rows 2 t (0, 2) and + 1 (1, 3)
   float m[NT][2], l[NT][2], mul[NT][2];   // of rows 8 n + 2 t, + 1
+  float acc[FLUSH ? kSteps : 1][NT][4];
+  int held = 0;                 // FLUSH: units in o
   float lr[kHalf ? NT : 1][2];            // fp16: the sum of the probabilities as the product with V has them
   int wexp = -200;              // the V scales enter as vs 2^-wexp
   bool fresh_piece = true;
@@ -355,7 +362,11 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
 #pragma unroll
       for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+        for (int n = 0; n < NT; ++n) {
+          o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+          if constexpr (FLUSH) acc[i][n][0] = acc[i][n][1] = acc[i][n][2] = acc[i][n][3] = 0.f;
+        }
+      held = 0;
       wexp = -200;
     }
     cp_wait<kStages - 1>();
@@ -479,6 +490,12 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
           o[i][n][1] *= f[1];
           o[i][n][2] *= f[0];
           o[i][n][3] *= f[1];
+          if constexpr (FLUSH) {
+            acc[i][n][0] *= f[0];
+            acc[i][n][1] *= f[1];
+            acc[i][n][2] *= f[0];
+            acc[i][n][3] *= f[1];
+          }
         }
       }
     }
@@ -550,6 +567,20 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
         }
       }
     }
+    if constexpr (FLUSH) {
+      if (++held == 8) {
+        held = 0;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              acc[i][n][e] += o[i][n][e];
+              o[i][n][e] = 0.f;
+            }
+      }
+    }
     stage ^= 1;
     if (stage == 0) parity ^= 1;
     const int range = cp.b * p.Nkv * p.nrt + cp.gr;
@@ -560,6 +591,14 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
     fresh_piece = true;
     const long long slot = worker + range;
     const float upw = __int_as_float((127 + wexp) << 23);   // O is in units of 2^wexp
+    if constexpr (FLUSH) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][n][e] += acc[i][n][e];
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -948,23 +987,27 @@ cudaError_t allow_smem(K kern, int bytes, bool* done) {
   return cudaSuccess;
 }
 
-template <typename T, int HP, int NT, bool PLAIN>
+template <typename T, int HP, int NT, bool PLAIN, bool FLUSH>
 cudaError_t attn_one(const BlockParams& p, cudaStream_t st) {
   static bool done[kMaxDevices];
   const int smem = kWarps * (int)sizeof(WarpSmem<HP>) + 1024;
-  cudaError_t e = allow_smem(block_attn_kernel<T, HP, NT, PLAIN>, smem, done);
+  cudaError_t e = allow_smem(block_attn_kernel<T, HP, NT, PLAIN, FLUSH>, smem, done);
   if (e != cudaSuccess) return e;
   CUtensorMap mk, mv;
   const uint64_t rows = (uint64_t)p.B * p.Nkv * p.C;
   if ((e = encode_codes(&mk, p.kc, rows, p.H, HP, kBlockUnit)) != cudaSuccess) return e;
   if ((e = encode_codes(&mv, p.vc, rows, p.H, HP, kBlockUnit)) != cudaSuccess) return e;
-  return launch_dependent(p.k != nullptr, block_attn_kernel<T, HP, NT, PLAIN>, dim3((unsigned)(p.workers / kWarps)),
+  return launch_dependent(p.k != nullptr, block_attn_kernel<T, HP, NT, PLAIN, FLUSH>, dim3((unsigned)(p.workers / kWarps)),
                           kWarps * 32, (size_t)smem, st, p, mk, mv);
 }
 
 template <typename T, int HP, int NT>
 cudaError_t attn_nt(const BlockParams& p, cudaStream_t st) {
-  return p.softcap > 0.f || p.stash ? attn_one<T, HP, NT, false>(p, st) : attn_one<T, HP, NT, true>(p, st);
+  const bool plain = !(p.softcap > 0.f || p.stash);
+  if constexpr (sizeof(T) == 4) {
+    if (p.flush) return plain ? attn_one<T, HP, NT, true, true>(p, st) : attn_one<T, HP, NT, false, true>(p, st);
+  }
+  return plain ? attn_one<T, HP, NT, true, false>(p, st) : attn_one<T, HP, NT, false, false>(p, st);
 }
 
 template <int HP>
@@ -996,7 +1039,7 @@ int block_row_tile(int t_type, int H, long long rows) { return t_type == kF16 &&
 // One worker per warp, as many CTAs of four as an SM holds; fewer when there
 // are not four units for each.
 int block_workers(const BlockParams& p) {
-  const long long most = 152LL * kWarps * (p.H > 128 ? 1 : p.rt_rows > 8 ? 2 : 3);
+  const long long most = 152LL * kWarps * (p.H > 128 ? 1 : p.rt_rows > 8 || p.flush ? 2 : 3);
   const int keys = p.window >= 0 && (long long)p.window + p.S < p.T ? p.window + p.S + kBlockUnit : p.T;
   const long long units =
       (long long)p.B * p.Nkv * p.nrt * ((keys + kBlockUnit - 1) / kBlockUnit + kBlockRangeCost);

@@ -47,12 +47,14 @@ struct BlockParams {
   // split-KV kernel
   int rt_rows, nrt;      // rows of a row tile, row tiles of a (b, g)
   int workers;           // warps of the grid
+  int flush;             // fp32 with several row tiles: O summed to nearest every few units
   float *part_o, *part_ml;
   float* stash;          // log2-domain scores [B*Nkv][stash_ld keys][stash_rows] (one row tile), or null
   int stash_ld, stash_rows;
   float* lse;            // log2-domain log-sum-exp [B*Nkv][S*G], or null
   // tensor-core prefill
   int qb_major;          // grid with the query block on the slow axis
+  float* o_acc;          // fp32: sums of O, 512 bytes a row of every 128-row query tile, or null
   long long wait_budget;
   int withhold_tile;
 };
@@ -92,6 +94,7 @@ int block_workers(const BlockParams& p);
 cudaError_t launch_block_attn(const BlockParams& p, cudaStream_t st);
 cudaError_t launch_block_merge(const BlockParams& p, cudaStream_t st);
 // Tensor-core prefill: head size 128, group size dividing 128.
+constexpr int kPrefillFlush = 512;   // keys after which the fp32 form moves O into sums
 cudaError_t launch_block_prefill(const BlockParams& p, cudaStream_t st);
 // Attention weights of the cache rows from the log-sum-exp of every query row.
 cudaError_t launch_block_weights(const BlockParams& p, cudaStream_t st);

@@ -19,6 +19,12 @@
 // fp16 operand tile (3 idle: register shares go by warpgroup). Converters that
 // loaded the next codes themselves waited for them at every proxy fence:
 // 2400 cycles a tile pair, which set the pace (4700 against 2400 of MMAs).
+// The tensor-memory accumulator rounds towards zero: over thousands of keys its
+// error outgrows the other fp32 roundings (2.4e-6 at 1500 keys, 3.3e-6 at
+// 4096). With fp32 queries O therefore moves, every 512 keys, into fp32 sums in
+// the workspace (one read and write of a row's 512 bytes through L2), and the
+// next P V starts from zero.
+//
 // A step is 64 or 128 keys. S of 64 keys is 64 tensor-memory columns, so each
 // query tile has two S buffers beside its O (2 x (2 x 64 + 128) = 512 columns)
 // and S of the step after next is issued behind P.V of this one: a softmax
@@ -210,6 +216,7 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
   const int kmin = p.window >= 0 ? max(0, past + i_lo - p.window) & ~15 : 0;   // scales change at multiples of 16
   const int nsteps = (kmax - kmin + STEP - 1) / STEP;
   const int ntiles = (nsteps + kSub - 1) / kSub;
+  const int flush = F32 && p.o_acc ? kPrefillFlush / STEP : 1 << 30;   // steps between two flushes of O
 
   if (warp == 1) tmem_alloc(&sm.tmem, 512);
   if (tid == 0) {
@@ -363,7 +370,7 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
       for (int ks = 0; ks < STEP / 16; ++ks) {
         const uint32_t col = (uint32_t)((ks >> 2) * 64 + (ks & 3) * 8);
         const uint64_t bv = b0 + (uint64_t)(ks * 128);
-        mma_f16_ts(d, pa + col, bv, kIdO, h > 0 || ks > 0);
+        mma_f16_ts(d, pa + col, bv, kIdO, h % flush > 0 || ks > 0);
         if constexpr (F32) mma_f16_ts(d, pa + col + 32, bv, kIdO, true);
       }
       mma_commit(&sm.o_done[q]);
@@ -487,7 +494,9 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
     }
     const float k_row = rho * p.scale * (CAP ? 1.f / p.softcap : kLog2e);
     const float c2 = p.softcap * kLog2e;
-    float m_run = kNegBig, l_run = 0.f;
+    float m_run = kNegBig, l_run = 0.f, m_acc = kNegBig;
+    // This row's sums, four floats at a time, rows of a tile side by side.
+    float4* o_acc = F32 && p.o_acc ? reinterpret_cast<float4*>(p.o_acc) + ((long long)(bg * nqb + qb) * 2 + q) * (kHD / 4) * kBM + rl : nullptr;
     for (int st = 0; st < nsteps && ok; ++st) {
       const int t = st / kSub, bf = st % kSub, slot = t & (kScStages - 1);
       bool got = mbar_wait(&sm.s_full[q][bf], (uint32_t)t & 1u, p.wait_budget) && !aborted(sm);
@@ -502,6 +511,35 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
       const int j0 = kmin + st * STEP;
       const int lo = max(lo_key - j0, 0), hi = min(hi_key - j0, STEP);   // visible columns [lo, hi)
       const bool full = __all_sync(0xffffffffu, lo == 0 && hi == STEP);
+      if constexpr (F32) {
+        if (st > 0 && st % flush == 0) {   // O of the steps before, complete, into the sums
+          if (!__all_sync(0xffffffffu, mbar_wait(&sm.o_done[q], (uint32_t)(st - 1) & 1u, p.wait_budget))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const bool first = st == flush;
+          const float f = ex2(m_acc - m_run);
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t raw[16];
+            tmem_ld16(o_addr + c * 16, raw);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float4 v = make_float4(__uint_as_float(raw[4 * e]), __uint_as_float(raw[4 * e + 1]),
+                                     __uint_as_float(raw[4 * e + 2]), __uint_as_float(raw[4 * e + 3]));
+              float4* at = o_acc + (4 * c + e) * kBM;
+              if (!first) {
+                const float4 a = *at;
+                v = make_float4(fmaf(a.x, f, v.x), fmaf(a.y, f, v.y), fmaf(a.z, f, v.z), fmaf(a.w, f, v.w));
+              }
+              *at = v;
+            }
+          }
+          m_acc = m_run;
+        }
+      }
       // Row max (a softcap is monotone); a softcap also takes the largest
       // |score|. Masked columns then hold what the exponent turns into -inf:
       // -inf, or +inf under a softcap's fit (its last coefficient is negative,
@@ -699,6 +737,17 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
         tmem_ld32(o_addr + c * 32, raw);
         tmem_ld_wait();
         if constexpr (F32) {   // box c: dims 32 c ..
+          if (nsteps > flush) {
+            const float fa = ex2(m_acc - m_run);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 a = o_acc[(8 * c + e) * kBM];
+              raw[4 * e] = __float_as_uint(fmaf(a.x, fa, __uint_as_float(raw[4 * e])));
+              raw[4 * e + 1] = __float_as_uint(fmaf(a.y, fa, __uint_as_float(raw[4 * e + 1])));
+              raw[4 * e + 2] = __float_as_uint(fmaf(a.z, fa, __uint_as_float(raw[4 * e + 2])));
+              raw[4 * e + 3] = __float_as_uint(fmaf(a.w, fa, __uint_as_float(raw[4 * e + 3])));
+            }
+          }
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<float4*>(stage + c * kBox + sw128_offset(rl, e >> 2)) =

@@ -100,6 +100,9 @@ CASES = {
     "prefill_window_f32": ("f32", 2, 100, 4, 2, 128, 700, 256, (641, 222), (100, 50), 200, 0, 0, 1, 1),
     "prefill_softcap_small": ("f16", 1, 200, 4, 2, 128, 512, 64, (400,), None, -1, 50.0, 1, 1, 1),
     "prefill_softcap_large": ("f32", 1, 100, 4, 2, 128, 512, 64, (301,), None, 150, 1.5, 1, 1, 1),
+    "prefill_flush_f32": ("f32", 1, 24, 2, 2, 128, 2600, 64, (2500,), None, -1, 0, 0, 1, 1),
+    "prefill_flush_softcap_f32": ("f32", 1, 20, 2, 2, 128, 1300, 64, (1200,), None, -1, 20.0, 0, 1, 1),
+    "flush_h80_f32": ("f32", 2, 9, 4, 2, 80, 1500, 64, (1500, 700), None, -1, 0, 0, 1, 1),
     "prefill_g1": ("f16", 1, 200, 2, 2, 128, 256, 16, (199,), (190,), -1, 0, 0, 1, 1),
     "prefill_g32": ("f16", 1, 20, 32, 1, 128, 256, 64, (150,), None, -1, 0, 0, 1, 1),
     "prefill_g128": ("f32", 1, 3, 128, 1, 128, 64, 16, (40,), None, -1, 0, 0, 1, 1),

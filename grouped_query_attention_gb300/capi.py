@@ -26,8 +26,8 @@ GQA_DEVICE_BAD_SEQLEN, GQA_DEVICE_BAD_ROTARY, GQA_DEVICE_TIMEOUT = 1, 2, 4
 EXPORTS = ["gqa_attrs_default", "gqa_create", "gqa_workspace_size", "gqa_forward",
            "gqa_read_device_status", "gqa_describe_plan", "gqa_destroy", "gqa_status_string",
            "gqa_last_error", "gqa_forward_noalloc", "gqa_profile_begin", "gqa_profile_end",
-           "gqa_set_wait_limit", "gqa_rotary_axes", "gqa_block_workspace_size", "gqa_block_forward",
-           "gqa_block_evict"]
+           "gqa_set_wait_limit", "gqa_rotary_axes", "gqa_block_workspace_size", "gqa_block_describe_plan",
+           "gqa_block_forward", "gqa_block_evict"]
 KERNEL_KINDS = {1: "copy_past", 2: "prepass", 3: "decode", 4: "prefill_cuda_core", 5: "prefill_tensor_core",
                 6: "decode_tensor_core", 7: "window_shift", 8: "bias_stage", 9: "rotary_axes", 10: "block_append",
                 11: "block_attention", 12: "block_merge", 13: "block_prefill", 14: "block_weights",
@@ -152,6 +152,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.gqa_block_workspace_size.argtypes = [V, P(GqaBlockCache), P(GqaBlockInputs), P(GqaBlockOutputs),
                                              P(ctypes.c_size_t)]
     lib.gqa_block_workspace_size.restype = ctypes.c_int
+    lib.gqa_block_describe_plan.argtypes = [V, P(GqaBlockCache), P(GqaBlockInputs), P(GqaBlockOutputs), P(GqaPlanInfo)]
+    lib.gqa_block_describe_plan.restype = ctypes.c_int
     lib.gqa_block_forward.argtypes = [V, P(GqaBlockCache), P(GqaBlockInputs), P(GqaBlockOutputs), V, ctypes.c_size_t,
                                       V, V]
     lib.gqa_block_forward.restype = ctypes.c_int
@@ -254,6 +256,13 @@ def gqa_block_workspace_size(handle, cache: GqaBlockCache, inputs: GqaBlockInput
     n = ctypes.c_size_t()
     _check(load_library().gqa_block_workspace_size(handle, cache, inputs, outputs, ctypes.byref(n)))
     return n.value
+
+
+def gqa_block_describe_plan(handle, cache: GqaBlockCache, inputs: GqaBlockInputs,
+                            outputs: GqaBlockOutputs) -> GqaPlanInfo:
+    info = GqaPlanInfo()
+    _check(load_library().gqa_block_describe_plan(handle, cache, inputs, outputs, ctypes.byref(info)))
+    return info
 
 
 def gqa_block_forward(handle, cache: GqaBlockCache, inputs: GqaBlockInputs, outputs: GqaBlockOutputs, workspace: int,

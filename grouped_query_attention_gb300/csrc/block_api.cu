@@ -120,6 +120,34 @@ gqa_status check_block_cache(const gqa_block_cache& c, const char* name, long lo
   return GQA_OK;
 }
 
+// Whether the tensor-core prefill takes a call, which its head size and group
+// size allow, rather than the split over the keys. The prefill runs a CTA per
+// 256 query rows of a KV head over their whole key range; few long ranges leave
+// most SMs idle there, while the split gives every warp an equal share. Both are
+// estimated from measurements (us; fp16, fp32, with a softcap): a wave of
+// prefill CTAs takes 1.95, 3.6, 3.5 per 128 keys (1.4 times that when only one
+// of its two query tiles has rows), a worker of the split 2.1, 2.1, 3.6
+// per 32 keys and row tile, its merge 0.003 per query row. Measured on both
+// sides: 64 rows a head on 32768 keys 492 against 240 us, 256 rows on 2048 keys
+// 43 against 96, 24 fp32 rows on 25000 keys 836 against 51.
+bool use_prefill(const BlockParams& P, long long rows) {
+  const int rt = gqa::block_row_tile(P.t_type, P.H, rows);
+  const double nrt = (double)((rows + rt - 1) / rt), heads = (double)P.B * P.Nkv;
+  const double ctas = heads * (double)((rows + 255) / 256), waves = ceil(ctas / 152.0);
+  double mean = P.T - 0.5 * P.S, most = P.T;   // keys a query row sees
+  if (P.window >= 0) {
+    mean = mean < P.window ? mean : P.window;
+    most = most < (double)P.window + P.S ? most : (double)P.window + P.S;
+  }
+  const bool f32 = P.t_type == gqa::kF32, cap = P.softcap > 0.f;
+  double tile = f32 ? 3.6 : cap ? 3.5 : 1.95;
+  if (rows <= 128) tile *= 1.4;
+  const double prefill = 8.0 + waves * (waves > 1.0 ? mean : most) / 128.0 * tile;
+  const double workers = P.H > 128 ? 608.0 : 1216.0;
+  const double split = 10.0 + heads * nrt * (mean / 32.0 + 2.0) / workers * (cap ? 3.6 : 2.1) + heads * rows * 0.003;
+  return prefill <= split;
+}
+
 struct BlockPlan {
   BlockParams P;
   bool prefill;                                // tensor-core prefill instead of the split over the keys
@@ -208,7 +236,7 @@ gqa_status plan_block(const gqa_handle* h, const gqa_block_cache* cache, const g
   P.withhold_tile = h->withhold_tile;
 
   const long long rows = S * G;
-  pl->prefill = H == 128 && 128 % G == 0 && rows > 16;
+  pl->prefill = H == 128 && 128 % G == 0 && rows > 16 && use_prefill(P, rows);
   pl->part_o = pl->part_ml = pl->stash = pl->lse = pl->o_acc = 0;
   if (pl->prefill) {
     const long long nqb = (rows + 255) / 256;
@@ -345,6 +373,20 @@ gqa_status gqa_block_workspace_size(const gqa_handle* h, const gqa_block_cache* 
   gqa_status s = plan_block(h, cache, in, out, &pl);
   if (s != GQA_OK) return s;
   *bytes = pl.total;
+  return GQA_OK;
+}
+
+gqa_status gqa_block_describe_plan(const gqa_handle* h, const gqa_block_cache* cache, const gqa_block_inputs* in,
+                                   const gqa_block_outputs* out, gqa_plan_info* info) {
+  if (!info) return fail(GQA_ERR_INVALID_ARGUMENT, "NULL info pointer");
+  BlockPlan pl;
+  gqa_status s = plan_block(h, cache, in, out, &pl);
+  if (s != GQA_OK) return s;
+  info->regime = pl.prefill ? GQA_REGIME_PREFILL : GQA_REGIME_DECODE;
+  info->launches = (pl.P.k ? 1 : 0) + (pl.prefill ? 1 : 2) + (pl.lse ? 1 : 0);
+  info->split_len = pl.prefill ? 0 : gqa::kBlockUnit;
+  info->max_splits = pl.prefill ? 0 : pl.P.workers;
+  info->workspace_bytes = pl.total;
   return GQA_OK;
 }
 

@@ -383,6 +383,14 @@ GQA_API gqa_status gqa_block_forward(gqa_handle* handle, const gqa_block_cache* 
                                      const gqa_block_outputs* out, void* workspace, size_t workspace_bytes,
                                      void* status, void* stream);
 
+/* Host-only description of how gqa_block_forward would run a call (same checks):
+ * regime GQA_REGIME_DECODE: the keys of every KV head split over the warps of the
+ * GPU (split_len keys a unit, max_splits workers); GQA_REGIME_PREFILL: the
+ * tensor-core prefill over whole key ranges. launches counts the kernels. */
+GQA_API gqa_status gqa_block_describe_plan(const gqa_handle* handle, const gqa_block_cache* cache,
+                                           const gqa_block_inputs* in, const gqa_block_outputs* out,
+                                           gqa_plan_info* info);
+
 /* Eviction from a block-scaled cache by accumulated attention weight: the live
  * rows of every (sequence, KV head) are reduced to at most `keep`, copied in
  * their order to rows 0 .. of another cache. Sequences with total_b <= keep

@@ -99,6 +99,7 @@ def step(query, key, value, seqlens_k, new_lens, cache, block_size, num_heads, k
                     rows = np.asarray(x[b, :new], F32).reshape(new, kv_num_heads, H)[:, g]
                     append(c[b, g], s[b, g], rows, past, block_size)
             k, v = values(kc[b, g], ks[b, g], total, block_size), values(vc[b, g], vs[b, g], total, block_size)
+            av, size = np.abs(v), np.abs(k).sum(-1)
             got = np.zeros(total)
             for i in range(new):
                 p = past + i
@@ -113,8 +114,8 @@ def step(query, key, value, seqlens_k, new_lens, cache, block_size, num_heads, k
                     e = np.exp(z - m)
                     e = e / (e.sum() + sum(math.exp(x - m) for x in extra))
                     out[b, i, h] = e @ v[lo:p + 1]
-                    mag[b, i, h] = e @ np.abs(v[lo:p + 1])
-                    reach[b, i, h] = np.abs(k[lo:p + 1]).sum(-1).max() * np.abs(q).max() * scale
+                    mag[b, i, h] = e @ av[lo:p + 1]
+                    reach[b, i, h] = size[lo:p + 1].max() * np.abs(q).max() * scale
                     got[lo:p + 1] += e
             if weights is not None:
                 had = 0.0 if past_weights is None else np.where(np.arange(total) < past, past_weights[b, g, :total], 0.0)

@@ -180,6 +180,21 @@ def test_workspace_size_grows_with_weights():
     assert c.size() > 0
 
 
+def test_plan_by_shape():
+    """One token: the split over the keys. A prompt: the tensor-core prefill. A few rows on long ranges: the split."""
+    def plan(**kw):
+        c = Call(**kw)
+        return c._run(lambda h: capi.gqa_block_describe_plan(h, c.cache, c.inp, c.out))
+
+    one = plan(S=1, H=128, C=4096)
+    assert one.regime == capi.GQA_REGIME_DECODE and one.launches == 3 and one.split_len == 32 and one.max_splits > 0
+    prompt = plan(S=1024, H=128, C=1024, B=4)
+    assert prompt.regime == capi.GQA_REGIME_PREFILL and prompt.launches == 2
+    assert plan(S=16, H=128, C=32768, B=1).regime == capi.GQA_REGIME_DECODE
+    assert plan(S=1024, H=96, C=1024, B=4).regime == capi.GQA_REGIME_DECODE
+    assert plan(S=1024, H=128, N=6, C=1024, B=4).regime == capi.GQA_REGIME_DECODE     # a group of 3
+
+
 @pytest.mark.parametrize("attrs", [dict(causal=0), dict(do_rotary=1), dict(k_quant_type=1, v_quant_type=1),
                                    dict(local_window_size=4, sliding_window_cache=1)])
 def test_forward_refuses_attributes(attrs):

@@ -91,17 +91,17 @@ CASES = {
     "prompt_f32_h128": ("f32", 2, 70, 4, 2, 128, 128, 64, (70, 41), (70, 41), -1, 0, 0, 1, 1),
     "prompt_h128": ("f16", 2, 150, 8, 2, 128, 256, 64, (150, 99), (150, 99), -1, 0, 0, 1, 1),
     "chunk_h128_window": ("f16", 2, 40, 8, 2, 128, 600, 16, (600, 300), None, 130, 0, 1, 1, 1),
-    "chunk_h128_softcap": ("f16", 1, 33, 16, 2, 128, 300, 32, (300,), None, -1, 4.0, 0, 1, 1),
+    "prefill_softcap_g16": ("f16", 1, 60, 64, 4, 128, 300, 32, (300,), None, -1, 4.0, 0, 1, 1),
     "chunk_h128_f32": ("f32", 2, 33, 8, 2, 128, 300, 32, (300, 40), (33, 7), -1, 0, 1, 1, 1),
     "prefill_two_tiles": ("f16", 1, 300, 4, 1, 128, 512, 64, (300,), None, -1, 0, 0, 1, 1),
-    "prefill_two_tiles_f32": ("f32", 1, 200, 4, 2, 128, 512, 128, (200,), None, -1, 0, 1, 1, 1),
+    "prefill_two_tiles_f32": ("f32", 1, 200, 16, 4, 128, 512, 128, (200,), None, -1, 0, 1, 1, 1),
     "prefill_past": ("f16", 3, 90, 8, 2, 128, 700, 16, (700, 333, 90), (90, 17, 90), -1, 0, 1, 1, 1),
     "prefill_window": ("f16", 2, 200, 4, 2, 128, 700, 32, (641, 222), None, 77, 0, 0, 1, 1),
-    "prefill_window_f32": ("f32", 2, 100, 4, 2, 128, 700, 256, (641, 222), (100, 50), 200, 0, 0, 1, 1),
-    "prefill_softcap_small": ("f16", 1, 200, 4, 2, 128, 512, 64, (400,), None, -1, 50.0, 1, 1, 1),
-    "prefill_softcap_large": ("f32", 1, 100, 4, 2, 128, 512, 64, (301,), None, 150, 1.5, 1, 1, 1),
-    "prefill_flush_f32": ("f32", 1, 24, 2, 2, 128, 2600, 64, (2500,), None, -1, 0, 0, 1, 1),
-    "prefill_flush_softcap_f32": ("f32", 1, 20, 2, 2, 128, 1300, 64, (1200,), None, -1, 20.0, 0, 1, 1),
+    "prefill_window_f32": ("f32", 2, 100, 16, 4, 128, 700, 256, (641, 222), (100, 50), 200, 0, 0, 1, 1),
+    "prefill_softcap_small": ("f16", 1, 200, 16, 4, 128, 512, 64, (400,), None, -1, 50.0, 1, 1, 1),
+    "prefill_softcap_large": ("f32", 1, 100, 16, 4, 128, 512, 64, (301,), None, 150, 1.5, 1, 1, 1),
+    "prefill_flush_f32": ("f32", 1, 50, 64, 8, 128, 1200, 64, (1100,), None, -1, 0, 0, 1, 1),
+    "prefill_flush_softcap_f32": ("f32", 1, 50, 64, 8, 128, 1200, 64, (1100,), None, -1, 20.0, 0, 1, 1),
     "flush_h80_f32": ("f32", 2, 9, 4, 2, 80, 1500, 64, (1500, 700), None, -1, 0, 0, 1, 1),
     "prefill_g1": ("f16", 1, 200, 2, 2, 128, 256, 16, (199,), (190,), -1, 0, 0, 1, 1),
     "prefill_g32": ("f16", 1, 20, 32, 1, 128, 256, 64, (150,), None, -1, 0, 0, 1, 1),
@@ -168,10 +168,17 @@ def check(d, got):
         assert (err <= tol).all(), f"weights off by {err.max()} (worst {np.max(err / tol)} of its tolerance)"
 
 
+def regime(op):
+    return capi.gqa_block_describe_plan(op.handle, *op._block_calls["forward"].structs).regime
+
+
 @pytest.mark.parametrize("name", list(CASES))
 def test_step(name):
     d = make(CASES[name])
-    check(d, run_gpu(d))
+    got = run_gpu(d)
+    if name.startswith("prefill"):
+        assert regime(got[3]) == capi.GQA_REGIME_PREFILL
+    check(d, got)
 
 
 def test_capacity_beyond_the_lengths():
@@ -256,14 +263,16 @@ def test_wide_range_of_value_scales():
 
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
 def test_wide_range_of_value_scales_prefill(dtype):
-    d = make((dtype, 1, 20, 2, 1, 128, 512, 16, (512,), None, -1, 0, 0, 1, 0), seed=7)
+    d = make((dtype, 1, 60, 64, 4, 128, 512, 16, (512,), None, -1, 0, 0, 1, 0), seed=7)
     d["cache"][3][:] = 0.01
     d["cache"][3][0, 0, 3] = 0.01 * 64
     d["cache"][3][0, 0, 20] = 0.0
     d["cache"][3][0, 0, 25] = 1e-30
     d["cache"][2][0, 0, 21] = 0.0
     d["cache"][1][0, 0, 320:336] = 0
-    check(d, run_gpu(d))
+    got = run_gpu(d)
+    assert regime(got[3]) == capi.GQA_REGIME_PREFILL
+    check(d, got)
 
 
 @pytest.mark.parametrize("name,tile", [("one_token", 0), ("long_split", 1), ("prefill_past", 0), ("prefill_past", 1),

@@ -33,39 +33,75 @@ __device__ __forceinline__ int code_slow(float x, float s, float inv) {
   return (int)fminf(fmaxf(nearest_step(x, 0.f, s, c), -127.f), 127.f);
 }
 
-// c = rint(x * (1/s)) is off by at most one and only beside a border. There
-// the remainder x - c s is exact in fp32 (both are multiples of the smaller
-// operand's last place, and it is about s / 2), so 2 |x - c s| < s proves c.
-// What it does not prove (a border, a tie, infinities, NaN) is `unsure`.
-__device__ __forceinline__ uint32_t code_bits(float x, float s, float inv, bool* unsure) {
-  const float r = fmaf(x, inv, kMagic);
-  const float rem = fmaf(-(r - kMagic), s, x);
-  *unsure |= !(2.f * fabsf(rem) < s);
-  return __float_as_uint(r) & 0xffu;
+// The larger of two values, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Low bytes of four words.
+__device__ __forceinline__ uint32_t low_bytes(float a, float b, float c, float d) {
+  const uint32_t lo = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040u);
+  const uint32_t hi = __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040u);
+  return __byte_perm(lo, hi, 0x5410u);
+}
+
+// Eight codes of x[0..7] by scale s > 0, inv = 1/s. c = rint(x inv) is off by
+// at most one and only beside a border. There the remainder x - c s is exact
+// in fp32 (both are multiples of the smaller operand's last place, and it is
+// about s / 2), so 2 |x - c s| < s proves c. What it does not prove (a border,
+// a tie, infinities, NaN) is settled one value at a time.
+__device__ __forceinline__ uint2 codes8(const float* x, float s, float inv) {
+  float2 r[4];
+  float worst = 0.f;
+  const float2 inv2 = make_float2(inv, inv), magic = make_float2(kMagic, kMagic), neg = make_float2(-kMagic, -kMagic);
+  const float2 s2 = make_float2(-s, -s);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = make_float2(x[2 * i], x[2 * i + 1]);
+    r[i] = ffma2(v, inv2, magic);
+    const float2 rem = ffma2(fadd2(r[i], neg), s2, v);
+    worst = max_nan(worst, max_nan(fabsf(rem.x), fabsf(rem.y)));
+  }
+  uint2 w = make_uint2(low_bytes(r[0].x, r[0].y, r[1].x, r[1].y), low_bytes(r[2].x, r[2].y, r[3].x, r[3].y));
+  if (!(2.f * worst < s)) {
+    w = make_uint2(0u, 0u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      w.x |= (uint32_t)(code_slow(x[e], s, inv) & 0xff) << (8 * e);
+      w.y |= (uint32_t)(code_slow(x[4 + e], s, inv) & 0xff) << (8 * e);
+    }
+  }
+  return w;
 }
 
 // Four codes as the integers nearest to code * from / to (ties to even), from
-// <= to. ratio is fp32(from / to): a product is within 2e-5 of its quotient,
+// <= to. ratio is fp32(from / to): code * ratio is within 2e-5 of its quotient,
 // so only one that close to a border needs the exact comparison.
 __device__ __forceinline__ uint32_t recode4(uint32_t w, float from, float to, float ratio) {
   const uint32_t u = w ^ 0x80808080u;   // code + 128 in each byte
-  uint32_t out = 0;
+  const float2 ratio2 = make_float2(ratio, ratio), magic = make_float2(kMagic, kMagic);
+  const float2 base = make_float2(-8388736.f, -8388736.f), minus = make_float2(-1.f, -1.f);
+  float2 r[2];
   float near = 0.f;
-  float q[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    // the byte under the exponent of 2^23, less 2^23 + 128
-    q[e] = (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440u | e)) - 8388736.f) * ratio;
-    const float r = q[e] + kMagic;
-    near = fmaxf(near, fabsf(q[e] - (r - kMagic)));
-    out |= (__float_as_uint(r) & 0xffu) << (8 * e);
+  for (int i = 0; i < 2; ++i) {
+    // a byte under the exponent of 2^23, less 2^23 + 128
+    const float2 v = fadd2(make_float2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440u | (2 * i))),
+                                       __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440u | (2 * i + 1)))), base);
+    r[i] = ffma2(v, ratio2, magic);
+    // v ratio - c, rounded once
+    const float2 d = ffma2(v, ratio2, ffma2(r[i], minus, magic));
+    near = fmax3(near, fabsf(d.x), fabsf(d.y));
   }
+  uint32_t out = low_bytes(r[0].x, r[0].y, r[1].x, r[1].y);
   if (near > 0.5f - 4e-5f) {
     out = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float c0 = (float)(int)(int8_t)(w >> (8 * e)), hi = c0 * from;
-      out |= (uint32_t)((int)nearest_step(hi, fmaf(c0, from, -hi), to, rintf(q[e])) & 0xff) << (8 * e);
+      out |= (uint32_t)((int)nearest_step(hi, fmaf(c0, from, -hi), to, rintf(c0 * ratio)) & 0xff) << (8 * e);
     }
   }
   return out;
@@ -100,6 +136,13 @@ __device__ __forceinline__ float finite_abs(float x) {
 
 constexpr int kAppendThreads = 128;
 
+// i / d for i < 8192, d <= 32 as a product (the rounding of 2^20 / d adds less than 1 / d).
+struct SmallDiv {
+  unsigned m, d;
+  __device__ explicit SmallDiv(int div) : m((1u << 20) / (unsigned)div + 1u), d((unsigned)div) {}
+  __device__ __forceinline__ int quot(int i) const { return (int)(((unsigned)i * m) >> 20); }
+};
+
 // One block of tokens of one (b, g), K (z = 0) or V (z = 1): the largest |x|
 // of its new rows, the scale, the codes. The rows are read twice, the second
 // time out of the L1 / L2 cache; HBM sees sizeof(T) + 1 bytes per element.
@@ -123,12 +166,13 @@ block_append_kernel(const BlockParams p) {
   int8_t* codes = (blockIdx.z == 0 ? p.kc : p.vc) + (long long)bg * p.C * p.H;
   float* scale = (blockIdx.z == 0 ? p.ks : p.vs) + (long long)bg * p.nblk + blk;
   const int chunks = p.H / 8, n = (hi - lo) * chunks;
+  const SmallDiv div(chunks);
   const long long ld = (long long)p.Nkv * p.H;                                   // elements between tokens
   const T* src = x + ((long long)b * p.S + (lo - past)) * ld + (long long)g * p.H;
 
   float amax = 0.f;
   for (int i = tid; i < n; i += kAppendThreads) {
-    const int r = i / chunks, c = i - r * chunks;
+    const int r = div.quot(i), c = i - r * chunks;
     float f[8];
     load8<T>(src + r * ld + 8 * c, f);
 #pragma unroll
@@ -157,21 +201,10 @@ block_append_kernel(const BlockParams p) {
   const float inv = __fdiv_rn(1.f, s);
   int8_t* dst = codes + (long long)lo * p.H;
   for (int i = tid; i < n; i += kAppendThreads) {
-    const int r = i / chunks, c = i - r * chunks;
+    const int r = div.quot(i), c = i - r * chunks;
     float f[8];
     load8<T>(src + r * ld + 8 * c, f);
-    uint32_t w[2] = {0u, 0u};
-    if (s > 0.f) {
-      bool unsure = false;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e >> 2] |= code_bits(f[e], s, inv, &unsure) << (8 * (e & 3));
-      if (unsure) {
-        w[0] = w[1] = 0u;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e >> 2] |= (uint32_t)(code_slow(f[e], s, inv) & 0xff) << (8 * (e & 3));
-      }
-    }
-    *reinterpret_cast<uint2*>(dst + (long long)i * 8) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(dst + (long long)i * 8) = s > 0.f ? codes8(f, s, inv) : make_uint2(0u, 0u);
   }
 }
 
@@ -187,15 +220,18 @@ __device__ __forceinline__ unsigned weight_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-constexpr int kSelCache = 16384;   // rows of a CTA whose keys stay in shared memory
-constexpr int kSelRows = 4096;     // rows a CTA is given before the cluster grows
+constexpr int kSelKeys = 16;                        // consecutive rows a thread holds in registers
+constexpr int kSelRows = kSelThreads * kSelKeys;    // rows of a CTA at a time
 
 // One (b, g) per cluster of CL CTAs, each with an equal slice of the rows
-// between `first` and `recent`. A radix selection (four passes of eight bits
-// from the top, the CTAs' histograms added over distributed shared memory)
-// finds the key of the last row that stays and how many rows with exactly that
-// key do; a scan in row order then writes the indices. Bound: latency, 4 bytes
-// a row; one CTA of 131072 rows took 250 us, a cluster of eight 30.
+// between `first` and `recent`. A radix selection, four bits at a time from
+// the top, finds the key of the last row that stays and how many rows with
+// exactly that key do; it ends early once every row with the digits found so
+// far stays. Sixteen counters of a thread's keys fit 4-bit fields of a 64-bit
+// register (no shared atomics, whose conflicts took most of an 8-bit pass),
+// warps add them with integer reductions, CTAs over distributed shared memory.
+// Threads hold consecutive rows, so one scan places the rows that stay in
+// order. Bound: latency, 4 bytes a row.
 __global__ void __launch_bounds__(kSelThreads)
 evict_select_kernel(const EvictParams p, int CL) {
   namespace cg = cooperative_groups;
@@ -220,131 +256,149 @@ evict_select_kernel(const EvictParams p, int CL) {
   for (int i = at; i < p.recent; i += step) kept[p.keep - p.recent + i] = hi + i;
   int need = p.keep - p.first - p.recent;   // of the rows [lo, hi); need < hi - lo
   if (need == 0) return;
-  const float* w = p.w + (long long)bg * p.C;
-  const int per = ((hi - lo + CL - 1) / CL + 31) & ~31;          // rows of a CTA
-  const int a = min(lo + rank * per, hi), n = min(per, hi - a);
-  extern __shared__ unsigned keys[];
-  const bool cached = n <= kSelCache;
-  if (cached)
-    for (int i = tid; i < n; i += kSelThreads) keys[i] = weight_key(w[a + i]);
-  auto key_at = [&](int i) { return cached ? keys[i] : weight_key(w[a + i]); };
-  __shared__ int hist[256];    // this CTA's counts
-  __shared__ int sum[256];     // the cluster's
-  __shared__ unsigned s_digit;
-  __shared__ int s_need, s_count[2];
-  __shared__ int wsum[2][kSelThreads / 32];
+  const int per = (hi - lo + CL - 1) / CL;                       // rows of a CTA
+  const int a = min(lo + rank * per, hi), n = min(per, hi - a);  // its own
+  const float* w = p.w + (long long)bg * p.C + a;
+  const int rounds = (n + kSelRows - 1) / kSelRows;              // 1 unless the slice exceeds the registers
+  const int kpt = min((n + kSelThreads - 1) / kSelThreads, kSelKeys);   // rows of a thread in a round
+  unsigned key[kSelKeys];
+  int mine = 0;                                                  // keys held
+  auto load = [&](int round) {
+    const int base = round * kSelRows + tid * kpt;
+    mine = max(0, min(kpt, n - base));
+#pragma unroll
+    for (int k = 0; k < kSelKeys; ++k)
+      if (k < mine) key[k] = weight_key(w[base + k]);
+  };
+  if (rounds <= 1) load(0);
+
+  __shared__ unsigned wcnt[kSelThreads / 32][16];
+  __shared__ int hist[2][16];          // the CTA's counts, by pass parity
+  __shared__ int wsum[kSelThreads / 32], s_count[2];
   unsigned prefix = 0, mask = 0;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-      const int i = i0 + tid;
-      const unsigned key = i < n ? key_at(i) : 0u;
-      const bool in = i < n && (key & mask) == prefix;
-      const unsigned digit = (key >> shift) & 255u;
-      const unsigned ins = __ballot_sync(0xffffffffu, in);
-      if (ins == 0) continue;
-      // a warp whose digits are all the same (top digits, ties) counts them as one
-      const unsigned first = __shfl_sync(0xffffffffu, digit, __ffs(ins) - 1);
-      if (__all_sync(0xffffffffu, !in || digit == first)) {
-        if (lane == 0) atomicAdd(&hist[first], __popc(ins));
-      } else if (in) {
-        atomicAdd(&hist[digit], 1);
-      }
-    }
-    if (CL > 1) cluster.sync(); else __syncthreads();
-    if (tid < 256) {
-      int c = 0;
-      for (int r = 0; r < CL; ++r) c += CL > 1 ? cluster.map_shared_rank(hist, r)[tid] : hist[tid];
-      sum[tid] = c;
-    }
-    __syncthreads();
-    if (warp == 0) {   // from the top digit down: the one at which `need` rows are reached
-      int n8 = 0;
-      for (int i = 0; i < 8; ++i) n8 += sum[255 - (8 * lane + i)];
-      int incl = n8;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      int before = incl - n8;
-      if (before < need && incl >= need) {
-        for (int i = 0; i < 8; ++i) {
-          const int d = 255 - (8 * lane + i), c = sum[d];
-          if (before + c >= need) {
-            s_digit = (unsigned)d;
-            s_need = need - before;
-            break;
-          }
-          before += c;
+  for (int shift = 28, pass = 0; shift >= 0; shift -= 4, ++pass) {
+    unsigned c0 = 0, c1 = 0;           // lane i < 8: the warp's keys with digit 2 i, 2 i + 1
+    for (int round = 0; round < max(rounds, 1); ++round) {
+      if (rounds > 1) load(round);
+      unsigned long long acc[2] = {0ull, 0ull};
+#pragma unroll
+      for (int k = 0; k < kSelKeys; ++k)
+        if (k < mine && (key[k] & mask) == prefix) acc[k >> 3] += 1ull << (4 * ((key[k] >> shift) & 15u));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        unsigned f = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const unsigned v = (unsigned)(acc[h] >> (8 * i)) & 0xffu;
+          f += (v & 15u) | (v >> 4) << 16;
+        }
+        f = __reduce_add_sync(0xffffffffu, f);
+        if (lane == i) {
+          c0 += f & 0xffffu;
+          c1 += f >> 16;
         }
       }
     }
-    if (CL > 1) cluster.sync(); else __syncthreads();   // the histograms have been read, the digit is there
-    prefix |= s_digit << shift;
-    mask |= 255u << shift;
-    need = s_need;
-  }
-  // `need` rows with key == prefix stay (the lowest), and all above it. Rows
-  // and ties of the CTAs before this one:
-  int above_n = 0, tie_n = 0;
-  for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-    const int i = i0 + tid;
-    const unsigned key = i < n ? key_at(i) : 0u;
-    above_n += i < n && key > prefix;
-    tie_n += i < n && key == prefix;
-  }
-  for (int o = 16; o; o >>= 1) {
-    above_n += __shfl_xor_sync(0xffffffffu, above_n, o);
-    tie_n += __shfl_xor_sync(0xffffffffu, tie_n, o);
-  }
-  if (lane == 0) {
-    wsum[0][warp] = above_n;
-    wsum[1][warp] = tie_n;
-  }
-  __syncthreads();
-  if (tid < 2) {
-    int c = 0;
-    for (int i = 0; i < kSelThreads / 32; ++i) c += wsum[tid][i];
-    s_count[tid] = c;
-  }
-  if (CL > 1) cluster.sync(); else __syncthreads();
-  int out = p.first, ties = 0;
-  for (int r = 0; r < rank; ++r) {
-    const int* c = cluster.map_shared_rank(s_count, r);
-    out += c[0];
-    ties += c[1];
-  }
-  out += min(ties, need);
-  for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-    const int i = i0 + tid;
-    const unsigned key = i < n ? key_at(i) : 0u;
-    const bool above = i < n && key > prefix, tie = i < n && key == prefix;
-    const unsigned ma = __ballot_sync(0xffffffffu, above), mt = __ballot_sync(0xffffffffu, tie);
-    __syncthreads();   // the counts of the round before have been read
-    if (lane == 0) {
-      wsum[0][warp] = __popc(ma);
-      wsum[1][warp] = __popc(mt);
-    }
+    if (lane < 8) *reinterpret_cast<uint2*>(&wcnt[warp][2 * lane]) = make_uint2(c0, c1);
     __syncthreads();
-    // every warp scans the 32 warp counts
-    const int va = wsum[0][lane], vt = wsum[1][lane];
-    int ia = va, it = vt;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int xa = __shfl_up_sync(0xffffffffu, ia, o), xt = __shfl_up_sync(0xffffffffu, it, o);
-      if (lane >= o) {
-        ia += xa;
-        it += xt;
+    if (warp < 16) {
+      const unsigned c = __reduce_add_sync(0xffffffffu, wcnt[lane][warp]);
+      if (lane == 0) hist[pass & 1][warp] = (int)c;
+    }
+    if (CL > 1) cluster.sync(); else __syncthreads();
+    // Every warp: counts of the digits from the top (lane l: digit 15 - l), and
+    // the one at which `need` rows are reached.
+    int c = 0;
+    if (lane < 16) {
+      if (CL > 1) {
+        for (int r = 0; r < CL; ++r) c += cluster.map_shared_rank(&hist[pass & 1][0], r)[15 - lane];
+      } else {
+        c = hist[pass & 1][15 - lane];
       }
     }
-    const int a_before = __shfl_sync(0xffffffffu, ia - va, warp), t_before = __shfl_sync(0xffffffffu, it - vt, warp);
-    const int a_all = __shfl_sync(0xffffffffu, ia, 31), t_all = __shfl_sync(0xffffffffu, it, 31);
-    const unsigned below = (1u << lane) - 1u;
-    const int t_rank = ties + t_before + __popc(mt & below);
-    const int t_taken = min(t_rank, need) - min(ties, need);   // border rows of this round before this one that stay
-    if (above || (tie && t_rank < need)) kept[out + a_before + __popc(ma & below) + t_taken] = a + i;
-    out += a_all + min(ties + t_all, need) - min(ties, need);
-    ties += t_all;
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int found = __ffs(__ballot_sync(0xffffffffu, lane < 16 && incl >= need)) - 1;
+    const int count = __shfl_sync(0xffffffffu, c, found);
+    need -= __shfl_sync(0xffffffffu, incl, found) - count;
+    prefix |= (unsigned)(15 - found) << shift;
+    mask |= 15u << shift;
+    if (need == count) break;          // all rows with this prefix stay
+  }
+  // Rows above the prefix stay, and the first `need` with it. A thread's counts
+  // of both in one word, scanned over the warp, the CTA and the CTAs before.
+  int out = p.first, ties = 0;
+  for (int round = 0; round < max(rounds, 1); ++round) {
+    if (rounds > 1) load(round);
+    unsigned own = 0;                  // above | ties << 16 (a round has at most 16384 rows)
+#pragma unroll
+    for (int k = 0; k < kSelKeys; ++k)
+      if (k < mine) own += (key[k] & mask) > prefix ? 1u : (key[k] & mask) == prefix ? 0x10000u : 0u;
+    unsigned incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    __syncthreads();                   // the warp sums of the round before have been read
+    if (lane == 31) wsum[warp] = (int)incl;
+    __syncthreads();
+    const unsigned wv = (unsigned)wsum[lane];
+    unsigned wincl = wv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned v = __shfl_up_sync(0xffffffffu, wincl, o);
+      if (lane >= o) wincl += v;
+    }
+    const unsigned all = __shfl_sync(0xffffffffu, wincl, 31);
+    const unsigned before = incl - own + __shfl_sync(0xffffffffu, wincl - wv, warp);
+    if (CL > 1 && round == 0) {        // totals of the CTAs before this one
+      int above_n = (int)(all & 0xffffu), tie_n = (int)(all >> 16);
+      for (int r2 = 1; r2 < rounds; ++r2) {   // a slice of several rounds counts them first
+        load(r2);
+        unsigned o2 = 0;
+#pragma unroll
+        for (int k = 0; k < kSelKeys; ++k)
+          if (k < mine) o2 += (key[k] & mask) > prefix ? 1u : (key[k] & mask) == prefix ? 0x10000u : 0u;
+        o2 = __reduce_add_sync(0xffffffffu, o2);
+        __syncthreads();
+        if (lane == 0) wsum[warp] = (int)o2;
+        __syncthreads();
+        const unsigned sum = __reduce_add_sync(0xffffffffu, (unsigned)wsum[lane]);
+        above_n += (int)(sum & 0xffffu);
+        tie_n += (int)(sum >> 16);
+      }
+      if (rounds > 1) load(0);
+      if (tid == 0) {
+        s_count[0] = above_n;
+        s_count[1] = tie_n;
+      }
+      cluster.sync();
+      for (int r = 0; r < rank; ++r) {
+        const int* cnt = cluster.map_shared_rank(s_count, r);
+        out += cnt[0];
+        ties += cnt[1];
+      }
+      out += min(ties, need);
+    }
+    int above_at = out + (int)(before & 0xffffu), tie_at = ties + (int)(before >> 16);
+    const int base = a + round * kSelRows + tid * kpt;
+#pragma unroll
+    for (int k = 0; k < kSelKeys; ++k) {
+      if (k >= mine) continue;
+      const unsigned v = key[k] & mask;
+      if (v > prefix || (v == prefix && tie_at < need))
+        kept[above_at + min(tie_at, need) - min(ties, need)] = base + k;
+      above_at += v > prefix;
+      tie_at += v == prefix;
+    }
+    const int tie_all = (int)(all >> 16);
+    out += (int)(all & 0xffffu) + min(ties + tie_all, need) - min(ties, need);
+    ties += tie_all;
   }
   if (CL > 1) cluster.sync();   // no CTA leaves while its counts may be read
 }
@@ -372,22 +426,24 @@ evict_gather_kernel(const EvictParams p) {
   const int8_t* from = (isv ? p.vc : p.kc) + (long long)bg * p.C * p.H;
   const float* sc = (isv ? p.vs : p.ks) + (long long)bg * p.nblk;
   int8_t* to = (isv ? p.vc_to : p.kc_to) + ((long long)bg * p.Cto + first) * p.H;
-  __shared__ float rs[256];
+  __shared__ float2 rs[256];       // scale of a row, and its ratio to the block's
   __shared__ float red[kGatherThreads / 32];
   const int* rows = p.kept + (long long)bg * p.keep + first;
   const int chunks = p.H / 16;
+  const SmallDiv div(chunks);
   uint4 ahead[kGatherAhead];
 #pragma unroll
   for (int k = 0; k < kGatherAhead; ++k) {
     const int i = k * kGatherThreads + tid;
+    const int r = div.quot(i);
     if (i < n * chunks)
-      ahead[k] = *reinterpret_cast<const uint4*>(from + (long long)rows[i / chunks] * p.H + 16 * (i % chunks));
+      ahead[k] = *reinterpret_cast<const uint4*>(from + (long long)rows[r] * p.H + 16 * (i - r * chunks));
   }
   float top = 0.f;
   for (int i = tid; i < n; i += kGatherThreads) {
     const int r = rows[i];
-    rs[i] = sc[r >> p.bs_log2];
-    top = fmaxf(top, rs[i]);
+    rs[i].x = sc[r >> p.bs_log2];
+    top = fmaxf(top, rs[i].x);
     if (!isv && p.w_to) p.w_to[(long long)bg * p.Cto + first + i] = p.w[(long long)bg * p.C + r];
   }
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -396,11 +452,12 @@ evict_gather_kernel(const EvictParams p) {
   top = red[0];
   for (int i = 1; i < kGatherThreads / 32; ++i) top = fmaxf(top, red[i]);
   if (tid == 0) (isv ? p.vs_to : p.ks_to)[(long long)bg * p.nblk_to + blockIdx.x] = top;
+  for (int i = tid; i < n; i += kGatherThreads) rs[i].y = top > 0.f ? __fdiv_rn(rs[i].x, top) : 0.f;   // a thread's own rows
+  __syncthreads();
   auto put = [&](int i, uint4 w) {
-    const int r = i / chunks, c = i - r * chunks;
-    const float s = rs[r];
+    const int r = div.quot(i), c = i - r * chunks;
+    const float s = rs[r].x, ratio = rs[r].y;
     if (s != top) {
-      const float ratio = top > 0.f ? __fdiv_rn(s, top) : 0.f;
       w = make_uint4(recode4(w.x, s, top, ratio), recode4(w.y, s, top, ratio), recode4(w.z, s, top, ratio),
                      recode4(w.w, s, top, ratio));
     }
@@ -412,7 +469,7 @@ evict_gather_kernel(const EvictParams p) {
     if (i < n * chunks) put(i, ahead[k]);
   }
   for (int i = kGatherAhead * kGatherThreads + tid; i < n * chunks; i += kGatherThreads)
-    put(i, *reinterpret_cast<const uint4*>(from + (long long)rows[i / chunks] * p.H + 16 * (i % chunks)));
+    put(i, *reinterpret_cast<const uint4*>(from + (long long)rows[div.quot(i)] * p.H + 16 * (i - div.quot(i) * chunks)));
 }
 
 }  // namespace
@@ -431,22 +488,9 @@ cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t st) {
   // A CTA for every kSelRows rows, up to the portable cluster size.
   int CL = 1;
   while (CL < 8 && (long long)CL * kSelRows < p.T) CL *= 2;
-  const long long per = ((p.T + CL - 1) / CL + 31) & ~31LL;
-  const size_t smem = (size_t)(per < kSelCache ? per : kSelCache) * sizeof(unsigned);
-  static bool done[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!done[dev]) {
-    e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCache * (int)sizeof(unsigned));
-    if (e != cudaSuccess) return e;
-    done[dev] = true;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.B * p.Nkv * CL));
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;

@@ -50,6 +50,15 @@ __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
   return *reinterpret_cast<float2*>(&dv);
 }
 
+// Packed fp32x2 sum: d = a + b per lane pair.
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  unsigned long long av = *reinterpret_cast<unsigned long long*>(&a);
+  unsigned long long bv = *reinterpret_cast<unsigned long long*>(&b);
+  unsigned long long dv;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(dv) : "l"(av), "l"(bv));
+  return *reinterpret_cast<float2*>(&dv);
+}
+
 // Maximum of three values (one instruction on sm_100 and later).
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;

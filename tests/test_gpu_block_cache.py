@@ -411,6 +411,8 @@ EVICT = {
     "keep_one": (2, 1, 16, 100, 16, 16, (100, 2), 1, 0, 0),
     "keep_more_than_there_is": (2, 2, 64, 100, 64, 100, (100, 50), 5000, 20, 4),
     "long": (1, 2, 128, 70000, 128, 4096, (69999,), 3000, 100, 8),
+    "two_ctas": (1, 1, 16, 40000, 64, 2048, (33001,), 2000, 1, 0),
+    "several_rounds": (1, 1, 16, 300000, 256, 8192, (299999,), 8000, 100, 3),
     "block_256": (2, 2, 256, 600, 256, 512, (600, 513), 300, 1, 0),
 }
 

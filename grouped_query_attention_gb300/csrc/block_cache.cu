@@ -223,15 +223,19 @@ __device__ __forceinline__ unsigned weight_key(float w) {
 constexpr int kSelKeys = 16;                        // consecutive rows a thread holds in registers
 constexpr int kSelRows = kSelThreads * kSelKeys;    // rows of a CTA at a time
 
+constexpr int kSelBins = 2048;                      // 11 bits a pass
+constexpr int kSelList = 512;                       // keys ranked by comparing each with each
+
 // One (b, g) per cluster of CL CTAs, each with an equal slice of the rows
-// between `first` and `recent`. A radix selection, four bits at a time from
-// the top, finds the key of the last row that stays and how many rows with
-// exactly that key do; it ends early once every row with the digits found so
-// far stays. Sixteen counters of a thread's keys fit 4-bit fields of a 64-bit
-// register (no shared atomics, whose conflicts took most of an 8-bit pass),
-// warps add them with integer reductions, CTAs over distributed shared memory.
-// Threads hold consecutive rows, so one scan places the rows that stay in
-// order. Bound: latency, 4 bytes a row.
+// between `first` and `recent`. A radix selection, 11 bits at a time from the
+// top, finds the key of the last row that stays and how many rows with exactly
+// that key do: counts in shared memory (the CTAs' added over distributed
+// shared memory), a scan over the bins. It ends once every row with the digits
+// found so far stays, or once at most 512 rows have them: those are ranked by
+// comparison. Threads hold consecutive rows in registers, so one scan places
+// the rows that stay in order. Bound: latency, 4 bytes a row. (Eight-bit
+// passes with a scan by one warp took 21 us on 8192 rows, four-bit passes with
+// counters in registers as much: their reductions cost what the atomics did.)
 __global__ void __launch_bounds__(kSelThreads)
 evict_select_kernel(const EvictParams p, int CL) {
   namespace cg = cooperative_groups;
@@ -272,62 +276,112 @@ evict_select_kernel(const EvictParams p, int CL) {
   };
   if (rounds <= 1) load(0);
 
-  __shared__ unsigned wcnt[kSelThreads / 32][16];
-  __shared__ int hist[2][16];          // the CTA's counts, by pass parity
-  __shared__ int wsum[kSelThreads / 32], s_count[2];
+  __shared__ int hist[2][kSelBins];    // the CTA's counts, by pass parity
+  __shared__ unsigned list[kSelList], all_list[kSelList];
+  __shared__ int wsum[kSelThreads / 32], s_count[2], s_list, s_need, s_bin_count;
+  __shared__ unsigned s_key;
+  auto group_sync = [&] {
+    if (CL > 1) cluster.sync(); else __syncthreads();
+  };
   unsigned prefix = 0, mask = 0;
-  for (int shift = 28, pass = 0; shift >= 0; shift -= 4, ++pass) {
-    unsigned c0 = 0, c1 = 0;           // lane i < 8: the warp's keys with digit 2 i, 2 i + 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kSelBins;
+    int* h = hist[pass & 1];
+    for (int i = tid; i < kSelBins; i += kSelThreads) h[i] = 0;
+    if (tid == 0) s_list = 0;
+    __syncthreads();
     for (int round = 0; round < max(rounds, 1); ++round) {
       if (rounds > 1) load(round);
-      unsigned long long acc[2] = {0ull, 0ull};
 #pragma unroll
-      for (int k = 0; k < kSelKeys; ++k)
-        if (k < mine && (key[k] & mask) == prefix) acc[k >> 3] += 1ull << (4 * ((key[k] >> shift) & 15u));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        unsigned f = 0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const unsigned v = (unsigned)(acc[h] >> (8 * i)) & 0xffu;
-          f += (v & 15u) | (v >> 4) << 16;
-        }
-        f = __reduce_add_sync(0xffffffffu, f);
-        if (lane == i) {
-          c0 += f & 0xffffu;
-          c1 += f >> 16;
+      for (int k = 0; k < kSelKeys; ++k) {
+        if (k >= kpt) continue;        // uniform
+        const bool in = k < mine && (key[k] & mask) == prefix;
+        const unsigned ins = __ballot_sync(0xffffffffu, in);
+        if (ins == 0) continue;
+        const unsigned digit = (key[k] >> shift) & (unsigned)(bins - 1);
+        const unsigned one = __shfl_sync(0xffffffffu, digit, __ffs(ins) - 1);
+        if (__all_sync(0xffffffffu, !in || digit == one)) {   // ties: one count for the warp
+          if (lane == 0) atomicAdd(&h[one], __popc(ins));
+        } else if (in) {
+          atomicAdd(&h[digit], 1);
         }
       }
     }
-    if (lane < 8) *reinterpret_cast<uint2*>(&wcnt[warp][2 * lane]) = make_uint2(c0, c1);
-    __syncthreads();
-    if (warp < 16) {
-      const unsigned c = __reduce_add_sync(0xffffffffu, wcnt[lane][warp]);
-      if (lane == 0) hist[pass & 1][warp] = (int)c;
-    }
-    if (CL > 1) cluster.sync(); else __syncthreads();
-    // Every warp: counts of the digits from the top (lane l: digit 15 - l), and
-    // the one at which `need` rows are reached.
-    int c = 0;
-    if (lane < 16) {
-      if (CL > 1) {
-        for (int r = 0; r < CL; ++r) c += cluster.map_shared_rank(&hist[pass & 1][0], r)[15 - lane];
-      } else {
-        c = hist[pass & 1][15 - lane];
+    group_sync();
+    // Thread t: bins - 1 - 2 t and the one below it; an inclusive scan from the top.
+    int c[2] = {0, 0};
+    const int top = bins - 1 - 2 * tid;
+    if (top > 0) {
+      for (int r = 0; r < CL; ++r) {
+        const int* o = CL > 1 ? cluster.map_shared_rank(h, r) : h;
+        c[0] += o[top];
+        c[1] += o[top - 1];
       }
     }
-    int incl = c;
+    int incl = c[0] + c[1];
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) {
+    for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    const int found = __ffs(__ballot_sync(0xffffffffu, lane < 16 && incl >= need)) - 1;
-    const int count = __shfl_sync(0xffffffffu, c, found);
-    need -= __shfl_sync(0xffffffffu, incl, found) - count;
-    prefix |= (unsigned)(15 - found) << shift;
-    mask |= 15u << shift;
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    int wv = wsum[lane], wincl = wv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, wincl, o);
+      if (lane >= o) wincl += v;
+    }
+    incl += __shfl_sync(0xffffffffu, wincl - wv, warp);
+    const int before = incl - c[0] - c[1];
+    if (before < need && need <= incl) {   // one thread
+      const int second = need > before + c[0];
+      s_key = (unsigned)(top - second);
+      s_need = need - before - (second ? c[0] : 0);
+      s_bin_count = c[second];
+    }
+    __syncthreads();
+    prefix |= s_key << shift;
+    mask |= (unsigned)(bins - 1) << shift;
+    need = s_need;
+    const int count = s_bin_count;
+    __syncthreads();
     if (need == count) break;          // all rows with this prefix stay
+    if (count <= kSelList && pass < 2) {
+      for (int round = 0; round < max(rounds, 1); ++round) {
+        if (rounds > 1) load(round);
+#pragma unroll
+        for (int k = 0; k < kSelKeys; ++k)
+          if (k < mine && (key[k] & mask) == prefix) list[atomicAdd(&s_list, 1)] = key[k];   // any order serves
+      }
+      group_sync();
+      int m = 0;                       // every CTA takes all the cluster's keys
+      for (int r = 0; r < CL; ++r) {
+        const unsigned* o = CL > 1 ? cluster.map_shared_rank(list, r) : list;
+        const int nr = CL > 1 ? *cluster.map_shared_rank(&s_list, r) : s_list;
+        for (int i = tid; i < nr; i += kSelThreads) all_list[m + i] = o[i];
+        m += nr;
+      }
+      __syncthreads();
+      if (tid < m) {
+        const unsigned v = all_list[tid];
+        int greater = 0, equal = 0;
+        for (int i = 0; i < m; ++i) {
+          greater += all_list[i] > v;
+          equal += all_list[i] == v;
+        }
+        if (greater < need && need <= greater + equal) {   // equal keys write equal values
+          s_key = v;
+          s_need = need - greater;
+        }
+      }
+      group_sync();                    // (no CTA reuses its list while it is read)
+      prefix = s_key;
+      mask = 0xffffffffu;
+      need = s_need;
+      __syncthreads();
+      break;
+    }
   }
   // Rows above the prefix stay, and the first `need` with it. A thread's counts
   // of both in one word, scanned over the warp, the CTA and the CTAs before.

@@ -129,10 +129,10 @@ __device__ long long all_units(const BlockParams& p) {
   return sum;
 }
 
-// Walk over a worker's units: cell (b, gr = g * nrt + rt) and unit `off` of
-// the sequence's units; `left` units of the share remain.
+// Walk over a worker's units: range (b, g, rt) and unit `off` of the sequence's
+// units; `left` units of the share remain. Divisions only where a range begins.
 struct Walk {
-  int b, gr, off, nt, t0, total, fresh, hi;
+  int b, g, rt, bg, off, nt, t0, total, fresh, hi;
   long long left;
 
   __device__ void enter_seq(const BlockParams& p) {
@@ -143,21 +143,25 @@ struct Walk {
   __device__ void settle(const BlockParams& p) {
     while (left > 0) {
       int lo;
-      tile_units(p, total, fresh, t0, nt, gr % p.nrt, &lo, &hi);
+      tile_units(p, total, fresh, t0, nt, rt, &lo, &hi);
       if (off < lo) {
         left -= lo - off;
         off = lo;
-        if (left <= 0) return;
+        if (left <= 0) break;
       }
-      if (off < hi) return;
+      if (off < hi) break;
       left -= nt + kBlockRangeCost - off;
       off = 0;
-      if (++gr == p.Nkv * p.nrt) {
-        gr = 0;
-        ++b;
-        if (left > 0) enter_seq(p);
+      if (++rt == p.nrt) {
+        rt = 0;
+        if (++g == p.Nkv) {
+          g = 0;
+          ++b;
+          if (left > 0) enter_seq(p);
+        }
       }
     }
+    bg = b * p.Nkv + g;
   }
   // A share of n units from unit u on (u below the sum of all); one warp.
   __device__ void start(const BlockParams& p, long long u, long long n) {
@@ -180,14 +184,20 @@ struct Walk {
       u -= __shfl_sync(0xffffffffu, s, 31);
     }
     seq_units(p, b, &total, &fresh, &t0, &nt);
-    gr = (int)(u / (nt + kBlockRangeCost));
-    off = (int)(u % (nt + kBlockRangeCost));
+    const int gr = (int)(u / (nt + kBlockRangeCost));
+    off = (int)(u - (long long)gr * (nt + kBlockRangeCost));
+    g = gr / p.nrt;
+    rt = gr - g * p.nrt;
     settle(p);
   }
-  __device__ void next(const BlockParams& p) {
+  // The next unit; true when it is not of the same range (or there is none).
+  __device__ bool next(const BlockParams& p) {
     --left;
     ++off;
-    if (off >= hi || left <= 0) settle(p);
+    if (off < hi && left > 0) return false;
+    const bool ends = off >= hi || left <= 0;
+    settle(p);
+    return ends;
   }
 };
 
@@ -307,9 +317,8 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
     if (ld.left > 0 && (p.withhold_tile < 0 || fetched != p.withhold_tile)) {
       ++fetched;
       const int j0 = (ld.t0 + ld.off) * kBlockUnit;
-      const int bg = ld.b * p.Nkv + ld.gr / p.nrt;
       if (lane == 0) {
-        const int row = bg * p.C + j0;   // below 2^31 (checked by the host)
+        const int row = ld.bg * p.C + j0;   // below 2^31 (checked by the host)
         tc::mbar_arrive_tx(&ctl.full[s], 2 * kTileBytes);
 #pragma unroll
         for (int x = 0; x < (HP > 128 ? 2 : 1); ++x) {
@@ -319,7 +328,7 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
       }
       if (lane < 4) {   // scales of the two 16-key groups; 0 behind the last row
         const int j = j0 + 16 * (lane & 1);
-        const float* src = (lane < 2 ? p.ks : p.vs) + (long long)bg * p.nblk;
+        const float* src = (lane < 2 ? p.ks : p.vs) + (long long)ld.bg * p.nblk;
         const bool on = j < ld.total;
         cp4((uint32_t)__cvta_generic_to_shared(&ctl.sc[s][lane]), src + (on ? j >> p.bs_log2 : 0), on);
       }
@@ -338,17 +347,21 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
   float lr[kHalf ? NT : 1][2];            // fp16: the sum of the probabilities as the product with V has them
   int wexp = -200;              // the V scales enter as vs 2^-wexp
   bool fresh_piece = true;
+  int r0 = 0, past = 0, pos_lo = 0, pos_hi = 0;   // of the piece: first row, cached rows, positions of its first and last row
   int stage = 0;
   uint32_t parity = 0;
   while (cp.left > 0) {
-    const int b = cp.b, g = cp.gr / p.nrt, rt = cp.gr % p.nrt;
-    const int j0 = (cp.t0 + cp.off) * kBlockUnit, past = cp.total - cp.fresh;
+    const int j0 = (cp.t0 + cp.off) * kBlockUnit;
     __syncwarp();                                  // the other stage has been read by every lane
     fetch(stage ^ 1);
     if (fresh_piece) {
       fresh_piece = false;
       float up[NT];
-      load_queries<T, HP, NT>(p, b, g, rt, qf, up);
+      load_queries<T, HP, NT>(p, cp.b, cp.g, cp.rt, qf, up);
+      r0 = cp.rt * p.rt_rows;
+      past = cp.total - cp.fresh;
+      pos_lo = past + r0 / p.G;
+      pos_hi = past + (r0 + 8 * NT - 1) / p.G;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -421,9 +434,7 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
           if (!PLAIN && p.softcap > 0.f) s[kk][n][e] = p.softcap * kLog2e * tanhf(s[kk][n][e] / p.softcap);
         }
       }
-    const int r0 = rt * p.rt_rows;
-    if (j0 + kBlockUnit - 1 > past + r0 / p.G ||
-        (p.window >= 0 && j0 < past + (r0 + 8 * NT - 1) / p.G - p.window)) {   // a mask border crosses the unit
+    if (j0 + kBlockUnit - 1 > pos_lo || (p.window >= 0 && j0 < pos_hi - p.window)) {   // a mask border crosses the unit
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -439,7 +450,7 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
         }
     }
     if (!PLAIN && p.stash) {
-      float* dst = p.stash + (((long long)b * p.Nkv + g) * p.stash_ld + j0 + gq) * p.stash_rows + 2 * t;
+      float* dst = p.stash + ((long long)cp.bg * p.stash_ld + j0 + gq) * p.stash_rows + 2 * t;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
         if (8 * n + 2 * t < p.stash_rows) {
@@ -583,13 +594,11 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
     }
     stage ^= 1;
     if (stage == 0) parity ^= 1;
-    const int range = cp.b * p.Nkv * p.nrt + cp.gr;
-    cp.next(p);
-    if (cp.left > 0 && cp.b * p.Nkv * p.nrt + cp.gr == range) continue;
+    const long long slot = worker + (long long)cp.bg * p.nrt + cp.rt;
+    if (!cp.next(p)) continue;
 
     // ---- the piece ends: (m, l) and O of its rows into slot worker + range
     fresh_piece = true;
-    const long long slot = worker + range;
     const float upw = __int_as_float((127 + wexp) << 23);   // O is in units of 2^wexp
     if constexpr (FLUSH) {
 #pragma unroll

@@ -802,9 +802,12 @@ cudaError_t launch_one(const BlockParams& p, cudaStream_t st) {
   const uint64_t crows = (uint64_t)p.B * p.Nkv * p.C;
   if ((e = encode_u8_2d(&mk, p.kc, crows, kHD, kHD, kHD, kBN)) != cudaSuccess) return e;
   if ((e = encode_u8_2d(&mv, p.vc, crows, kHD, kHD, kHD, kBN)) != cudaSuccess) return e;
-  auto encode = F32 ? encode_f32_query_sw128 : encode_fp16_query_sw128;
-  if ((e = encode(&mq, p.q, p.B, p.S, p.N, (uint32_t)p.G)) != cudaSuccess) return e;
-  if ((e = encode(&mo, p.out, p.B, p.S, p.N, (uint32_t)p.G)) != cudaSuccess) return e;
+  auto encode = [&](CUtensorMap* m, const void* base) {
+    return F32 ? encode_f32_query_sw128(m, base, p.B, p.S, p.N, (uint32_t)p.G)
+               : encode_fp16_query_sw128(m, base, p.B, p.S, p.N, (uint32_t)p.G);
+  };
+  if ((e = encode(&mq, p.q)) != cudaSuccess) return e;
+  if ((e = encode(&mo, p.out)) != cudaSuccess) return e;
   const unsigned nqb = (unsigned)((p.S * p.G + 2 * kBM - 1) / (2 * kBM)), nbg = (unsigned)(p.B * p.Nkv);
   return launch_dependent(p.k != nullptr, kern, p.qb_major ? dim3(nbg, nqb) : dim3(nqb, nbg), kThreads, (size_t)smem, st,
                           p, mq, mo, mk, mv);

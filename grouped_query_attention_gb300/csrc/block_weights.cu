@@ -4,13 +4,13 @@
 // prefill left in the workspace (log2 domain).
 //
 // CTA = 128 keys of one KV head. Keys are the M side of S^T = K Q^T (128 keys
-// x 128 query rows a tile), so a key is a tensor-memory lane and its sum stays
+// x 64 query rows a tile), so a key is a tensor-memory lane and its sum stays
 // in one thread: no reduction across threads, no atomics, and the K scale is
-// one number per thread. Query tiles arrive by TMA (two stages); two softmax
-// groups take alternate tiles, each with its own tensor-memory buffer.
+// one number per thread. The key tile is the A operand and stays in tensor
+// memory (64 columns, beside three S buffers of 64), so that a tile's products
+// read the query rows alone from shared memory. Query tiles arrive by TMA (four
+// stages); two softmax groups take alternate tiles. Two CTAs share an SM.
 //
-// Bound: exp2, one per visible pair (16 a clock and SM: 1024 cycles a tile
-// against 512 of MMAs). Two CTAs share an SM (256 tensor-memory columns each).
 // Causal: key tile 0 meets every query row, the last few; the longest start first.
 #include <cuda_fp16.h>
 
@@ -26,20 +26,22 @@ namespace {
 using namespace tc;
 
 constexpr int kKeys = 128;                     // keys of a CTA
-constexpr int kRows = 128;                     // query rows of a tile
+constexpr int kRows = 64;                      // query rows of a tile
+constexpr int kStages = 4;                     // query tiles in shared memory
+constexpr int kBufs = 3;                       // S buffers in tensor memory
 constexpr int kHD = 128;
 constexpr int kThreads = 384;
 constexpr int kSoftWarp0 = 4;
-constexpr uint32_t kBox = 128u * 128u;
+constexpr uint32_t kBox = kRows * 128u;        // 64 rows x 128 bytes
 constexpr uint32_t kTile = 2u * kBox;
-constexpr uint32_t kIdS = idesc_f16(128, 128, 0, 0);
+constexpr uint32_t kIdS = idesc_f16(kKeys, kRows, 0, 0);
 
 struct __align__(1024) WtSmem {
-  uint8_t k[kTile];                            // fp16 codes, K-major
-  uint8_t q[2][kTile];
-  float nl[2][kRows];                          // -lse of the tile's rows
+  uint8_t q[kStages][kTile];
+  float nl[kBufs][kRows];                      // -lse of the tile's rows
   float part[kKeys];                           // the second group's sums
-  uint64_t q_full[2], q_empty[2], nl_full[2], nl_empty[2], s_full[2], s_empty[2];
+  uint64_t q_full[kStages], q_empty[kStages];
+  uint64_t nl_full[kBufs], s_full[kBufs], s_empty[kBufs];
   uint64_t drain;
   uint32_t tmem;
   int abort;
@@ -75,11 +77,12 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
 
   if (warp == 1) tmem_alloc(&sm.tmem, 256);
   if (tid == 0) {
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < kStages; ++t) {
       mbar_init(&sm.q_full[t], 1);
       mbar_init(&sm.q_empty[t], 1);
+    }
+    for (int t = 0; t < kBufs; ++t) {
       mbar_init(&sm.nl_full[t], 1);
-      mbar_init(&sm.nl_empty[t], 4);
       mbar_init(&sm.s_full[t], 1);
       mbar_init(&sm.s_empty[t], 4);
     }
@@ -87,23 +90,23 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
     sm.abort = 0;
     mbar_fence_init();
   }
-  // The key tile: rows behind the sequence are left as zeros.
-  for (int x = tid; x < kKeys * 8; x += kThreads) {
-    const int row = x >> 3, j = x & 7;
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (j0 + row < total)
-      w = *reinterpret_cast<const uint4*>(p.kc + ((long long)bg * p.C + j0 + row) * kHD + 16 * j);
-    uint32_t h[8];
-    codes16(w, h);
-    uint8_t* bx = sm.k + (j >> 2) * kBox;
-    *reinterpret_cast<uint4*>(bx + sw128_offset(row, 2 * (j & 3))) = make_uint4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<uint4*>(bx + sw128_offset(row, 2 * (j & 3) + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
-  }
-  fence_async_smem();   // key tile (generic stores) -> async proxy: the MMAs read it
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem;
+  const uint32_t tmem = sm.tmem, tmem_k = tmem + kBufs * kRows;
+  // The key tile as fp16 pairs, a key per lane; rows behind the sequence are zeros.
+  if (warp >= kSoftWarp0) {
+    const int row = j0 + (warp & 3) * 32 + lane, half = (warp - kSoftWarp0) >> 2;
+    const uint4* src = reinterpret_cast<const uint4*>(p.kc + ((long long)bg * p.C + row) * kHD) + 4 * half;
+    uint32_t h[32];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) codes16(row < total ? src[k] : make_uint4(0u, 0u, 0u, 0u), h + 8 * k);
+    tmem_st32(tmem_k + ((uint32_t)((warp & 3) * 32) << 16) + 32 * half, h);
+    tmem_st_wait();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
 
   if (warp == 0) {
     // ================================================================ TMA: query tiles
@@ -111,37 +114,38 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
     int n = 0;
     for (; n < ntiles && ok; ++n) {
       if (n == p.withhold_tile) break;   // testing: this tile is never copied, the waits for it expire
-      ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_empty[n & 1], ((uint32_t)(n >> 1) & 1u) ^ 1u, p.wait_budget) && !aborted(sm));
+      ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_empty[n % kStages], ((uint32_t)(n / kStages) & 1u) ^ 1u, p.wait_budget) && !aborted(sm));
       if (ok && elect_one()) {
-        mbar_arrive_tx(&sm.q_full[n & 1], kTile);
+        mbar_arrive_tx(&sm.q_full[n % kStages], kTile);
         for (int k = 0; k < 2; ++k)
-          tma_load_4d(sm.q[n & 1] + k * kBox, &tmq, 64 * k, g * p.G, i_lo + n * (kRows / p.G), b, &sm.q_full[n & 1]);
+          tma_load_4d(sm.q[n % kStages] + k * kBox, &tmq, 64 * k, g * p.G + n * kRows % p.G, i_lo + n * kRows / p.G, b,
+                      &sm.q_full[n % kStages]);
       }
       __syncwarp();
     }
     if (!ok && lane == 0) set_abort(p, sm);
     if (!ok) --n;
     // No copy of this CTA may still be landing when it exits.
-    for (int x = n > 2 ? n - 2 : 0; x < n; ++x) mbar_wait(&sm.q_full[x & 1], (uint32_t)(x >> 1) & 1u, p.wait_budget);
+    for (int x = n > kStages ? n - kStages : 0; x < n; ++x)
+      mbar_wait(&sm.q_full[x % kStages], (uint32_t)(x / kStages) & 1u, p.wait_budget);
   } else if (warp == 1) {
     // ================================================================ MMA issuer
-    const uint64_t dk = desc_kmajor_sw128(smem_addr(sm.k)), dq = desc_kmajor_sw128(smem_addr(sm.q[0]));
+    const uint64_t dq = desc_kmajor_sw128(smem_addr(sm.q[0]));
     bool ok = true;
     for (int n = 0; n < ntiles && ok; ++n) {
-      const int bf = n & 1;
-      const uint32_t par = (uint32_t)(n >> 1) & 1u;
-      ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full[bf], par, p.wait_budget) &&
-                                       mbar_wait(&sm.s_empty[bf], par ^ 1u, p.wait_budget) && !aborted(sm));
+      const int st = n % kStages, bf = n % kBufs;
+      ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full[st], (uint32_t)(n / kStages) & 1u, p.wait_budget) &&
+                                       mbar_wait(&sm.s_empty[bf], ((uint32_t)(n / kBufs) & 1u) ^ 1u, p.wait_budget) &&
+                                       !aborted(sm));
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
-        const uint64_t b0 = dq + (uint64_t)(bf * (int)(kTile >> 4));
+        const uint64_t b0 = dq + (uint64_t)(st * (int)(kTile >> 4));
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          const uint64_t off = (uint64_t)((ks >> 2) * 1024 + (ks & 3) * 2);
-          mma_f16_ss(tmem + bf * 128, dk + off, b0 + off, kIdS, ks > 0);
-        }
-        mma_commit(&sm.q_empty[bf]);
+        for (int ks = 0; ks < 8; ++ks)
+          mma_f16_ts(tmem + bf * kRows, tmem_k + ks * 8, b0 + (uint64_t)((ks >> 2) * (int)(kBox >> 4) + (ks & 3) * 2), kIdS,
+                     ks > 0);
+        mma_commit(&sm.q_empty[st]);
         mma_commit(&sm.s_full[bf]);
       }
       __syncwarp();
@@ -155,24 +159,21 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
   } else if (warp == 2) {
     // ================================================================ -lse of the rows, a tile ahead
     const float* lse = p.lse + (long long)bg * p.S * p.G;
-    auto load = [&](int n, float* v) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = rows0 + n * kRows + 4 * lane + i;
-        v[i] = r < rows1 ? -lse[r] : 0.f;   // rows from rows1 on are masked
-      }
+    auto load = [&](int n) -> float2 {   // rows from rows1 on are masked
+      const int r = rows0 + n * kRows + 2 * lane;
+      return make_float2(r < rows1 ? -lse[r] : 0.f, r + 1 < rows1 ? -lse[r + 1] : 0.f);
     };
-    float next[4];
-    load(0, next);
+    float2 next = load(0);
     bool ok = true;
     for (int n = 0; n < ntiles && ok; ++n) {
-      float v[4] = {next[0], next[1], next[2], next[3]};
-      if (n + 1 < ntiles) load(n + 1, next);
-      ok = __all_sync(0xffffffffu, mbar_wait(&sm.nl_empty[n & 1], ((uint32_t)(n >> 1) & 1u) ^ 1u, p.wait_budget) && !aborted(sm));
+      const float2 v = next;
+      if (n + 1 < ntiles) next = load(n + 1);
+      // The buffer's last readers are those of its S.
+      ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_empty[n % kBufs], ((uint32_t)(n / kBufs) & 1u) ^ 1u, p.wait_budget) && !aborted(sm));
       if (!ok) break;
-      *reinterpret_cast<float4*>(&sm.nl[n & 1][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float2*>(&sm.nl[n % kBufs][2 * lane]) = v;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.nl_full[n & 1]);
+      if (lane == 0) mbar_arrive(&sm.nl_full[n % kBufs]);
     }
     if (!ok && lane == 0) set_abort(p, sm);
   }
@@ -181,7 +182,6 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
   if (warp >= kSoftWarp0) {
     // ================================================================ sums of one key
     const int grp = (warp - kSoftWarp0) >> 2;
-    const uint32_t s_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16) + grp * 128;
     const float ks = j < total ? p.ks[(long long)bg * p.nblk + (j >> p.bs_log2)] : 0.f;
     const float kk = ks * p.scale * (CAP ? 1.f / p.softcap : kLog2e), c2 = p.softcap * kLog2e;
     const float2 kk2 = make_float2(kk, kk);
@@ -190,9 +190,10 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
     const int r_hi = j < total ? (p.window >= 0 ? min(rows1, (int)min((long long)(j - past) + p.window + 1, (long long)fresh) * p.G) : rows1) : 0;
     bool ok = true;
     for (int n = grp; n < ntiles && ok; n += 2) {
-      const uint32_t par = (uint32_t)(n >> 1) & 1u;
-      ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[grp], par, p.wait_budget) &&
-                                       mbar_wait(&sm.nl_full[grp], par, p.wait_budget) && !aborted(sm));
+      const int bf = n % kBufs;
+      const uint32_t par = (uint32_t)(n / kBufs) & 1u, s_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16) + bf * kRows;
+      ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[bf], par, p.wait_budget) &&
+                                       mbar_wait(&sm.nl_full[bf], par, p.wait_budget) && !aborted(sm));
       if (!ok) break;
       tc_fence_after();
       const int r0 = rows0 + n * kRows;
@@ -216,7 +217,7 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
           constexpr int MODE = decltype(m)::value;
 #pragma unroll
           for (int e4 = 0; e4 < 32; e4 += 4) {
-            const float4 nl = *reinterpret_cast<const float4*>(&sm.nl[grp][32 * c + e4]);
+            const float4 nl = *reinterpret_cast<const float4*>(&sm.nl[bf][32 * c + e4]);
             const float nv[4] = {nl.x, nl.y, nl.z, nl.w};
 #pragma unroll
             for (int e = e4; e < e4 + 4; e += 2) {
@@ -254,10 +255,7 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
       sum += acc.x + acc.y;
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sm.s_empty[grp]);
-        mbar_arrive(&sm.nl_empty[grp]);
-      }
+      if (lane == 0) mbar_arrive(&sm.s_empty[bf]);
     }
     if (!ok && lane == 0) set_abort(p, sm);
     if (grp == 1) sm.part[key] = sum;
@@ -287,7 +285,7 @@ cudaError_t launch_one(const BlockParams& p, cudaStream_t st) {
     done[dev] = true;
   }
   CUtensorMap mq;
-  if ((e = encode_fp16_query_sw128(&mq, p.q, p.B, p.S, p.N, (uint32_t)p.G)) != cudaSuccess) return e;
+  if ((e = encode_fp16_query_sw128(&mq, p.q, p.B, p.S, p.N, (uint32_t)p.G, kRows)) != cudaSuccess) return e;
   const dim3 grid((unsigned)(p.B * p.Nkv), (unsigned)((p.T + kKeys - 1) / kKeys));
   return launch_dependent(true, block_weights_tc_kernel<CAP>, grid, kThreads, (size_t)smem, st, p, mq);
 }

@@ -52,13 +52,13 @@ cudaError_t encode_f32_2d(CUtensorMap* map, const void* base, uint64_t rows, uin
 }
 
 cudaError_t encode_fp16_query_sw128(CUtensorMap* map, const void* base, uint64_t B, uint64_t S, uint64_t N,
-                                    uint32_t G) {
+                                    uint32_t G, uint32_t rows) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   const uint64_t H = 128;
   const cuuint64_t dims[4] = {H, N, S, B};
   const cuuint64_t strides[3] = {H * 2, N * H * 2, S * N * H * 2};
-  const cuuint32_t box[4] = {64, G, 128 / G, 1};
+  const cuuint32_t box[4] = {64, G < rows ? G : rows, G < rows ? rows / G : 1, 1};
   const cuuint32_t estride[4] = {1, 1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(base), dims, strides, box, estride,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

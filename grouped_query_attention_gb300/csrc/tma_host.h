@@ -15,12 +15,12 @@ cudaError_t encode_fp16_2d_sw128(CUtensorMap* map, const void* base, uint64_t ro
                                  uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows);
 
 // 4D map of a (B, S, N, 128) fp16 query tensor (BSH layout, head size 128)
-// with the 128-byte swizzle: boxes of 64 dims x G heads x 128/G positions x 1
-// batch land as 128 rows of 128 bytes in (position, head) order, the layout of
-// a 64-column K-major MMA operand box; positions past S read as zero.
-// G must divide 128.
+// with the 128-byte swizzle: boxes of 64 dims x G heads x rows/G positions x 1
+// batch land as `rows` rows of 128 bytes in (position, head) order, the layout
+// of a 64-column K-major MMA operand box; positions past S read as zero.
+// G must divide 128; a box of fewer rows than G holds that many heads of one position.
 cudaError_t encode_fp16_query_sw128(CUtensorMap* map, const void* base, uint64_t B, uint64_t S, uint64_t N,
-                                    uint32_t G);
+                                    uint32_t G, uint32_t rows = 128);
 
 // 4D map of a (B, S, N, 128) fp32 query tensor with the 128-byte swizzle:
 // boxes of 32 dims x G heads x 128/G positions x 1 batch land as 128 rows of

@@ -199,11 +199,11 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
       const int r0 = rows0 + n * kRows;
       const int lo = r_lo - r0, hi = r_hi - r0;   // visible columns [lo, hi)
       const bool full = __all_sync(0xffffffffu, lo <= 0 && hi >= kRows);
-      float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int c = 0; c < kRows / 32; ++c) {
+      float2 acc = make_float2(0.f, 0.f), acc2 = make_float2(0.f, 0.f);
+#pragma unroll 1
+      for (int c = 0; c < kRows; c += 32) {
         uint32_t x[32];
-        tmem_ld32(s_addr + 32 * c, x);
+        tmem_ld32(s_addr + c, x);
         tmem_ld_wait();
         int mode = 0;
         if constexpr (CAP) {
@@ -213,11 +213,11 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
           a *= kk;
           mode = __all_sync(0xffffffffu, !(a > kCapLow)) ? 3 : __all_sync(0xffffffffu, !(a > kCapHigh)) ? 7 : 9;
         }
-        auto add = [&](auto m) {
+        auto add = [&](auto m, auto whole) {
           constexpr int MODE = decltype(m)::value;
 #pragma unroll
           for (int e4 = 0; e4 < 32; e4 += 4) {
-            const float4 nl = *reinterpret_cast<const float4*>(&sm.nl[bf][32 * c + e4]);
+            const float4 nl = *reinterpret_cast<const float4*>(&sm.nl[bf][c + e4]);
             const float nv[4] = {nl.x, nl.y, nl.z, nl.w};
 #pragma unroll
             for (int e = e4; e < e4 + 4; e += 2) {
@@ -236,22 +236,29 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
                   arg = ffma2(u, cap_fit<MODE>(z, c2), n2);
                 }
               }
-              if (!full) {
-                arg.x = 32 * c + e >= lo && 32 * c + e < hi ? arg.x : -INFINITY;
-                arg.y = 32 * c + e + 1 >= lo && 32 * c + e + 1 < hi ? arg.y : -INFINITY;
+              if constexpr (!decltype(whole)::value) {
+                arg.x = c + e >= lo && c + e < hi ? arg.x : -INFINITY;
+                arg.y = c + e + 1 >= lo && c + e + 1 < hi ? arg.y : -INFINITY;
               }
-              acc = ffma2(make_float2(ex2(arg.x), ex2(arg.y)), make_float2(1.f, 1.f), acc);
+              const float2 w = make_float2(ex2(arg.x), ex2(arg.y));
+              if (e & 2) acc2 = fadd2(acc2, w);
+              else acc = fadd2(acc, w);
             }
           }
         };
-        if constexpr (CAP) {
-          if (mode == 3) add(std::integral_constant<int, 3>());
-          else if (mode == 7) add(std::integral_constant<int, 7>());
-          else add(std::integral_constant<int, 9>());
-        } else {
-          add(std::integral_constant<int, 0>());
-        }
+        auto pick = [&](auto whole) {
+          if constexpr (CAP) {
+            if (mode == 3) add(std::integral_constant<int, 3>(), whole);
+            else if (mode == 7) add(std::integral_constant<int, 7>(), whole);
+            else add(std::integral_constant<int, 9>(), whole);
+          } else {
+            add(std::integral_constant<int, 0>(), whole);
+          }
+        };
+        if (full) pick(std::true_type());
+        else pick(std::false_type());
       }
+      acc = fadd2(acc, acc2);
       sum += acc.x + acc.y;
       tc_fence_before();
       __syncwarp();

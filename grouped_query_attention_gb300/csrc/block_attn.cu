@@ -814,23 +814,42 @@ block_merge_kernel(const BlockParams p, long long row_blocks, int weight_chunks,
   units_of(p, total, fresh, &t0, &nt);
   const long long at0 = (long long)bg * p.C;
   const float* st = p.stash + (long long)bg * p.stash_ld * rs;
-#pragma unroll 4
-  for (int k = 0; k < keys / THREADS; ++k) {
-    const int j = j0 + k * THREADS + tid;
-    if (j >= total) break;
-    float w = p.past_w && j < total - fresh ? p.past_w[at0 + j] : 0.f;
-    if (j >= t0 * kBlockUnit) {
-      const float* sj = st + (long long)j * rs;
-      int r = 0;
-      if ((rs & 3) == 0) {
-        for (; r + 4 <= nrows; r += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(sj + r);
-          w += (ex2(v.x + nl[r]) + ex2(v.y + nl[r + 1])) + (ex2(v.z + nl[r + 2]) + ex2(v.w + nl[r + 3]));
-        }
-      }
-      for (; r < nrows; ++r) w += ex2(sj[r] + nl[r]);
+  const int jend = min(total, j0 + keys);
+  // Four keys of a thread at a time: their loads are under way together.
+  for (int j = j0 + tid; j < jend; j += 4 * THREADS) {
+    float w[4];
+    const float* sj[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int ju = j + u * THREADS;
+      w[u] = p.past_w && ju < min(jend, total - fresh) ? p.past_w[at0 + ju] : 0.f;
+      sj[u] = ju < jend && ju >= t0 * kBlockUnit ? st + (long long)ju * rs : nullptr;   // keys before t0: no scores
     }
-    p.present_w[at0 + j] = w;
+    int r = 0;
+    if ((rs & 3) == 0) {
+      for (; r + 4 <= nrows; r += 4) {
+        float4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (sj[u]) v[u] = *reinterpret_cast<const float4*>(sj[u] + r);
+        const float4 n = make_float4(nl[r], nl[r + 1], nl[r + 2], nl[r + 3]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (sj[u]) w[u] += (ex2(v[u].x + n.x) + ex2(v[u].y + n.y)) + (ex2(v[u].z + n.z) + ex2(v[u].w + n.w));
+      }
+    }
+    for (; r < nrows; ++r) {
+      float v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (sj[u]) v[u] = sj[u][r];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (sj[u]) w[u] += ex2(v[u] + nl[r]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (j + u * THREADS < jend) p.present_w[at0 + j + u * THREADS] = w[u];
   }
 }
 

@@ -16,6 +16,9 @@ from . import capi
 # The current stream's handle without a Stream object (2 us less per call), where torch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+# Likewise the current device and whether a graph is being captured (asked once a CUDA tensor is in hand).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
 
 _DTYPE_CODE = {torch.float32: capi.GQA_F32, torch.float16: capi.GQA_F16, torch.int8: capi.GQA_I8,
                torch.uint8: capi.GQA_U8, torch.int32: capi.GQA_I32, torch.bfloat16: capi.GQA_BF16}
@@ -75,16 +78,16 @@ class BlockCacheOps:
         self._block_calls: dict[str, _Bound] = {}
         self._block_ws: dict[tuple[int, int], torch.Tensor] = {}
         self._block_status: dict[int, torch.Tensor] = {}
+        self._block_status_ptr: dict[int, int] = {}
 
     # ---- marshalling
 
     def _bind(self, kind: str, tensors, extra, build) -> _Bound:
         """The structs of a call of this kind with the tensors' pointers set. ``build()`` makes new structs:
         (structs, [descriptor of each tensor])."""
-        dev = tensors[0].device
+        index = tensors[0].get_device()   # negative: not a CUDA tensor
         rec = self._block_calls.get(kind)
-        if rec is not None and rec.extra == extra and dev.type == "cuda":
-            index = dev.index
+        if rec is not None and index >= 0 and rec.extra == extra:
             for t, sig, f in zip(tensors, rec.sigs, rec.fields):
                 if t is None:
                     if sig is not None:
@@ -96,6 +99,7 @@ class BlockCacheOps:
                     f.data = t.data_ptr()
             else:
                 return rec
+        dev = tensors[0].device
         for t in tensors:
             if t is None:
                 continue
@@ -123,16 +127,17 @@ class BlockCacheOps:
             s = torch.zeros(64, dtype=torch.int32, device=dev)
             torch.cuda.current_stream(dev).synchronize()   # other streams may use it from now on
             self._block_status[dev.index] = s
+            self._block_status_ptr[dev.index] = s.data_ptr()
         return s.data_ptr()
 
-    def _scratch(self, nbytes: int, dev: torch.device, stream: int) -> torch.Tensor | None:
+    def _scratch(self, nbytes: int, index: int, stream: int) -> torch.Tensor | None:
         """Workspace of a call: one per (device, stream); a captured call gets its own from the graph's pool."""
-        if torch.cuda.is_current_stream_capturing():
-            return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-        ws = self._block_ws.get((dev.index, stream))
+        captured = _capturing()
+        ws = None if captured else self._block_ws.get((index, stream))
         if ws is None or ws.numel() < nbytes:
-            ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-            self._block_ws[(dev.index, stream)] = ws
+            ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
+            if not captured:
+                self._block_ws[(index, stream)] = ws
         return ws
 
     def block_status(self, device=None) -> int:
@@ -153,8 +158,9 @@ class BlockCacheOps:
         """Rotate query (and key, or None) at positions (axes, B, S) on several axes; returns (query, key).
 
         sections: pairs of each axis. out_query / out_key may be the inputs (in place)."""
-        if query.device.type == "cuda" and query.device.index != torch.cuda.current_device():
-            with torch.cuda.device(query.device):
+        index = query.get_device()
+        if index >= 0 and index != _current_device():
+            with torch.cuda.device(index):
                 return self.rotary_axes(query, key, positions, cos_cache, sin_cache, sections, interleaved,
                                         q_norm_weight, k_norm_weight, out_query, out_key)
         if out_query is None:
@@ -177,16 +183,17 @@ class BlockCacheOps:
         with self._block_lock:
             rec = self._bind("rotary", (query, key, positions, cos_cache, sin_cache, q_norm_weight, k_norm_weight,
                                         out_query, out_key), extra, build)
-            dev = query.device
-            capi.gqa_rotary_axes(self.handle, *rec.refs, self._status_word(dev), _raw_stream(dev.index))
+            status = self._block_status_ptr.get(index) or self._status_word(query.device)
+            capi.gqa_rotary_axes(self.handle, *rec.refs, status, _raw_stream(index))
         return out_query, out_key
 
     def block_forward(self, query, key, value, seqlens_k, total_sequence_length, cache: BlockCache, new_lens=None,
                       head_sink=None, past_weights=None, present_weights=None, output=None):
         """One step over a block-scaled cache: store key / value (None: already stored), attend, and with
         present_weights add up the attention weight of every cache row. Returns ``output``."""
-        if query.device.type == "cuda" and query.device.index != torch.cuda.current_device():
-            with torch.cuda.device(query.device):
+        index = query.get_device()
+        if index >= 0 and index != _current_device():
+            with torch.cuda.device(index):
                 return self.block_forward(query, key, value, seqlens_k, total_sequence_length, cache, new_lens,
                                           head_sink, past_weights, present_weights, output)
         if output is None:
@@ -208,10 +215,9 @@ class BlockCacheOps:
                 rec.nbytes = None
                 inp.total_sequence_length = int(total_sequence_length)
                 rec.nbytes = capi.gqa_block_workspace_size(self.handle, *rec.structs)
-            dev = query.device
-            stream = _raw_stream(dev.index)
-            status = self._status_word(dev)
-            ws = self._scratch(rec.nbytes, dev, stream)
+            stream = _raw_stream(index)
+            status = self._block_status_ptr.get(index) or self._status_word(query.device)
+            ws = self._scratch(rec.nbytes, index, stream)
             capi.gqa_block_forward(self.handle, *rec.refs, ws.data_ptr(), ws.numel(), status, stream)
         return output
 
@@ -219,8 +225,9 @@ class BlockCacheOps:
                     into_weights=None, recent: int = 0, first: int = 0, kept=None, into_seqlens_k=None):
         """Copy the rows of `cache` that stay (first, recent, and the largest weights between) to `into`.
         Returns (kept, into_seqlens_k): the source row of every kept row (-1 behind the last) and the lengths."""
-        if weights.device.type == "cuda" and weights.device.index != torch.cuda.current_device():
-            with torch.cuda.device(weights.device):
+        index = weights.get_device()
+        if index >= 0 and index != _current_device():
+            with torch.cuda.device(index):
                 return self.block_evict(cache, weights, seqlens_k, total_sequence_length, keep, into, into_weights,
                                         recent, first, kept, into_seqlens_k)
         extra = (int(keep), int(recent), int(first), cache.block_size, into.block_size)
@@ -240,6 +247,6 @@ class BlockCacheOps:
             rec = self._bind("evict", (weights, seqlens_k, into_weights, kept, into_seqlens_k, *cache.tensors(),
                                        *into.tensors()), extra, build)
             rec.structs[0].total_sequence_length = int(total_sequence_length)
-            dev = weights.device
-            capi.gqa_block_evict(self.handle, *rec.refs, self._status_word(dev), _raw_stream(dev.index))
+            status = self._block_status_ptr.get(index) or self._status_word(weights.device)
+            capi.gqa_block_evict(self.handle, *rec.refs, status, _raw_stream(index))
         return kept, into_seqlens_k

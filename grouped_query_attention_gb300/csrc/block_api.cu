@@ -236,7 +236,8 @@ gqa_status plan_block(const gqa_handle* h, const gqa_block_cache* cache, const g
   P.withhold_tile = h->withhold_tile;
 
   const long long rows = S * G;
-  pl->prefill = H == 128 && 128 % G == 0 && rows > 16 && use_prefill(P, rows);
+  // (The prefill takes row maxima and masks before the scale: a negative one would turn them.)
+  pl->prefill = H == 128 && 128 % G == 0 && P.scale > 0.f && rows > 16 && use_prefill(P, rows);
   pl->part_o = pl->part_ml = pl->stash = pl->lse = pl->o_acc = 0;
   if (pl->prefill) {
     const long long nqb = (rows + 255) / 256;

@@ -311,7 +311,7 @@ GQA_API gqa_status gqa_rotary_axes(gqa_handle* handle, const gqa_rotary_inputs* 
  * Beside the per-tensor and per-channel scales of section Inputs (k_scale,
  * v_scale), which are fixed by the caller, these belong to the cache and
  * follow the data. Row r of head g of sequence b is
- *   value[d] = code[b][g][r][d] * scale[b][g][r / block_size].
+ *   value[d] = code[b][g][r][d] * scale[b][g][r / block_size],  scale >= 0.
  *   key/value_codes   int8 (B, N_kv, C, H)
  *   key/value_scales  float32 (B, N_kv, ceil(C / block_size))
  *   block_size        16, 32, 64, 128 or 256 tokens */

@@ -303,20 +303,29 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.status, GQA_DEVICE_BAD_SEQLEN_BIT);
   }
   const long long units = all_units(p);   // lengths are older than the kernel ahead
-  dep_wait();
   dep_launch();
   const long long u0 = units * worker / p.workers, u1 = units * (worker + 1) / p.workers;
-  if (u0 >= u1) return;
+  if (u0 >= u1) {
+    dep_wait();
+    return;
+  }
   Walk ld, cp;
   ld.start(p, u0, u1 - u0);
   cp = ld;
 
+  // The append kernel writes the blocks from the first new row's on and no
+  // other: units before them are copied while it may still run.
+  bool waited = false;
   int fetched = 0;
   // Start the copies of the unit at `ld` into stage s and move on.
   auto fetch = [&](int s) {
     if (ld.left > 0 && (p.withhold_tile < 0 || fetched != p.withhold_tile)) {
       ++fetched;
       const int j0 = (ld.t0 + ld.off) * kBlockUnit;
+      if (!waited && j0 + kBlockUnit > ((ld.total - ld.fresh) >> p.bs_log2 << p.bs_log2)) {
+        dep_wait();
+        waited = true;
+      }
       if (lane == 0) {
         const int row = ld.bg * p.C + j0;   // below 2^31 (checked by the host)
         tc::mbar_arrive_tx(&ctl.full[s], 2 * kTileBytes);
@@ -633,6 +642,7 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
       }
   }
   cp_wait<0>();
+  if (!waited) dep_wait();   // also without need: what follows on the stream waits for this kernel alone
 }
 
 // ------------------------------------------------------------------ merge

@@ -21,6 +21,11 @@
 // nothing waits for another warp. A worker's piece of a range ends as a
 // partial (m, l, O) in the workspace; a second launch merges the pieces of
 // each row and adds the attention weights of the cache rows.
+//
+// Measured: fp16, 16 sequences of 1025 to 8192 keys, 8 KV heads of 128 (151
+// MB): 31 us, 4.9 TB/s (DRAM 58 % busy, 2.2 instructions a clock), merge 7 us.
+// fp32, 32 sequences of 4097 to 16384 keys with weights (672 MB of codes and
+// scores): 118 us, 5.5 TB/s; merge and weights 20 us.
 #include <cuda_fp16.h>
 
 #include "block_internal.h"

@@ -31,6 +31,13 @@
 // never waits for its own P.V, but S runs at half the rate (its B operand is
 // half as wide). S of 128 keys has one buffer, at the full rate. Every barrier
 // wait is bounded.
+//
+// Bound: the latency of a tile's softmax between its S and its P V. Two fp16
+// prompts of 4096 tokens, 32 heads over 8 (275 GFLOP): 256 us, 1.07 PFLOP/s,
+// tensor pipe 46 % busy, 1.9 instructions a clock. Chunks of 8 x 512 tokens, 64
+// heads over 8, window 4096, softcap (488 GFLOP): 655 us, 0.74 PFLOP/s, tensor
+// pipe 31 %, FMA pipe (the softcap's polynomial) 39 %. Two threads per row took
+// 274 and 634 us, loops over 32 columns instead of unrolled steps 275 and 688.
 #include <cuda_fp16.h>
 
 #include "block_internal.h"

@@ -9,7 +9,9 @@
 // pairs 8 l .. 8 l + 7 (both halves, so a pair never leaves its lane) or 16
 // coordinates behind the rotated part. The angles depend on the token alone:
 // a warp loads its eight cosines and sines per lane once and runs over heads
-// of that token with them in registers.
+// of that token with them in registers. 4 x 4096 tokens of 32 + 8 heads of 128,
+// fp16 with norm (340 MB): 72 us, 4.7 TB/s, 2.7 instructions a clock; four
+// blocks an SM, or norm weights held in registers, took 75 to 80 us.
 #include <cuda_fp16.h>
 
 #include "block_internal.h"

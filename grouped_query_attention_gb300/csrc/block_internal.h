@@ -66,6 +66,20 @@ __host__ __device__ inline bool block_lengths(const BlockParams& p, int b, int* 
   return *total >= 0 && *total <= p.T && *fresh >= 0 && *fresh <= p.S && *fresh <= *total;
 }
 
+// Programmatic dependent launch: wait until the kernel ahead on the stream has
+// completed (and its writes are visible); allow the next one to start.
+__device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Packed fp32x2 sum: d = a + b per lane pair.
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  unsigned long long av = *reinterpret_cast<unsigned long long*>(&a);
+  unsigned long long bv = *reinterpret_cast<unsigned long long*>(&b);
+  unsigned long long dv;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(dv) : "l"(av), "l"(bv));
+  return *reinterpret_cast<float2*>(&dv);
+}
+
 // Launch that may start before the kernel ahead of it on the stream has
 // finished (`early`): it calls dep_wait() before it touches what that one
 // writes. What the kernels before those two wrote is complete by then, as the

@@ -25,11 +25,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Programmatic dependent launch: wait until the kernel ahead on the stream has
-// completed (and its writes are visible); allow the next one to start.
-__device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 __device__ __forceinline__ void flag_status(const Params& p, unsigned int bit) {
   atomicOr(p.status, bit);
 }
@@ -47,15 +42,6 @@ __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
   unsigned long long cv = *reinterpret_cast<unsigned long long*>(&c);
   unsigned long long dv;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(dv) : "l"(av), "l"(bv), "l"(cv));
-  return *reinterpret_cast<float2*>(&dv);
-}
-
-// Packed fp32x2 sum: d = a + b per lane pair.
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
-  unsigned long long av = *reinterpret_cast<unsigned long long*>(&a);
-  unsigned long long bv = *reinterpret_cast<unsigned long long*>(&b);
-  unsigned long long dv;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(dv) : "l"(av), "l"(bv));
   return *reinterpret_cast<float2*>(&dv);
 }
 

@@ -62,6 +62,15 @@ struct Vec8<float> {
   }
 };
 
+// Packed product, each lane rounded as __fmul_rn does.
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  unsigned long long av = *reinterpret_cast<unsigned long long*>(&a);
+  unsigned long long bv = *reinterpret_cast<unsigned long long*>(&b);
+  unsigned long long dv;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(dv) : "l"(av), "l"(bv));
+  return *reinterpret_cast<float2*>(&dv);
+}
+
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 
@@ -121,18 +130,19 @@ rotary_axes_kernel(const RotaryAxesParams p, int per_item, int items_per_token, 
   const int lo = rot ? 8 * l : 2 * p.pairs + 16 * (l - p.pairs / 8);
   const int hi = rot ? lo + p.pairs : lo + 8;
 
-  auto row_of = [&](int hh, bool out) -> T* {
-    const bool isq = hh < p.N;
-    const void* base = isq ? (out ? p.qo : p.q) : (out ? p.ko : p.k);
-    const long long r = isq ? tok * p.N + hh : tok * p.Nkv + (hh - p.N);
-    return const_cast<T*>(static_cast<const T*>(base)) + r * p.H;
-  };
+  // Rows of this token: head hh of the queries, hh - N of the keys.
+  const long long q_at = tok * p.N * p.H, k_at = (tok * p.Nkv - p.N) * p.H;
+  const T* q_in = static_cast<const T*>(p.q) + q_at;
+  const T* k_in = static_cast<const T*>(p.k) + k_at;
+  T* q_out = static_cast<T*>(p.qo) + q_at;
+  T* k_out = static_cast<T*>(p.ko) + k_at;
+  auto row_in = [&](int hh) { return (hh < p.N ? q_in : k_in) + hh * p.H; };
   Vec8<T> va, vb;
   int hh = h0 + sub;
   bool on = lane_on && hh < heads;
   if (on) {
-    va.load(row_of(hh, false) + lo);
-    vb.load(row_of(hh, false) + hi);
+    va.load(row_in(hh) + lo);
+    vb.load(row_in(hh) + hi);
   }
   for (int it = 0; it < per_item; ++it) {
     if (h0 + it * kRows >= heads) break;   // uniform: the warp's rows are all past the last head
@@ -149,9 +159,10 @@ rotary_axes_kernel(const RotaryAxesParams p, int per_item, int items_per_token, 
     hh += kRows;
     on = lane_on && it + 1 < per_item && hh < heads;
     if (on) {   // the next row's loads run while this one is computed
-      va.load(row_of(hh, false) + lo);
-      vb.load(row_of(hh, false) + hi);
+      va.load(row_in(hh) + lo);
+      vb.load(row_in(hh) + hi);
     }
+    float2 a2[4], b2[4];   // two coordinates an instruction; every lane rounds as the scalar forms do
     if (p.qw) {
       const T* w = static_cast<const T*>(cur < p.N ? p.qw : p.kw);
       float sa = sumsq8_rn(a), sb = sumsq8_rn(b);
@@ -161,32 +172,40 @@ rotary_axes_kernel(const RotaryAxesParams p, int per_item, int items_per_token, 
         sb = __fadd_rn(sb, __shfl_xor_sync(0xffffffffu, sb, o));
       }
       const float rn = rms_inv_rn(__fadd_rn(sa, sb), p.H, p.eps);
-      if (cur_on) {
-        Vec8<T> wa, wb;
-        float fa[8], fb[8];
-        wa.load(w + lo);
-        wb.load(w + hi);
-        wa.get(fa);
-        wb.get(fb);
+      if (!cur_on) continue;
+      Vec8<T> wa, wb;
+      float fa[8], fb[8];
+      wa.load(w + lo);
+      wb.load(w + hi);
+      wa.get(fa);
+      wb.get(fb);
+      const float2 rn2 = make_float2(rn, rn);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          a[e] = norm_rn(a[e], rn, fa[e]);
-          b[e] = norm_rn(b[e], rn, fb[e]);
-        }
+      for (int e = 0; e < 4; ++e) {
+        a2[e] = fmul2(fmul2(make_float2(a[2 * e], a[2 * e + 1]), rn2), make_float2(fa[2 * e], fa[2 * e + 1]));
+        b2[e] = fmul2(fmul2(make_float2(b[2 * e], b[2 * e + 1]), rn2), make_float2(fb[2 * e], fb[2 * e + 1]));
+      }
+    } else {
+      if (!cur_on) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        a2[e] = make_float2(a[2 * e], a[2 * e + 1]);
+        b2[e] = make_float2(b[2 * e], b[2 * e + 1]);
       }
     }
-    if (!cur_on) continue;
     if (rot) {
+      const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float x = a[e], y = b[e];
-        a[e] = rope_first_rn(x, y, c[e], s[e]);
-        b[e] = rope_second_rn(y, x, c[e], s[e]);
+      for (int e = 0; e < 4; ++e) {
+        const float2 c2 = make_float2(c[2 * e], c[2 * e + 1]), s2 = make_float2(s[2 * e], s[2 * e + 1]);
+        const float2 x = a2[e], y = b2[e];
+        a2[e] = ffma2(fmul2(y, s2), minus, fmul2(x, c2));   // x c - y s: three roundings
+        b2[e] = fadd2(fmul2(y, c2), fmul2(x, s2));
       }
     }
-    T* o = row_of(cur, true);
-    Vec8<T>::store(o + lo, a);
-    Vec8<T>::store(o + hi, b);
+    T* o = (cur < p.N ? q_out : k_out) + cur * p.H;
+    Vec8<T>::store(o + lo, reinterpret_cast<const float*>(a2));
+    Vec8<T>::store(o + hi, reinterpret_cast<const float*>(b2));
   }
 }
 

@@ -10,8 +10,9 @@
 // coordinates behind the rotated part. The angles depend on the token alone:
 // a warp loads its eight cosines and sines per lane once and runs over heads
 // of that token with them in registers. 4 x 4096 tokens of 32 + 8 heads of 128,
-// fp16 with norm (340 MB): 72 us, 4.7 TB/s, 2.7 instructions a clock; four
-// blocks an SM, or norm weights held in registers, took 75 to 80 us.
+// fp16 with norm (340 MB): 65 us, 5.2 TB/s; with three blocks an SM instead of
+// four 70, with one coordinate an instruction 72. fp32 rows need the registers
+// of three (12 + 4 heads of 96, 3 x 1025 tokens: 13 to 14 us against 15.7).
 #include <cuda_fp16.h>
 
 #include "block_internal.h"
@@ -92,7 +93,7 @@ __device__ __forceinline__ void load_table(const RotaryAxesParams& p, const void
 // LPR lanes per row; the warp's rows are consecutive heads (queries first,
 // then keys) of one token, `per_item` passes of them.
 template <typename T, int LPR>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3)
 rotary_axes_kernel(const RotaryAxesParams p, int per_item, int items_per_token, long long items) {
   constexpr int kRows = 32 / LPR;
   const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);

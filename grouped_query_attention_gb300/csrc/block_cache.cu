@@ -228,6 +228,7 @@ __device__ __forceinline__ unsigned weight_key(float w) {
 constexpr int kSelKeys = 16;                        // consecutive rows a thread holds in registers
 constexpr int kSelRows = kSelThreads * kSelKeys;    // rows of a CTA at a time
 
+constexpr int kSelCluster = 8;                      // CTAs of a cluster, at most
 constexpr int kSelBins = 2048;                      // 11 bits a pass
 constexpr int kSelList = 512;                       // keys ranked by comparing each with each
 
@@ -241,7 +242,7 @@ constexpr int kSelList = 512;                       // keys ranked by comparing 
 // the rows that stay in order. Bound: latency, 4 bytes a row. (Eight-bit
 // passes with a scan by one warp took 21 us on 8192 rows, four-bit passes with
 // counters in registers as much: their reductions cost what the atomics did.)
-// 128 (b, g) of 8192 rows: 12 us; 8 of 131072 rows, clusters of 8: 30 us.
+// 128 (b, g) of 8192 rows: 12 us; 8 of 131072 rows, clusters of 8: 23 us.
 __global__ void __launch_bounds__(kSelThreads)
 evict_select_kernel(const EvictParams p, int CL) {
   namespace cg = cooperative_groups;
@@ -282,7 +283,7 @@ evict_select_kernel(const EvictParams p, int CL) {
   };
   if (rounds <= 1) load(0);
 
-  __shared__ int hist[2][kSelBins];    // the CTA's counts, by pass parity
+  __shared__ __align__(8) int hist[2][kSelBins];    // the CTA's counts, by pass parity
   __shared__ unsigned list[kSelList], all_list[kSelList];
   __shared__ int wsum[kSelThreads / 32], s_count[2], s_list, s_need, s_bin_count;
   __shared__ unsigned s_key;
@@ -318,10 +319,17 @@ evict_select_kernel(const EvictParams p, int CL) {
     int c[2] = {0, 0};
     const int top = bins - 1 - 2 * tid;
     if (top > 0) {
-      for (int r = 0; r < CL; ++r) {
-        const int* o = CL > 1 ? cluster.map_shared_rank(h, r) : h;
-        c[0] += o[top];
-        c[1] += o[top - 1];
+      const int2* at = reinterpret_cast<const int2*>(h + top - 1);
+      if (CL == 1) {
+        c[0] = at->y;
+        c[1] = at->x;
+      } else {
+#pragma unroll 8
+        for (int r = 0; r < CL; ++r) {
+          const int2 v = *cluster.map_shared_rank(at, r);
+          c[0] += v.y;
+          c[1] += v.x;
+        }
       }
     }
     int incl = c[0] + c[1];
@@ -361,12 +369,20 @@ evict_select_kernel(const EvictParams p, int CL) {
           if (k < mine && (key[k] & mask) == prefix) list[atomicAdd(&s_list, 1)] = key[k];   // any order serves
       }
       group_sync();
-      int m = 0;                       // every CTA takes all the cluster's keys
-      for (int r = 0; r < CL; ++r) {
-        const unsigned* o = CL > 1 ? cluster.map_shared_rank(list, r) : list;
-        const int nr = CL > 1 ? *cluster.map_shared_rank(&s_list, r) : s_list;
-        for (int i = tid; i < nr; i += kSelThreads) all_list[m + i] = o[i];
-        m += nr;
+      int m = 0;                       // every CTA takes all the cluster's keys (at most kSelList), one a thread
+      if (CL == 1) {
+        m = s_list;
+        if (tid < m) all_list[tid] = list[tid];
+      } else {
+        int at_r = 0, at_i = 0, cnt[kSelCluster];
+#pragma unroll
+        for (int r = 0; r < kSelCluster; ++r) cnt[r] = r < CL ? *cluster.map_shared_rank(&s_list, r) : 0;
+#pragma unroll
+        for (int r = 0; r < kSelCluster; ++r) {
+          if (tid >= m && tid < m + cnt[r]) at_r = r, at_i = tid - m;
+          m += cnt[r];
+        }
+        if (tid < m) all_list[tid] = cluster.map_shared_rank(list, at_r)[at_i];
       }
       __syncthreads();
       if (tid < m) {
@@ -438,10 +454,13 @@ evict_select_kernel(const EvictParams p, int CL) {
         s_count[1] = tie_n;
       }
       cluster.sync();
-      for (int r = 0; r < rank; ++r) {
-        const int* cnt = cluster.map_shared_rank(s_count, r);
-        out += cnt[0];
-        ties += cnt[1];
+#pragma unroll
+      for (int r = 0; r < kSelCluster - 1; ++r) {
+        if (r < rank) {
+          const int* cnt = cluster.map_shared_rank(s_count, r);
+          out += cnt[0];
+          ties += cnt[1];
+        }
       }
       out += min(ties, need);
     }
@@ -546,9 +565,10 @@ cudaError_t launch_block_append(const BlockParams& p, cudaStream_t st) {
 }
 
 cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t st) {
-  // A CTA for every kSelRows rows, up to the portable cluster size.
+  // A CTA for every kSelRows rows, up to the portable cluster size (clusters of
+  // 16 took 53 us where 8 take 33, on 8 (b, g) of 131072 rows).
   int CL = 1;
-  while (CL < 8 && (long long)CL * kSelRows < p.T) CL *= 2;
+  while (CL < kSelCluster && (long long)CL * kSelRows < p.T) CL *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.B * p.Nkv * CL));
   cfg.blockDim = dim3(kSelThreads);

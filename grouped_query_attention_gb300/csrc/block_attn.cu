@@ -740,7 +740,15 @@ block_merge_kernel(const BlockParams p, long long row_blocks, int weight_chunks,
     const RangeInfo ri = range_info(p, b, g * p.nrt + rt);
     const bool has_sink = p.sink || p.smooth;
     const float sink = has_sink ? (p.sink ? load_t(p.sink, h, p.t_type) : 0.f) * kLog2e : kNegBig;
+    const int groups = THREADS / q4, grp = tid / q4, c = tid % q4;
+    const float* src = p.part_o + (ri.slot0 * p.rt_rows + row) * p.H + 4 * c;
+    const long long ld = (long long)p.rt_rows * p.H;
     dep_wait();
+    constexpr int kAhead = 4;   // pieces of a thread under way while their factors are worked out
+    float4 ahead[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (grp < groups && grp + k * groups < ri.n) ahead[k] = *reinterpret_cast<const float4*>(src + (grp + k * groups) * ld);
     float m = sink;
     for (int x = tid; x < ri.n; x += THREADS) {
       fac[x] = p.part_ml[((ri.slot0 + x) * p.rt_rows + row) * 4];
@@ -761,20 +769,19 @@ block_merge_kernel(const BlockParams p, long long row_blocks, int weight_chunks,
       if (tid == 0) p.lse[(long long)bg * nrows + r] = l > 0.f ? m + log2f(l) : INFINITY;
     }
     l = block_reduce<THREADS, false>(lr, red) + extra;   // (fac is complete behind it)
-    const int groups = THREADS / q4, grp = tid / q4, c = tid % q4;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float4 v, float f) {
+      a.x = fmaf(v.x, f, a.x);
+      a.y = fmaf(v.y, f, a.y);
+      a.z = fmaf(v.z, f, a.z);
+      a.w = fmaf(v.w, f, a.w);
+    };
     if (grp < groups) {
-      const float* src = p.part_o + (ri.slot0 * p.rt_rows + row) * p.H + 4 * c;
-      const long long ld = (long long)p.rt_rows * p.H;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (grp + k * groups < ri.n) add(ahead[k], fac[grp + k * groups]);
 #pragma unroll 4
-      for (int x = grp; x < ri.n; x += groups) {
-        const float f = fac[x];
-        const float4 v = *reinterpret_cast<const float4*>(src + x * ld);
-        a.x = fmaf(v.x, f, a.x);
-        a.y = fmaf(v.y, f, a.y);
-        a.z = fmaf(v.z, f, a.z);
-        a.w = fmaf(v.w, f, a.w);
-      }
+      for (int x = grp + kAhead * groups; x < ri.n; x += groups) add(*reinterpret_cast<const float4*>(src + x * ld), fac[x]);
     }
     acc[tid] = a;
     __syncthreads();

@@ -744,7 +744,7 @@ block_merge_kernel(const BlockParams p, long long row_blocks, int weight_chunks,
     const float* src = p.part_o + (ri.slot0 * p.rt_rows + row) * p.H + 4 * c;
     const long long ld = (long long)p.rt_rows * p.H;
     dep_wait();
-    constexpr int kAhead = 4;   // pieces of a thread under way while their factors are worked out
+    constexpr int kAhead = 8;   // pieces of a thread under way while their factors are worked out
     float4 ahead[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)

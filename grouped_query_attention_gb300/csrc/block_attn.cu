@@ -25,7 +25,7 @@
 // Measured: fp16, 16 sequences of 1025 to 8192 keys, 8 KV heads of 128 (151
 // MB): 31 us, 4.9 TB/s (DRAM 58 % busy, 2.2 instructions a clock), merge 7 us.
 // fp32, 32 sequences of 4097 to 16384 keys with weights (672 MB of codes and
-// scores): 118 us, 5.5 TB/s; merge and weights 20 us.
+// scores): 117 us, 5.7 TB/s; merge and weights 17 us.
 #include <cuda_fp16.h>
 
 #include "block_internal.h"
@@ -815,7 +815,28 @@ block_merge_kernel(const BlockParams p, long long row_blocks, int weight_chunks,
   __shared__ float nl[16];                       // -lse of the rows
   const int nrows = fresh * p.G, rs = p.stash_rows;   // live rows (at most one row tile)
   const RangeInfo ri = range_info(p, b, g);
+  int t0, nt;
+  units_of(p, total, fresh, &t0, &nt);
+  const long long at0 = (long long)bg * p.C;
+  const float* st = p.stash + (long long)bg * p.stash_ld * rs;
+  const int jend = min(total, j0 + keys), seen = t0 * kBlockUnit;   // keys before `seen`: no scores
   dep_wait();
+  // A thread's keys, kAhead at a time: their loads are under way together, the
+  // first ones while the rows' sums are worked out.
+  constexpr int kAhead = 8;
+  const bool quads = (rs & 3) == 0 && nrows >= 4;
+  float w[kAhead];
+  float4 v[kAhead];
+  auto scored = [&](int j) { return j < jend && j >= seen; };
+  auto fetch = [&](int j) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int ju = j + u * THREADS;
+      w[u] = p.past_w && ju < min(jend, total - fresh) ? p.past_w[at0 + ju] : 0.f;
+      if (quads && scored(ju)) v[u] = *reinterpret_cast<const float4*>(st + (long long)ju * rs);
+    }
+  };
+  fetch(j0 + tid);
   for (int r = warp; r < nrows; r += THREADS / 32) {   // a warp per row, lanes over the pieces
     const float4* ml = reinterpret_cast<const float4*>(p.part_ml) + ri.slot0 * p.rt_rows + r;   // (m, l, ..)
     const bool has_sink = p.sink || p.smooth;
@@ -824,53 +845,42 @@ block_merge_kernel(const BlockParams p, long long row_blocks, int weight_chunks,
     for (int i = lane; i < ri.n; i += 32) m = fmaxf(m, ml[(long long)i * p.rt_rows].x);
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     for (int i = lane; i < ri.n; i += 32) {
-      const float4 v = ml[(long long)i * p.rt_rows];
-      l = fmaf(v.y, ex2(v.x - m), l);
+      const float4 x4 = ml[(long long)i * p.rt_rows];
+      l = fmaf(x4.y, ex2(x4.x - m), l);
     }
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (has_sink) l += ex2(sink - m);
     if (lane == 0) nl[r] = -(m + log2f(l));
   }
   __syncthreads();
-  int t0, nt;
-  units_of(p, total, fresh, &t0, &nt);
-  const long long at0 = (long long)bg * p.C;
-  const float* st = p.stash + (long long)bg * p.stash_ld * rs;
-  const int jend = min(total, j0 + keys);
-  // Four keys of a thread at a time: their loads are under way together.
-  for (int j = j0 + tid; j < jend; j += 4 * THREADS) {
-    float w[4];
-    const float* sj[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int ju = j + u * THREADS;
-      w[u] = p.past_w && ju < min(jend, total - fresh) ? p.past_w[at0 + ju] : 0.f;
-      sj[u] = ju < jend && ju >= t0 * kBlockUnit ? st + (long long)ju * rs : nullptr;   // keys before t0: no scores
-    }
+  for (int j = j0 + tid; j < jend; j += kAhead * THREADS) {
+    if (j != j0 + tid) fetch(j);
     int r = 0;
-    if ((rs & 3) == 0) {
+    if (quads) {
       for (; r + 4 <= nrows; r += 4) {
-        float4 v[4];
+        if (r > 0) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (sj[u]) v[u] = *reinterpret_cast<const float4*>(sj[u] + r);
+          for (int u = 0; u < kAhead; ++u)
+            if (scored(j + u * THREADS)) v[u] = *reinterpret_cast<const float4*>(st + (long long)(j + u * THREADS) * rs + r);
+        }
         const float4 n = make_float4(nl[r], nl[r + 1], nl[r + 2], nl[r + 3]);
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (sj[u]) w[u] += (ex2(v[u].x + n.x) + ex2(v[u].y + n.y)) + (ex2(v[u].z + n.z) + ex2(v[u].w + n.w));
+        for (int u = 0; u < kAhead; ++u)
+          if (scored(j + u * THREADS))
+            w[u] += (ex2(v[u].x + n.x) + ex2(v[u].y + n.y)) + (ex2(v[u].z + n.z) + ex2(v[u].w + n.w));
       }
     }
     for (; r < nrows; ++r) {
-      float v[4];
+      float s1[kAhead];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (sj[u]) v[u] = sj[u][r];
+      for (int u = 0; u < kAhead; ++u)
+        if (scored(j + u * THREADS)) s1[u] = st[(long long)(j + u * THREADS) * rs + r];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (sj[u]) w[u] += ex2(v[u] + nl[r]);
+      for (int u = 0; u < kAhead; ++u)
+        if (scored(j + u * THREADS)) w[u] += ex2(s1[u] + nl[r]);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < kAhead; ++u)
       if (j + u * THREADS < jend) p.present_w[at0 + j + u * THREADS] = w[u];
   }
 }

@@ -88,7 +88,7 @@ struct __align__(1024) PfSmem {
   uint64_t raw_full[2], raw_empty[2];
   uint64_t q_land[2], q_ready[2];
   uint64_t kf_full[2], kf_empty[2], vf_full[2], vf_empty[2];
-  uint64_t s_full[2][2], p_full[2][2], o_done[2];   // [query tile][buffer]
+  uint64_t s_full[2][2], p_full[2][2], o_done[2];   // [query tile][buffer; P of one buffer: half]
   uint64_t drain;
   uint32_t tmem;
   unsigned vmax;                 // bits of the largest V scale
@@ -368,19 +368,21 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
       mma_commit(&sm.s_full[q][bf]);
     };
     // O_q += P V of step h: keys 64 x .. of it in columns 64 x .. + 31 of the S buffer (lo pairs in the next 32).
-    auto issue_pv = [&](int q, int h) {
+    // A step of 128 keys in two halves, as their P is ready.
+    auto issue_pv = [&](int q, int h, int half) {
       const int bf = h % kSub, t = h / kSub;
       const uint32_t d = tmem + 256 + q * 128;
       const uint32_t pa = tmem + q * 128 + bf * STEP;
       const uint64_t b0 = dv0 + (uint64_t)((t % kNB) * (int)(kTile >> 4) + bf * (STEP * 128 >> 4));
 #pragma unroll
-      for (int ks = 0; ks < STEP / 16; ++ks) {
+      for (int i = 0; i < 4; ++i) {
+        const int ks = 4 * half + i;
         const uint32_t col = (uint32_t)((ks >> 2) * 64 + (ks & 3) * 8);
         const uint64_t bv = b0 + (uint64_t)(ks * 128);
         mma_f16_ts(d, pa + col, bv, kIdO, h % flush > 0 || ks > 0);
         if constexpr (F32) mma_f16_ts(d, pa + col + 32, bv, kIdO, true);
       }
-      mma_commit(&sm.o_done[q]);
+      if (half == kHalves - 1) mma_commit(&sm.o_done[q]);
     };
     auto wait1 = [&](uint64_t* bar, uint32_t par) {
       return __all_sync(0xffffffffu, mbar_wait(bar, par, p.wait_budget)) != 0;
@@ -407,11 +409,18 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
       const int t = h / kSub, bf = h % kSub;
       if (bf == 0) ok = wait1(&sm.vf_full[t % kNB], (uint32_t)(t / kNB) & 1u);
       for (int q = 0; q < 2 && ok; ++q) {
-        ok = wait1(&sm.p_full[q][bf], (uint32_t)t & 1u);
+        if constexpr (kHalves == 2) {
+          ok = wait1(&sm.p_full[q][0], (uint32_t)t & 1u);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) issue_pv(q, h, 0);
+          __syncwarp();
+        }
+        ok = wait1(&sm.p_full[q][kHalves == 2 ? 1 : bf], (uint32_t)t & 1u);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          issue_pv(q, h);
+          issue_pv(q, h, kHalves - 1);
           if (q == 1 && (bf == kSub - 1 || h + 1 == nsteps)) mma_commit(&sm.vf_empty[t % kNB]);
         }
         __syncwarp();
@@ -693,6 +702,12 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
             tmem_st16(s_buf + hf * 64 + 16 * qq, ph);
             if constexpr (F32) tmem_st16(s_buf + hf * 64 + 32 + 16 * qq, pl);
           }
+          if (hf == 0 && kHalves == 2) {   // P V of the first half may start
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.p_full[q][0]);
+          }
         }
       };
       if constexpr (CAP) {
@@ -717,7 +732,7 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&sm.p_full[q][bf]);
+        mbar_arrive(&sm.p_full[q][kHalves == 2 ? 1 : bf]);
         if (bf == kSub - 1 || st + 1 == nsteps) mbar_arrive(&sm.sc_empty[slot]);
       }
     }

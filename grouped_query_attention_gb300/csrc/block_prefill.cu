@@ -665,7 +665,7 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
             for (int gi = 0; gi < 2; ++gi) {
               const int gr = 2 * qq + gi;
               const float2 kk2 = make_float2(kkg[gr], kkg[gr]), cc2 = make_float2(ccg[gr], ccg[gr]);
-              float2 ls = make_float2(0.f, 0.f);
+              float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};   // two chains
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 const int e = 16 * gr + 2 * k;
@@ -688,7 +688,7 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
                   }
                 }
                 const float pa = ex2(arg.x), pb = ex2(arg.y);
-                ls = ffma2(make_float2(pa, pb), make_float2(1.f, 1.f), ls);
+                ls[k & 1] = fadd2(make_float2(pa, pb), ls[k & 1]);
                 const __half2 hp = __floats2half2_rn(pa, pb);
                 ph[8 * gi + k] = *reinterpret_cast<const uint32_t*>(&hp);
                 if constexpr (F32) {
@@ -697,7 +697,8 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
                   pl[8 * gi + k] = *reinterpret_cast<const uint32_t*>(&lp);
                 }
               }
-              l_run = fmaf(ls.x + ls.y, ivg[gr], l_run);
+              const float2 lt = fadd2(ls[0], ls[1]);
+              l_run = fmaf(lt.x + lt.y, ivg[gr], l_run);
             }
             tmem_st16(s_buf + hf * 64 + 16 * qq, ph);
             if constexpr (F32) tmem_st16(s_buf + hf * 64 + 32 + 16 * qq, pl);

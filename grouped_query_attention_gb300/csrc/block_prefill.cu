@@ -32,12 +32,15 @@
 // half as wide). S of 128 keys has one buffer, at the full rate. Every barrier
 // wait is bounded.
 //
-// Bound: the latency of a tile's softmax between its S and its P V. Two fp16
-// prompts of 4096 tokens, 32 heads over 8 (275 GFLOP): 256 us, 1.07 PFLOP/s,
-// tensor pipe 46 % busy, 1.9 instructions a clock. Chunks of 8 x 512 tokens, 64
-// heads over 8, window 4096, softcap (488 GFLOP): 655 us, 0.74 PFLOP/s, tensor
-// pipe 31 %, FMA pipe (the softcap's polynomial) 39 %. Two threads per row took
-// 274 and 634 us, loops over 32 columns instead of unrolled steps 275 and 688.
+// Bound: without a softcap the chain of a query tile's S, softmax and P V (of
+// 3500 clocks 1850 are the softmax, 770 MMAs behind it, the rest the hand-offs
+// between the roles; P V of the first 64 keys runs beside the softmax of the
+// others). Two fp16 prompts of 4096 tokens, 32 heads over 8 (275 GFLOP): 244
+// us, 1.13 PFLOP/s. With one, instructions: the fit, the exponents and the codes'
+// conversion take 12 a score. Chunks of 8 x 512 tokens, 64 heads over 8, window
+// 4096 (488 GFLOP): 651 us, 0.75 PFLOP/s, FMA pipe 39 % busy, tensor pipe 31 %.
+// Two threads per row took 274 and 634 us, loops over 32 columns instead of
+// unrolled steps 275 and 688, the second 64 scores kept in registers 272.
 #include <cuda_fp16.h>
 
 #include "block_internal.h"
@@ -841,7 +844,7 @@ cudaError_t launch_one(const BlockParams& p, cudaStream_t st) {
 cudaError_t launch_block_prefill(const BlockParams& p, cudaStream_t st) {
   const bool cap = p.softcap > 0.f;
   // With a softcap the softmax sets the pace and two S buffers hide its waits
-  // (64 keys a step: 0.68 against 0.85 ms on 512-token chunks of 8 sequences);
+  // (64 keys a step: 0.65 against 0.86 ms on 512-token chunks of 8 sequences);
   // without, the MMAs do, and a 64-key S takes as long as a 128-key one (0.30
   // against 0.26 ms on two 4096-token prompts). fp32: equal.
   if (p.t_type == kF32) return cap ? launch_one<true, true, 64>(p, st) : launch_one<true, false, 128>(p, st);

@@ -107,30 +107,55 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float from, float to, fl
   return out;
 }
 
+// Eight values of a row as loaded.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* f);
+struct Raw8;
 template <>
-__device__ __forceinline__ void load8<__half>(const __half* p, float* f) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
-    f[2 * i] = a.x;
-    f[2 * i + 1] = a.y;
+struct Raw8<__half> {
+  static constexpr unsigned kInfinity = 0x7c00u;
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const __half* p) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
   }
-}
+  __device__ __forceinline__ void get(float* f) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = a.x;
+      f[2 * i + 1] = a.y;
+    }
+  }
+  // The larger of m and the bits of every |x| (ordered as the values are), two halves side by side.
+  __device__ __forceinline__ unsigned top(unsigned m) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    return m;
+  }
+  static __device__ __forceinline__ unsigned fold(unsigned m) { return max(m & 0xffffu, m >> 16); }
+  static __device__ __forceinline__ float value(unsigned bits) { return __half2float(__ushort_as_half((unsigned short)bits)); }
+};
 template <>
-__device__ __forceinline__ void load8<float>(const float* p, float* f) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-
-__device__ __forceinline__ float finite_abs(float x) {
-  const float a = fabsf(x);
-  return a <= 3.402823466e38f ? a : 0.f;   // infinities and NaN do not enter a scale
-}
+struct Raw8<float> {
+  static constexpr unsigned kInfinity = 0x7f800000u;
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const float* p) {
+    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  }
+  __device__ __forceinline__ void get(float* f) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+  }
+  __device__ __forceinline__ unsigned top(unsigned m) const {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) m = max(max(m, w[i] & 0x7fffffffu), w[i + 1] & 0x7fffffffu);
+    return m;
+  }
+  static __device__ __forceinline__ unsigned fold(unsigned m) { return m; }
+  static __device__ __forceinline__ float value(unsigned bits) { return __uint_as_float(bits); }
+};
 
 // ------------------------------------------------------------------ append
 
@@ -175,20 +200,38 @@ block_append_kernel(const BlockParams p) {
   const long long ld = (long long)p.Nkv * p.H;                                   // elements between tokens
   const T* src = x + ((long long)b * p.S + (lo - past)) * ld + (long long)g * p.H;
 
-  float amax = 0.f;
-  for (int i = tid; i < n; i += kAppendThreads) {
-    const int r = div.quot(i), c = i - r * chunks;
-    float f[8];
-    load8<T>(src + r * ld + 8 * c, f);
+  auto load = [&](int i) {
+    const int r = div.quot(i);
+    Raw8<T> v;
+    v.load(src + r * ld + 8 * (i - r * chunks));
+    return v;
+  };
+  __shared__ unsigned red[kAppendThreads / 32];
+  auto block_max = [&](unsigned m) {
+    m = __reduce_max_sync(0xffffffffu, m);
+    __syncthreads();
+    if ((tid & 31) == 0) red[tid >> 5] = m;
+    __syncthreads();
+    m = red[0];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(f[e]));
+    for (int i = 1; i < kAppendThreads / 32; ++i) m = max(m, red[i]);
+    return m;
+  };
+  unsigned mx = 0;
+#pragma unroll 4
+  for (int i = tid; i < n; i += kAppendThreads) mx = load(i).top(mx);
+  mx = block_max(Raw8<T>::fold(mx));
+  float amax = Raw8<T>::value(mx);
+  if (mx >= Raw8<T>::kInfinity) {   // infinities and NaN do not enter a scale: once more without them
+    amax = 0.f;
+    for (int i = tid; i < n; i += kAppendThreads) {
+      float f[8];
+      load(i).get(f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]) <= 3.402823466e38f ? fabsf(f[e]) : 0.f);
+    }
+    amax = __uint_as_float(block_max(__float_as_uint(amax)));
   }
-  __shared__ float red[kAppendThreads / 32];
-  for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((tid & 31) == 0) red[tid >> 5] = amax;
-  __syncthreads();
-  amax = red[0];
-  for (int i = 1; i < kAppendThreads / 32; ++i) amax = fmaxf(amax, red[i]);
 
   float s = __fmul_rn(amax, 1.0f / 127.0f);
   if (first < past) {   // the block holds rows already
@@ -205,10 +248,10 @@ block_append_kernel(const BlockParams p) {
   if (tid == 0) *scale = s;
   const float inv = __fdiv_rn(1.f, s);
   int8_t* dst = codes + (long long)lo * p.H;
+#pragma unroll 2
   for (int i = tid; i < n; i += kAppendThreads) {
-    const int r = div.quot(i), c = i - r * chunks;
     float f[8];
-    load8<T>(src + r * ld + 8 * c, f);
+    load(i).get(f);
     *reinterpret_cast<uint2*>(dst + (long long)i * 8) = s > 0.f ? codes8(f, s, inv) : make_uint2(0u, 0u);
   }
 }

@@ -133,7 +133,7 @@ gqa_status check_block_cache(const gqa_block_cache& c, const char* name, long lo
 bool use_prefill(const BlockParams& P, long long rows) {
   const int rt = gqa::block_row_tile(P.t_type, P.H, rows);
   const double nrt = (double)((rows + rt - 1) / rt), heads = (double)P.B * P.Nkv;
-  const double ctas = heads * (double)((rows + 255) / 256), waves = ceil(ctas / 152.0);
+  const double ctas = heads * (double)((rows + 2 * P.tile_rows - 1) / (2 * P.tile_rows)), waves = ceil(ctas / 152.0);
   double mean = P.T - 0.5 * P.S, most = P.T;   // keys a query row sees
   if (P.window >= 0) {
     mean = mean < P.window ? mean : P.window;
@@ -141,7 +141,7 @@ bool use_prefill(const BlockParams& P, long long rows) {
   }
   const bool f32 = P.t_type == gqa::kF32, cap = P.softcap > 0.f;
   double tile = f32 ? 3.6 : cap ? 3.5 : 1.95;
-  if (rows <= 128) tile *= 1.4;
+  if (rows <= P.tile_rows) tile *= 1.4;
   const double prefill = 8.0 + waves * (waves > 1.0 ? mean : most) / 128.0 * tile;
   const double workers = P.H > 128 ? 608.0 : 1216.0;
   const double split = 10.0 + heads * nrt * (mean / 32.0 + 2.0) / workers * (cap ? 3.6 : 2.1) + heads * rows * 0.003;
@@ -237,10 +237,11 @@ gqa_status plan_block(const gqa_handle* h, const gqa_block_cache* cache, const g
 
   const long long rows = S * G;
   // (The prefill takes row maxima and masks before the scale: a negative one would turn them.)
-  pl->prefill = H == 128 && 128 % G == 0 && P.scale > 0.f && rows > 16 && use_prefill(P, rows);
+  P.tile_rows = G <= 128 ? (int)(128 / G * G) : 0;
+  pl->prefill = H <= 128 && G <= 128 && P.scale > 0.f && rows > 16 && use_prefill(P, rows);
   pl->part_o = pl->part_ml = pl->stash = pl->lse = pl->o_acc = 0;
   if (pl->prefill) {
-    const long long nqb = (rows + 255) / 256;
+    const long long nqb = (rows + 2 * P.tile_rows - 1) / (2 * P.tile_rows);
     if (nqb > 65535 || (T + 127) / 128 > 65535) return fail(GQA_ERR_UNSUPPORTED, "query too large");
     if (P.t_type == gqa::kF32 && T > gqa::kPrefillFlush)
       pl->o_acc = align_up((size_t)(B * Nkv) * nqb * 2 * 128 * 128 * sizeof(float));
@@ -425,7 +426,8 @@ gqa_status gqa_block_forward(gqa_handle* h, const gqa_block_cache* cache, const 
   }
   if (P.lse) {
     e = timed_launch(h, GQA_KERNEL_BLOCK_WEIGHTS, st, [&] {
-      return pl.prefill && P.t_type == gqa::kF16 ? gqa::launch_block_weights_tc(P, st) : gqa::launch_block_weights(P, st);
+      const bool tc = pl.prefill && P.t_type == gqa::kF16 && (P.G <= 64 || P.G == 128);
+      return tc ? gqa::launch_block_weights_tc(P, st) : gqa::launch_block_weights(P, st);
     });
     if (e != cudaSuccess) return cuda_fail(e, "weights launch");
   }

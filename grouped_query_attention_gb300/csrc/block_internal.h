@@ -53,6 +53,7 @@ struct BlockParams {
   int stash_ld, stash_rows;
   float* lse;            // log2-domain log-sum-exp [B*Nkv][S*G], or null
   // tensor-core prefill
+  int tile_rows;         // rows of a 128-row query tile in use: whole positions of G rows
   int qb_major;          // grid with the query block on the slow axis
   float* o_acc;          // fp32: sums of O, 512 bytes a row of every 128-row query tile, or null
   long long wait_budget;
@@ -107,7 +108,7 @@ int block_row_tile(int t_type, int H, long long rows);   // query rows per row t
 int block_workers(const BlockParams& p);
 cudaError_t launch_block_attn(const BlockParams& p, cudaStream_t st);
 cudaError_t launch_block_merge(const BlockParams& p, cudaStream_t st);
-// Tensor-core prefill: head size 128, group size dividing 128.
+// Tensor-core prefill: head and group sizes up to 128.
 constexpr int kPrefillFlush = 512;   // keys after which the fp32 form moves O into sums
 cudaError_t launch_block_prefill(const BlockParams& p, cudaStream_t st);
 // Attention weights of the cache rows from the log-sum-exp of every query row.

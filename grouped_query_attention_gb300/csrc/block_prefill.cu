@@ -1,8 +1,9 @@
 // Tensor-core attention over the block-scaled int8 cache for prompts and long
-// chunks (head size 128, group size dividing 128), fp16 or fp32 queries.
+// chunks (head and group sizes up to 128), fp16 or fp32 queries.
 //
 // CTA = two 128-row query tiles of one KV head (b, g), rows = (position,
-// grouped head). The codes of a 128-key tile become fp16 operand tiles (small
+// grouped head), whole positions of a group: of 128 rows a group of 7 heads uses
+// 126. Dims behind the head size are zeros (copies past the tensors' ends). The codes of a 128-key tile become fp16 operand tiles (small
 // integers, exact); S = Q K^T and O += P V run on tcgen05 with S, P and O in
 // tensor memory. Scales are one number for 16 keys (the smallest block):
 //   score (log2 domain)  s = S ks k_row,  k_row = scale log2(e) [2^e fp32 row]
@@ -56,7 +57,7 @@ using namespace tc;
 
 constexpr int kBM = 128;                       // rows per query tile
 constexpr int kBN = 128;                       // keys per K/V tile
-constexpr int kHD = 128;                       // head size
+constexpr int kHD = 128;                       // dims of the operand tiles; those behind the head size are zeros
 constexpr int kGroups = kBN / 16;              // 16-key groups of a tile, one scale each
 constexpr int kThreads = 512;
 constexpr int kSoftWarp0 = 4;
@@ -197,7 +198,8 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
   SM& sm = *reinterpret_cast<SM*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nrows = p.S * p.G;
-  const int nqb = (nrows + 2 * kBM - 1) / (2 * kBM);
+  const int tr = p.tile_rows;
+  const int nqb = (nrows + 2 * tr - 1) / (2 * tr);
   const bool qbm = p.qb_major != 0;
   const int qb = nqb - 1 - (int)(qbm ? blockIdx.y : blockIdx.x);   // longest key ranges first
   const int bg = (int)(qbm ? blockIdx.x : blockIdx.y), b = bg / p.Nkv, g = bg % p.Nkv;
@@ -210,15 +212,15 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
     return;
   }
   const int past = total - fresh;
-  const int r0 = qb * 2 * kBM;
+  const int r0 = qb * 2 * tr;
   const int i_lo = r0 / p.G;
-  const int i_hi = min((min(r0 + 2 * kBM, nrows) - 1) / p.G, fresh - 1);
+  const int i_hi = min((min(r0 + 2 * tr, nrows) - 1) / p.G, fresh - 1);
   if (i_lo > i_hi) {   // padding rows only
     dep_wait();
-    for (int x = tid; x < 2 * kBM * kHD; x += kThreads) {
-      const int r = r0 + x / kHD, d = x % kHD;
+    for (int x = tid; x < 2 * tr * p.H; x += kThreads) {
+      const int r = r0 + x / p.H, d = x % p.H;
       if (r < nrows)
-        static_cast<T*>(p.out)[((long long)(b * (long long)p.S + r / p.G) * p.N + g * p.G + r % p.G) * kHD + d] = T(0.f);
+        static_cast<T*>(p.out)[((long long)(b * (long long)p.S + r / p.G) * p.N + g * p.G + r % p.G) * p.H + d] = T(0.f);
     }
     return;
   }
@@ -254,14 +256,21 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
     sm.vmax = 0;
     mbar_fence_init();
   }
+  if (tr < kBM) {   // rows of the query tiles that no copy fills
+    for (int x = tid; x < 2 * kBoxes * (kBM - tr) * 8; x += kThreads) {
+      const int box = x / ((kBM - tr) * 8), at = x % ((kBM - tr) * 8);
+      *reinterpret_cast<uint4*>(sm.q[box / kBoxes] + (box % kBoxes) * kBox + tr * 128 + at * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_async_smem();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 0 && elect_one()) {   // query tiles
     for (int q = 0; q < 2; ++q) {
-      mbar_arrive_tx(&sm.q_land[q], SM::kQ);
+      mbar_arrive_tx(&sm.q_land[q], (uint32_t)(kBoxes * tr * 128));
       for (int k = 0; k < kBoxes; ++k)
-        tma_load_4d(sm.q[q] + k * kBox, &tmq, kBoxDims * k, g * p.G, (r0 + q * kBM) / p.G, b, &sm.q_land[q]);
+        tma_load_4d(sm.q[q] + k * kBox, &tmq, kBoxDims * k, g * p.G, (r0 + q * tr) / p.G, b, &sm.q_land[q]);
     }
   }
   __syncwarp();
@@ -493,13 +502,14 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
     const int q = (warp - kSoftWarp0) >> 2;   // query tile of this group
     const int quarter = warp & 3;             // tensor-memory lane quarter of this warp
     const int rl = quarter * 32 + lane;
-    const int r = r0 + q * kBM + rl;
+    // Rows behind the tile's last (zeros) see what that one sees, and are not written.
+    const int r = r0 + q * tr + min(rl, tr - 1);
     const bool row_ok = r < nrows;
     const int i = row_ok ? r / p.G : 0;
     const int h = g * p.G + (row_ok ? r % p.G : 0);
     const int pos = past + i;
-    const bool live = row_ok && i < fresh;
-    const int hi_key = live ? pos + 1 : 0;    // visible keys [lo_key, hi_key)
+    const bool seen = row_ok && i < fresh, live = seen && rl < tr;
+    const int hi_key = seen ? pos + 1 : 0;    // visible keys [lo_key, hi_key)
     const int lo_key = p.window >= 0 ? max(0, pos - p.window) : 0;
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_addr = tmem + lane_addr + q * 128;
@@ -798,8 +808,8 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
     if (!group_all(ok, q)) {
       if (lane == 0) set_abort(p, sm);
     } else if (quarter == 0 && elect_one()) {   // one thread of the group
-      for (int k = 0; k < kBoxes; ++k)
-        tma_store_4d(&tmo, sm.q[q] + k * kBox, kBoxDims * k, g * p.G, (r0 + q * kBM) / p.G, b);
+      for (int k = 0; k < kBoxes && kBoxDims * k < p.H; ++k)
+        tma_store_4d(&tmo, sm.q[q] + k * kBox, kBoxDims * k, g * p.G, (r0 + q * tr) / p.G, b);
       bulk_commit();
       bulk_wait_read();   // the staged tile is read before the CTA may exit
     }
@@ -826,15 +836,15 @@ cudaError_t launch_one(const BlockParams& p, cudaStream_t st) {
   }
   CUtensorMap mq, mo, mk, mv;
   const uint64_t crows = (uint64_t)p.B * p.Nkv * p.C;
-  if ((e = encode_u8_2d(&mk, p.kc, crows, kHD, kHD, kHD, kBN)) != cudaSuccess) return e;
-  if ((e = encode_u8_2d(&mv, p.vc, crows, kHD, kHD, kHD, kBN)) != cudaSuccess) return e;
+  if ((e = encode_u8_2d(&mk, p.kc, crows, p.H, p.H, kHD, kBN)) != cudaSuccess) return e;
+  if ((e = encode_u8_2d(&mv, p.vc, crows, p.H, p.H, kHD, kBN)) != cudaSuccess) return e;
   auto encode = [&](CUtensorMap* m, const void* base) {
-    return F32 ? encode_f32_query_sw128(m, base, p.B, p.S, p.N, (uint32_t)p.G)
-               : encode_fp16_query_sw128(m, base, p.B, p.S, p.N, (uint32_t)p.G);
+    return F32 ? encode_f32_query_sw128(m, base, p.B, p.S, p.N, (uint32_t)p.G, (uint64_t)p.H)
+               : encode_fp16_query_sw128(m, base, p.B, p.S, p.N, (uint32_t)p.G, kBM, (uint64_t)p.H);
   };
   if ((e = encode(&mq, p.q)) != cudaSuccess) return e;
   if ((e = encode(&mo, p.out)) != cudaSuccess) return e;
-  const unsigned nqb = (unsigned)((p.S * p.G + 2 * kBM - 1) / (2 * kBM)), nbg = (unsigned)(p.B * p.Nkv);
+  const unsigned nqb = (unsigned)((p.S * p.G + 2 * p.tile_rows - 1) / (2 * p.tile_rows)), nbg = (unsigned)(p.B * p.Nkv);
   return launch_dependent(p.k != nullptr, kern, p.qb_major ? dim3(nbg, nqb) : dim3(nqb, nbg), kThreads, (size_t)smem, st,
                           p, mq, mo, mk, mv);
 }

@@ -1,5 +1,5 @@
-// Attention weights of the cache rows after a tensor-core prefill (head size
-// 128, group size dividing 128, fp16): w[j] = sum over the query rows r that
+// Attention weights of the cache rows after a tensor-core prefill (fp16, head
+// size up to 128, group size up to 64 or 128): w[j] = sum over the query rows r that
 // see key j of exp2(s_rj - lse_r), lse_r the row's log-sum-exp that the
 // prefill left in the workspace (log2 domain).
 //
@@ -80,7 +80,8 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
   const int i_lo = max(0, j0 - past);
   const int i_hi = p.window >= 0 ? min(fresh, j0 + kKeys + p.window - past) : fresh;
   const int rows0 = i_lo * p.G, rows1 = i_hi * p.G;
-  const int ntiles = rows1 > rows0 ? (rows1 - rows0 + kRows - 1) / kRows : 0;
+  const int tr = p.G < kRows ? kRows / p.G * p.G : kRows;   // rows of a tile in use: whole positions, or a part of one
+  const int ntiles = rows1 > rows0 ? (rows1 - rows0 + tr - 1) / tr : 0;
 
   if (warp == 1) tmem_alloc(&sm.tmem, 256);
   if (tid == 0) {
@@ -97,6 +98,13 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
     sm.abort = 0;
     mbar_fence_init();
   }
+  if (tr < kRows) {   // rows of the query tiles that no copy fills
+    for (int x = tid; x < 2 * kStages * (kRows - tr) * 8; x += kThreads) {
+      const int box = x / ((kRows - tr) * 8), at = x % ((kRows - tr) * 8);
+      *reinterpret_cast<uint4*>(sm.q[box / 2] + (box & 1) * kBox + tr * 128 + at * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_async_smem();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -104,10 +112,10 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
   // The key tile as fp16 pairs, a key per lane; rows behind the sequence are zeros.
   if (warp >= kSoftWarp0) {
     const int row = j0 + (warp & 3) * 32 + lane, half = (warp - kSoftWarp0) >> 2;
-    const uint4* src = reinterpret_cast<const uint4*>(p.kc + ((long long)bg * p.C + row) * kHD) + 4 * half;
+    const uint4* src = reinterpret_cast<const uint4*>(p.kc + ((long long)bg * p.C + row) * p.H) + 4 * half;
     uint32_t h[32];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) codes16(row < total ? src[k] : make_uint4(0u, 0u, 0u, 0u), h + 8 * k);
+    for (int k = 0; k < 4; ++k) codes16(row < total && 64 * half + 16 * k < p.H ? src[k] : make_uint4(0u, 0u, 0u, 0u), h + 8 * k);
     tmem_st32(tmem_k + ((uint32_t)((warp & 3) * 32) << 16) + 32 * half, h);
     tmem_st_wait();
   }
@@ -123,9 +131,9 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
       if (n == p.withhold_tile) break;   // testing: this tile is never copied, the waits for it expire
       ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_empty[n % kStages], ((uint32_t)(n / kStages) & 1u) ^ 1u, p.wait_budget) && !aborted(sm));
       if (ok && elect_one()) {
-        mbar_arrive_tx(&sm.q_full[n % kStages], kTile);
+        mbar_arrive_tx(&sm.q_full[n % kStages], (uint32_t)(2 * tr * 128));
         for (int k = 0; k < 2; ++k)
-          tma_load_4d(sm.q[n % kStages] + k * kBox, &tmq, 64 * k, g * p.G + n * kRows % p.G, i_lo + n * kRows / p.G, b,
+          tma_load_4d(sm.q[n % kStages] + k * kBox, &tmq, 64 * k, g * p.G + n * tr % p.G, i_lo + n * tr / p.G, b,
                       &sm.q_full[n % kStages]);
       }
       __syncwarp();
@@ -166,9 +174,9 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
   } else if (warp == 2) {
     // ================================================================ -lse of the rows, a tile ahead
     const float* lse = p.lse + (long long)bg * p.S * p.G;
-    auto load = [&](int n) -> float2 {   // rows from rows1 on are masked
-      const int r = rows0 + n * kRows + 2 * lane;
-      return make_float2(r < rows1 ? -lse[r] : 0.f, r + 1 < rows1 ? -lse[r + 1] : 0.f);
+    auto load = [&](int n) -> float2 {   // rows behind the tile's or the last one add nothing
+      const int r = rows0 + n * tr + 2 * lane, end = min(rows1, rows0 + (n + 1) * tr);
+      return make_float2(r < end ? -lse[r] : -INFINITY, r + 1 < end ? -lse[r + 1] : -INFINITY);
     };
     float2 next = load(0);
     bool ok = true;
@@ -203,9 +211,9 @@ block_weights_tc_kernel(const BlockParams p, const __grid_constant__ CUtensorMap
                                        mbar_wait(&sm.nl_full[bf], par, p.wait_budget) && !aborted(sm));
       if (!ok) break;
       tc_fence_after();
-      const int r0 = rows0 + n * kRows;
+      const int r0 = rows0 + n * tr;
       const int lo = r_lo - r0, hi = r_hi - r0;   // visible columns [lo, hi)
-      const bool full = __all_sync(0xffffffffu, lo <= 0 && hi >= kRows);
+      const bool full = __all_sync(0xffffffffu, lo <= 0 && hi >= tr);
       float2 acc = make_float2(0.f, 0.f), acc2 = make_float2(0.f, 0.f);
 #pragma unroll 1
       for (int c = 0; c < kRows; c += 32) {
@@ -299,7 +307,7 @@ cudaError_t launch_one(const BlockParams& p, cudaStream_t st) {
     done[dev] = true;
   }
   CUtensorMap mq;
-  if ((e = encode_fp16_query_sw128(&mq, p.q, p.B, p.S, p.N, (uint32_t)p.G, kRows)) != cudaSuccess) return e;
+  if ((e = encode_fp16_query_sw128(&mq, p.q, p.B, p.S, p.N, (uint32_t)p.G, kRows, (uint64_t)p.H)) != cudaSuccess) return e;
   const dim3 grid((unsigned)(p.B * p.Nkv), (unsigned)((p.T + kKeys - 1) / kKeys));
   return launch_dependent(true, block_weights_tc_kernel<CAP>, grid, kThreads, (size_t)smem, st, p, mq);
 }

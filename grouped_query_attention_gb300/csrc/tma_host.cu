@@ -52,10 +52,9 @@ cudaError_t encode_f32_2d(CUtensorMap* map, const void* base, uint64_t rows, uin
 }
 
 cudaError_t encode_fp16_query_sw128(CUtensorMap* map, const void* base, uint64_t B, uint64_t S, uint64_t N,
-                                    uint32_t G, uint32_t rows) {
+                                    uint32_t G, uint32_t rows, uint64_t H) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
-  const uint64_t H = 128;
   const cuuint64_t dims[4] = {H, N, S, B};
   const cuuint64_t strides[3] = {H * 2, N * H * 2, S * N * H * 2};
   const cuuint32_t box[4] = {64, G < rows ? G : rows, G < rows ? rows / G : 1, 1};
@@ -67,10 +66,9 @@ cudaError_t encode_fp16_query_sw128(CUtensorMap* map, const void* base, uint64_t
 }
 
 cudaError_t encode_f32_query_sw128(CUtensorMap* map, const void* base, uint64_t B, uint64_t S, uint64_t N,
-                                   uint32_t G) {
+                                   uint32_t G, uint64_t H) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
-  const uint64_t H = 128;
   const cuuint64_t dims[4] = {H, N, S, B};
   const cuuint64_t strides[3] = {H * 4, N * H * 4, S * N * H * 4};
   const cuuint32_t box[4] = {32, G, 128 / G, 1};

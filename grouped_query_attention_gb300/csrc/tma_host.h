@@ -14,20 +14,21 @@ namespace gqa {
 cudaError_t encode_fp16_2d_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                                  uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows);
 
-// 4D map of a (B, S, N, 128) fp16 query tensor (BSH layout, head size 128)
+// 4D map of a (B, S, N, H) fp16 query tensor (BSH layout, head size H <= 128)
 // with the 128-byte swizzle: boxes of 64 dims x G heads x rows/G positions x 1
 // batch land as `rows` rows of 128 bytes in (position, head) order, the layout
-// of a 64-column K-major MMA operand box; positions past S read as zero.
-// G must divide 128; a box of fewer rows than G holds that many heads of one position.
+// of a 64-column K-major MMA operand box; positions past S and dims past H read
+// as zero. Where G does not divide the rows, a box holds as many whole
+// positions as fit; one of fewer rows than G that many heads of one position.
 cudaError_t encode_fp16_query_sw128(CUtensorMap* map, const void* base, uint64_t B, uint64_t S, uint64_t N,
-                                    uint32_t G, uint32_t rows = 128);
+                                    uint32_t G, uint32_t rows = 128, uint64_t H = 128);
 
 // 4D map of a (B, S, N, 128) fp32 query tensor with the 128-byte swizzle:
 // boxes of 32 dims x G heads x 128/G positions x 1 batch land as 128 rows of
 // 128 bytes in (position, head) order; positions past S read as zero. G must
 // divide 128.
 cudaError_t encode_f32_query_sw128(CUtensorMap* map, const void* base, uint64_t B, uint64_t S, uint64_t N,
-                                   uint32_t G);
+                                   uint32_t G, uint64_t H = 128);
 
 // 2D map of a row-major [rows][cols] byte matrix without swizzle: boxes of
 // box_cols (a multiple of 16, <= 256) x box_rows bytes land as box_rows dense

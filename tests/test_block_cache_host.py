@@ -191,8 +191,9 @@ def test_plan_by_shape():
     prompt = plan(S=1024, H=128, C=1024, B=4)
     assert prompt.regime == capi.GQA_REGIME_PREFILL and prompt.launches == 2
     assert plan(S=16, H=128, C=32768, B=1).regime == capi.GQA_REGIME_DECODE
-    assert plan(S=1024, H=96, C=1024, B=4).regime == capi.GQA_REGIME_DECODE
-    assert plan(S=1024, H=128, N=6, C=1024, B=4).regime == capi.GQA_REGIME_DECODE     # a group of 3
+    assert plan(S=1024, H=96, C=1024, B=4).regime == capi.GQA_REGIME_PREFILL
+    assert plan(S=1024, H=128, N=6, C=1024, B=4).regime == capi.GQA_REGIME_PREFILL    # a group of 3
+    assert plan(S=1024, H=192, C=1024, B=4).regime == capi.GQA_REGIME_DECODE
 
 
 @pytest.mark.parametrize("attrs", [dict(causal=0), dict(do_rotary=1), dict(k_quant_type=1, v_quant_type=1),

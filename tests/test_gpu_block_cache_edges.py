@@ -69,6 +69,21 @@ def test_prompt_weights_of_group_sizes(N, Nkv, S, total, window, softcap):
     check(d, got)
 
 
+@pytest.mark.parametrize("softcap", [0.0, 4.0])
+@pytest.mark.parametrize("dtype,N,Nkv,H,S,total,window",
+                         [("f16", 14, 2, 128, 90, 300, -1), ("f32", 6, 2, 128, 150, 150, -1), ("f16", 5, 1, 64, 130, 257, 70),
+                          ("f32", 12, 1, 96, 60, 129, -1), ("f16", 8, 4, 16, 200, 200, -1), ("f32", 3, 3, 32, 150, 290, 33),
+                          ("f16", 48, 1, 80, 20, 150, -1), ("f32", 100, 1, 48, 6, 200, -1), ("f16", 65, 1, 112, 7, 140, -1),
+                          ("f16", 9, 3, 64, 129, 400, -1)])
+def test_prefill_of_odd_heads_and_groups(dtype, N, Nkv, H, S, total, window, softcap):
+    """Head sizes below 128 and groups that leave rows of a query tile empty, padded and empty sequences among them."""
+    d = make((dtype, 4, S, N, Nkv, H, 448, 32, (total, total - 3, S - 1, 0), (S, S - 3, S - 1, 0), window, softcap, 1, 1, 1),
+             seed=56)
+    got = run_gpu(d)
+    assert regime(got[3]) == capi.GQA_REGIME_PREFILL
+    check(d, got)
+
+
 @pytest.mark.parametrize("dtype,S", [("f16", 1), ("f32", 2), ("f16", 100), ("f32", 60)])
 def test_cache_offsets_beyond_32_bits(dtype, S):
     """A cache of 4.6 GB of codes each: the last sequence's rows lie behind 2^32."""

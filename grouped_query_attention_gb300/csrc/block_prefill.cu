@@ -217,10 +217,9 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
   const int i_hi = min((min(r0 + 2 * tr, nrows) - 1) / p.G, fresh - 1);
   if (i_lo > i_hi) {   // padding rows only
     dep_wait();
-    for (int x = tid; x < 2 * tr * p.H; x += kThreads) {
-      const int r = r0 + x / p.H, d = x % p.H;
-      if (r < nrows)
-        static_cast<T*>(p.out)[((long long)(b * (long long)p.S + r / p.G) * p.N + g * p.G + r % p.G) * p.H + d] = T(0.f);
+    for (int r = r0 + warp; r < min(r0 + 2 * tr, nrows); r += kThreads / 32) {   // a warp per row
+      T* o = static_cast<T*>(p.out) + ((long long)(b * (long long)p.S + r / p.G) * p.N + g * p.G + r % p.G) * p.H;
+      for (int x = lane; x < p.H * (int)sizeof(T) / 16; x += 32) reinterpret_cast<uint4*>(o)[x] = make_uint4(0u, 0u, 0u, 0u);
     }
     return;
   }

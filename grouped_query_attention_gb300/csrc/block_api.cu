@@ -143,8 +143,7 @@ bool use_prefill(const BlockParams& P, long long rows) {
   double tile = f32 ? 3.6 : cap ? 3.5 : 1.95;
   if (rows <= P.tile_rows) tile *= 1.4;
   const double prefill = 8.0 + waves * (waves > 1.0 ? mean : most) / 128.0 * tile;
-  const double workers = P.H > 128 ? 608.0 : 1216.0;
-  const double split = 10.0 + heads * nrt * (mean / 32.0 + 2.0) / workers * (cap ? 3.6 : 2.1) + heads * rows * 0.003;
+  const double split = 10.0 + heads * nrt * (mean / 32.0 + 2.0) / 1216.0 * (cap ? 3.6 : 2.1) + heads * rows * 0.003;
   return prefill <= split;
 }
 

@@ -36,7 +36,9 @@
 namespace gqa {
 namespace {
 
-constexpr int kWarps = 4;
+// Warps of a CTA. Three CTAs of four share an SM up to a head size of 128; behind
+// it a warp's ring takes 32 KB and one CTA of seven fills the shared memory.
+constexpr int warps_of(int H) { return H > 128 ? 7 : 4; }
 
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -279,7 +281,7 @@ __device__ void load_queries(const BlockParams& p, int b, int g, int rt, uint2 (
 // meets whole ranges (1.8e-6 against 0.6e-6 at 1500 keys); a decode step's
 // pieces are short and its registers go to a third CTA.
 template <typename T, int HP, int NT, bool PLAIN, bool FLUSH>
-__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<HP, NT, FLUSH>())
+__global__ void __launch_bounds__(warps_of(HP) * 32, ctas_per_sm<HP, NT, FLUSH>())
 block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
   constexpr bool kHalf = sizeof(T) == 2;
   constexpr int kParts = kHalf ? 1 : 2;     // fp16 parts of queries and probabilities
@@ -288,11 +290,11 @@ block_attn_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tmk, 
   constexpr float kGrow = 4.f;              // log2 growth of a maximum tolerated before rescaling
   extern __shared__ uint8_t smem_raw[];
   WarpSmem<HP>* rings = reinterpret_cast<WarpSmem<HP>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ WarpCtl ctls[kWarps];
+  __shared__ WarpCtl ctls[warps_of(HP)];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, t = lane & 3;
   WarpSmem<HP>& sm = rings[warp];
   WarpCtl& ctl = ctls[warp];
-  const long long worker = (long long)blockIdx.x * kWarps + warp;
+  const long long worker = (long long)blockIdx.x * warps_of(HP) + warp;
 
   if (lane == 0) {
     for (int s = 0; s < kStages; ++s) tc::mbar_init(&ctl.full[s], 1);
@@ -691,7 +693,7 @@ __device__ RangeInfo range_info(const BlockParams& p, int b, int gr) {
   return r;
 }
 
-constexpr int kMaxPieces = 152 * kWarps * 3 + 1;   // workers, at most
+constexpr int kMaxPieces = 152 * warps_of(128) * 3 + 1;   // workers, at most
 
 // Maximum / sum of v over the THREADS threads of the block.
 template <int THREADS, bool MAX>
@@ -1050,7 +1052,8 @@ cudaError_t allow_smem(K kern, int bytes, bool* done) {
 template <typename T, int HP, int NT, bool PLAIN, bool FLUSH>
 cudaError_t attn_one(const BlockParams& p, cudaStream_t st) {
   static bool done[kMaxDevices];
-  const int smem = kWarps * (int)sizeof(WarpSmem<HP>) + 1024;
+  constexpr int kWarps = warps_of(HP), smem = kWarps * (int)sizeof(WarpSmem<HP>) + 1024;
+  static_assert(smem + kWarps * sizeof(WarpCtl) <= 232448, "shared memory per CTA");
   cudaError_t e = allow_smem(block_attn_kernel<T, HP, NT, PLAIN, FLUSH>, smem, done);
   if (e != cudaSuccess) return e;
   CUtensorMap mk, mv;
@@ -1099,6 +1102,7 @@ int block_row_tile(int t_type, int H, long long rows) { return t_type == kF16 &&
 // One worker per warp, as many CTAs of four as an SM holds; fewer when there
 // are not four units for each.
 int block_workers(const BlockParams& p) {
+  const int kWarps = warps_of(p.H);
   const long long most = 152LL * kWarps * (p.H > 128 ? 1 : p.rt_rows > 8 || p.flush ? 2 : 3);
   const int keys = p.window >= 0 && (long long)p.window + p.S < p.T ? p.window + p.S + kBlockUnit : p.T;
   const long long units =

@@ -13,7 +13,7 @@
 //
 // Bound: exp2 (one per visible pair, 32 a clock and SM) and the MMAs, 512
 // clocks each per 128 x 128 pairs. Two prompts of 4096 tokens, 32 heads over 8
-// (537 M pairs): 129 us, either pipe 45 % busy, 2.3 instructions a clock; the
+// (537 M pairs): 133 us, either pipe 45 % busy, 2.3 instructions a clock; the
 // rest waits for S. With the key tile in shared memory, where the MMAs fetch
 // both operands (twice the bytes a clock can bring), it took 175 us; with whole
 // and masked tiles in one unrolled loop, whose instructions had to be fetched

@@ -237,11 +237,11 @@ gqa_status plan_block(const gqa_handle* h, const gqa_block_cache* cache, const g
   const long long rows = S * G;
   // (The prefill takes row maxima and masks before the scale: a negative one would turn them.)
   P.tile_rows = G <= 128 ? (int)(128 / G * G) : 0;
-  pl->prefill = H <= 128 && G <= 128 && P.scale > 0.f && rows > 16 && use_prefill(P, rows);
+  const long long nqb = G <= 128 ? (rows + 2 * P.tile_rows - 1) / (2 * P.tile_rows) : 0;
+  const bool grid_ok = nqb <= 65535 && (T + 127) / 128 <= 65535;
+  pl->prefill = H <= 128 && G <= 128 && P.scale > 0.f && rows > 16 && grid_ok && use_prefill(P, rows);
   pl->part_o = pl->part_ml = pl->stash = pl->lse = pl->o_acc = 0;
   if (pl->prefill) {
-    const long long nqb = (rows + 2 * P.tile_rows - 1) / (2 * P.tile_rows);
-    if (nqb > 65535 || (T + 127) / 128 > 65535) return fail(GQA_ERR_UNSUPPORTED, "query too large");
     if (P.t_type == gqa::kF32 && T > gqa::kPrefillFlush)
       pl->o_acc = align_up((size_t)(B * Nkv) * nqb * 2 * 128 * 128 * sizeof(float));
     P.qb_major = 2 * S >= T;   // key ranges differ by query block more than by sequence

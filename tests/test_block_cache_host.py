@@ -135,7 +135,7 @@ class Call:
         self.ev.total_sequence_length, self.ev.keep, self.ev.recent, self.ev.first = C, 40, 10, 2
 
     def t(self, dtype, shape):
-        self.next += 1 << 24
+        self.next += 1 << 36
         return capi.describe(self.next, dtype, shape)
 
     def make_cache(self, B, Nkv, C, H, bs, nb):
@@ -194,6 +194,7 @@ def test_plan_by_shape():
     assert plan(S=1024, H=96, C=1024, B=4).regime == capi.GQA_REGIME_PREFILL
     assert plan(S=1024, H=128, N=6, C=1024, B=4).regime == capi.GQA_REGIME_PREFILL    # a group of 3
     assert plan(S=1024, H=192, C=1024, B=4).regime == capi.GQA_REGIME_DECODE
+    assert plan(S=60000, H=64, C=8_500_000, B=1).regime == capi.GQA_REGIME_DECODE     # past the prefill's grid
 
 
 @pytest.mark.parametrize("attrs", [dict(causal=0), dict(do_rotary=1), dict(k_quant_type=1, v_quant_type=1),

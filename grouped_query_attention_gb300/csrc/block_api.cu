@@ -125,8 +125,8 @@ gqa_status check_block_cache(const gqa_block_cache& c, const char* name, long lo
 // 256 query rows of a KV head over their whole key range; few long ranges leave
 // most SMs idle there, while the split gives every warp an equal share. Both are
 // estimated from measurements (us; fp16, fp32, with a softcap): a wave of
-// prefill CTAs takes 1.95, 3.6, 3.5 per 128 keys (1.4 times that when only one
-// of its two query tiles has rows), a worker of the split 2.1, 2.1, 3.6
+// prefill CTAs takes 1.95, 3.6, 3.5 per 128 keys (0.95, fp32 1.1 times that for
+// one query tile, whose softmax nothing runs beside), a worker of the split 2.1, 2.1, 3.6
 // per 32 keys and row tile, its merge 0.003 per query row. Measured on both
 // sides: 64 rows a head on 32768 keys 492 against 240 us, 256 rows on 2048 keys
 // 43 against 96, 24 fp32 rows on 25000 keys 836 against 51.
@@ -141,7 +141,7 @@ bool use_prefill(const BlockParams& P, long long rows) {
   }
   const bool f32 = P.t_type == gqa::kF32, cap = P.softcap > 0.f;
   double tile = f32 ? 3.6 : cap ? 3.5 : 1.95;
-  if (rows <= P.tile_rows) tile *= 1.4;
+  if (rows <= P.tile_rows) tile *= f32 ? 1.1 : 0.95;
   const double prefill = 8.0 + waves * (waves > 1.0 ? mean : most) / 128.0 * tile;
   const double split = 10.0 + heads * nrt * (mean / 32.0 + 2.0) / 1216.0 * (cap ? 3.6 : 2.1) + heads * rows * 0.003;
   return prefill <= split;

@@ -36,7 +36,6 @@ constexpr int kKeys = 128;                     // keys of a CTA
 constexpr int kRows = 64;                      // query rows of a tile
 constexpr int kStages = 4;                     // query tiles in shared memory
 constexpr int kBufs = 3;                       // S buffers in tensor memory
-constexpr int kHD = 128;
 constexpr int kThreads = 384;
 constexpr int kSoftWarp0 = 4;
 constexpr uint32_t kBox = kRows * 128u;        // 64 rows x 128 bytes

@@ -84,6 +84,56 @@ def test_prefill_of_odd_heads_and_groups(dtype, N, Nkv, H, S, total, window, sof
     check(d, got)
 
 
+ONE_TILE = {   # at most 128 query rows a KV head
+    "f16": ("f16", 4, 30, 8, 2, 128, 448, 32, (300, 447, 30, 5), (30, 17, 30, 0), -1, 0, 1, 1, 1),
+    "f16_softcap": ("f16", 4, 30, 8, 2, 96, 448, 64, (300, 447, 30, 5), (30, 17, 30, 0), 100, 6.0, 0, 1, 1),
+    "f16_long": ("f16", 8, 32, 32, 8, 128, 1600, 64, (1500, 1100, 1600, 32, 33, 900, 1599, 700), None, -1, 0, 0, 1, 0),
+    "f32": ("f32", 16, 18, 14, 2, 64, 448, 16, (300, 447, 18, 5) * 4, (18, 17, 18, 0) * 4, -1, 0, 1, 1, 1),
+    "f32_softcap_long": ("f32", 16, 16, 16, 4, 128, 800, 64, (700,) * 16, None, -1, 6.0, 0, 0, 0),
+}
+
+
+@pytest.mark.parametrize("name", list(ONE_TILE))
+def test_prefill_of_one_query_tile(name):
+    d = make(ONE_TILE[name], seed=58)
+    got = run_gpu(d)
+    assert regime(got[3]) == capi.GQA_REGIME_PREFILL
+    check(d, got)
+
+
+@pytest.mark.parametrize("name,tile", [("f16", 0), ("f16_softcap", 1), ("f32", 1)])
+def test_withheld_copies_of_one_query_tile_time_out(name, tile):
+    d = make(ONE_TILE[name], seed=59)
+    op = GroupQueryAttention(d["N"], d["Nkv"], softcap=float(d["softcap"]), local_window_size=d["window"])
+    capi.gqa_set_wait_limit(op.handle, 200000, tile)
+    run_gpu(d, op)
+    assert op.block_status() == capi.GQA_DEVICE_TIMEOUT
+    capi.gqa_set_wait_limit(op.handle, 0, -1)
+    check(d, run_gpu(d, op))
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("dtype,N,Nkv,H", [("f16", 14, 2, 128), ("f32", 6, 2, 96), ("f16", 24, 8, 64)])
+def test_prefill_padding_and_free_rows_are_not_read(dtype, N, Nkv, H, bad):
+    """Padding rows of query, key and value, and scales of blocks behind the sequences, may hold anything."""
+    d = make((dtype, 3, 140, N, Nkv, H, 448, 32, (300, 139, 41), (140, 100, 41), -1, 0, 1, 1, 1), seed=57)
+    for b, (t, n) in enumerate(zip(d["totals"], d["news"])):
+        for x in (d["q"], d["k"], d["v"]):
+            x[b, n:] = bad
+        for x in d["cache"][2:]:
+            x[b, :, -(-int(t) // 32):] = bad
+        d["past_w"][b, :, t - n:] = bad
+    got = run_gpu(d)
+    assert regime(got[3]) == capi.GQA_REGIME_PREFILL
+    out, cache, w, op = got
+    ref = [x.copy() for x in d["cache"]]
+    for a, x, b in zip(cache, ref, range(4)):
+        if b >= 2:   # compare what the oracle compares: NaN equals NaN there
+            np.nan_to_num(a, copy=False), np.nan_to_num(x, copy=False)
+    d["cache"] = ref
+    check(d, (out, cache, w, op))
+
+
 @pytest.mark.parametrize("dtype,S", [("f16", 1), ("f32", 2), ("f16", 100), ("f32", 60)])
 def test_cache_offsets_beyond_32_bits(dtype, S):
     """A cache of 4.6 GB of codes each: the last sequence's rows lie behind 2^32."""

@@ -73,6 +73,10 @@ constexpr uint32_t kBox = 128u * 128u;         // 128 rows x 128 bytes
 constexpr uint32_t kTile = 2u * kBox;          // fp16 operand tile
 constexpr float kLazy = 8.0f;                  // log2 growth tolerated before rescaling O
 constexpr float kLift = 6.0f;
+// Keys whose V scale is below 2^-9 of the largest (kLift + log2 v' at most this)
+// enter the sum of the rounded probabilities with the exact ones: theirs may
+// round to nothing in fp16, and a block of zero values still has its weight.
+constexpr float kRoundedLv = kLift - 9.0f;
 constexpr uint32_t kIdO = idesc_f16(128, 128, 0, 1);
 
 // F32: hi and lo query tiles (the raw fp32 tile before) and one operand tile each of K and V; fp16: two each.
@@ -684,6 +688,7 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
           const float4 ig = *reinterpret_cast<const float4*>(&sm.iv[slot][bf * (STEP / 16) + 4 * hf]);
           const float kkg[4] = {kg.x * k_row, kg.y * k_row, kg.z * k_row, kg.w * k_row};
           const float ccg[4] = {lg.x - m_run, lg.y - m_run, lg.z - m_run, lg.w - m_run}, ivg[4] = {ig.x, ig.y, ig.z, ig.w};
+          [[maybe_unused]] const float lvg[4] = {lg.x, lg.y, lg.z, lg.w};
           if constexpr (kHalves == 2) tmem_ld_wait();
 #pragma unroll
           for (int qq = 0; qq < 2; ++qq) {
@@ -731,7 +736,7 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
               l_run = fmaf(lt.x + lt.y, ivg[gr], l_run);
               if constexpr (RND) {
                 const float2 rt = fadd2(lr[0], lr[1]);
-                l_rnd = fmaf(rt.x + rt.y, ivg[gr], l_rnd);
+                l_rnd = fmaf(lvg[gr] > kRoundedLv ? rt.x + rt.y : lt.x + lt.y, ivg[gr], l_rnd);
               }
             }
             tmem_st16(s_buf + hf * 64 + 16 * qq, ph);

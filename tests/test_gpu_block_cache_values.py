@@ -1,0 +1,46 @@
+"""Block-cache prefills on values at the ends of their ranges: V blocks of zeros or of far smaller scales."""
+
+import numpy as np
+import pytest
+
+from grouped_query_attention_gb300 import capi
+from test_gpu_block_cache import check, make, regime, run_gpu
+
+pytestmark = pytest.mark.gpu
+
+# One query tile (128 rows a KV head) and several; eight 16-token blocks.
+TILES = {"one_tile": (8, 16), "two_tiles": (60, 16)}
+
+
+@pytest.mark.parametrize("softcap", [0.0, 5.0])
+@pytest.mark.parametrize("tiles", list(TILES))
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("which", ["one_zero", "seven_zero", "far_apart", "near_border"])
+def test_value_blocks_of_far_smaller_scales(dtype, which, tiles, softcap):
+    """Their probabilities stay in the denominator, whatever of them the product with V can hold."""
+    S, G = TILES[tiles]
+    d = make((dtype, 2, S, 4 * G, 4, 128, 128, 16, (128, 125), None, -1, softcap, 0, 1, 0), seed=70)
+    d["cache"][2][:] = 0.01          # equal K scales: no block is without weight
+    vs = d["cache"][3]
+    vs[:] = 0.02
+    if which == "one_zero":
+        vs[:, :, 3] = 0
+    elif which == "seven_zero":
+        vs[:, :, [0, 1, 2, 4, 5, 6, 7]] = 0
+    elif which == "far_apart":
+        vs[:, :, ::2] *= np.float32(2.0 ** -35)
+    else:                            # about where fp16 probabilities run out of bits
+        vs *= np.float32(2.0) ** -np.array([0, 7, 8, 9, 10, 11, 20, 26], np.float32)
+    got = run_gpu(d)
+    assert regime(got[3]) == capi.GQA_REGIME_PREFILL
+    check(d, got)
+
+
+def test_appended_zero_values():
+    """The same through the append: a prompt whose middle rows have values of zero."""
+    d = make(("f16", 2, 60, 16, 4, 128, 128, 16, (60, 60), None, -1, 0, 0, 1, 1), seed=71)
+    d["v"][:, 16:48] = 0
+    d["k"] *= np.float16(0.25)
+    got = run_gpu(d)
+    assert regime(got[3]) == capi.GQA_REGIME_PREFILL
+    check(d, got)

@@ -72,6 +72,7 @@ constexpr int kScStages = 4;                   // scale slots: a tile's are read
 constexpr uint32_t kBox = 128u * 128u;         // 128 rows x 128 bytes
 constexpr uint32_t kTile = 2u * kBox;          // fp16 operand tile
 constexpr float kLazy = 8.0f;                  // log2 growth tolerated before rescaling O
+constexpr float kMinNormal = 1.17549435e-38f;
 constexpr float kLift = 6.0f;
 // Keys whose V scale is below 2^-9 of the largest (kLift + log2 v' at most this)
 // enter the sum of the rounded probabilities with the exact ones: theirs may
@@ -359,7 +360,7 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
       ok = __all_sync(0xffffffffu, mbar_wait(&sm.sc_empty[slot], ((uint32_t)(u / kScStages) & 1u) ^ 1u, p.wait_budget) && !aborted(sm));
       if (!ok) break;
       if (lane < kGroups) {
-        sm.ks[slot][lane] = fmaxf(scale, 1e-30f);   // positive: a mask of -inf stays -inf
+        sm.ks[slot][lane] = scale;
       } else if (lane < 2 * kGroups) {
         // v' at least 2^-60: a zero block's V adds nothing that counts, but its keys' P must reach l
         const float v = fminf(fmaxf(scale * __int_as_float((127 - wexp) << 23), 0x1p-60f), 1.f);
@@ -598,7 +599,9 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
         tmem_ld32(s_buf + hf * 64, x);
         tmem_ld32(s_buf + hf * 64 + 32, x + 32);
         const float4 kg = *reinterpret_cast<const float4*>(sc_k + 4 * hf);
-        const float ksg[4] = {kg.x, kg.y, kg.z, kg.w};
+        // (Scale and row factor first: either may be far out of range where their product is not. A group that
+        // is masked as a whole gives -inf, or NaN on a scale of 0, which the maximum passes over.)
+        const float ksg[4] = {kg.x * k_row, kg.y * k_row, kg.z * k_row, kg.w * k_row};
         tmem_ld_wait();
         if constexpr (CAP) {
           if (!full) {
@@ -643,8 +646,6 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
         }
       }
       if (kHalves == 2 && !full) tmem_st_wait();
-      mt *= k_row;
-      ua *= k_row;
       if constexpr (CAP) {
         if (mt > kNegBig) mt = cap_far(mt, c2);   // a reference: any rounding serves
       }
@@ -686,7 +687,9 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
           const float4 kg = *reinterpret_cast<const float4*>(sc_k + 4 * hf);
           const float4 lg = *reinterpret_cast<const float4*>(&sm.lv[slot][bf * (STEP / 16) + 4 * hf]);
           const float4 ig = *reinterpret_cast<const float4*>(&sm.iv[slot][bf * (STEP / 16) + 4 * hf]);
-          const float kkg[4] = {kg.x * k_row, kg.y * k_row, kg.z * k_row, kg.w * k_row};
+          // At least the smallest normal number: a masked score (-inf) times 0 would be NaN.
+          const float kkg[4] = {fmaxf(kg.x * k_row, kMinNormal), fmaxf(kg.y * k_row, kMinNormal),
+                                fmaxf(kg.z * k_row, kMinNormal), fmaxf(kg.w * k_row, kMinNormal)};
           const float ccg[4] = {lg.x - m_run, lg.y - m_run, lg.z - m_run, lg.w - m_run}, ivg[4] = {ig.x, ig.y, ig.z, ig.w};
           [[maybe_unused]] const float lvg[4] = {lg.x, lg.y, lg.z, lg.w};
           if constexpr (kHalves == 2) tmem_ld_wait();

@@ -1,10 +1,11 @@
-"""Block-cache prefills on values at the ends of their ranges: V blocks of zeros or of far smaller scales."""
+"""Block-cache prefills on values at the ends of their ranges: V blocks of zeros or of far smaller scales, scores that
+vanish beside masked ones, scales far out of range whose products are not."""
 
 import numpy as np
 import pytest
 
 from grouped_query_attention_gb300 import capi
-from test_gpu_block_cache import check, make, regime, run_gpu
+from test_gpu_block_cache import NP, check, make, regime, run_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -43,4 +44,35 @@ def test_appended_zero_values():
     d["k"] *= np.float16(0.25)
     got = run_gpu(d)
     assert regime(got[3]) == capi.GQA_REGIME_PREFILL
+    check(d, got)
+
+
+@pytest.mark.parametrize("softcap", [0.0, 0.5, 30.0])
+@pytest.mark.parametrize("tiles", list(TILES))
+@pytest.mark.parametrize("dtype,tiny", [("f32", 1e-20), ("f32", 1e-36), ("f16", 1.0)])
+def test_vanishing_scores_beside_masked_ones(dtype, tiny, tiles, softcap):
+    """Rows of tiny queries on key blocks of zeros: every masked key stays without weight, padding rows are zeros."""
+    S, G = TILES[tiles]
+    d = make((dtype, 3, S, 4 * G, 4, 128, 256, 16, (200, S, 131), (S, S - 3, S // 2), 90, softcap, 0, 1, 0), seed=72)
+    d["cache"][2][:] = 0.01
+    d["cache"][2][:, :, ::2] = 0
+    d["cache"][2][:, :, (200 - S) // 16:] = 0      # the diagonal of the first sequence
+    d["q"][:, ::3] *= NP[dtype](tiny)
+    d["q"][2, S // 2:] *= NP[dtype](tiny)     # padding rows
+    got = run_gpu(d)
+    assert regime(got[3]) == capi.GQA_REGIME_PREFILL
+    check(d, got)
+
+
+@pytest.mark.parametrize("softcap", [0.0, 2.0])
+@pytest.mark.parametrize("tiles", list(TILES) + ["split"])
+@pytest.mark.parametrize("factor", [1e30, 1e-30, 1e-35, 1e35])
+def test_scales_far_out_of_range(factor, tiles, softcap):
+    """Large queries on keys as much smaller, and the other way round: the scores are ordinary ones."""
+    S, G = TILES.get(tiles, (2, 8))
+    d = make(("f32", 2, S, 4 * G, 4, 128, 256, 16, (200, S + 7), (S, S - 1), -1, softcap, 0, 1, 0), seed=73)
+    d["q"] *= np.float32(factor)
+    d["cache"][2][:] /= np.float32(factor)
+    got = run_gpu(d)
+    assert (regime(got[3]) == capi.GQA_REGIME_PREFILL) == (tiles != "split")
     check(d, got)

@@ -216,7 +216,8 @@ gqa_status plan_block(const gqa_handle* h, const gqa_block_cache* cache, const g
   P.bs_log2 = log2_of(cache->block_size);
   P.nblk = (int)cache->key_scales.shape[2];
   P.t_type = q.dtype == GQA_F16 ? gqa::kF16 : gqa::kF32;
-  P.window = a.local_window_size;
+  // A window that reaches every row hides none; what remains is below 2^30, so the kernels' sums fit 32 bits.
+  P.window = a.local_window_size < T ? a.local_window_size : -1;
   P.scale = a.scale != 0.f ? a.scale : 1.0f / sqrtf((float)H);
   P.softcap = a.softcap;
   P.smooth = a.smooth_softmax == 1 ? 1 : 0;

@@ -1,5 +1,5 @@
 """Block-cache prefills on values at the ends of their ranges: V blocks of zeros or of far smaller scales, scores that
-vanish beside masked ones, scales far out of range whose products are not."""
+vanish beside masked ones, scales far out of range whose products are not, windows up to the largest."""
 
 import numpy as np
 import pytest
@@ -76,3 +76,20 @@ def test_scales_far_out_of_range(factor, tiles, softcap):
     got = run_gpu(d)
     assert (regime(got[3]) == capi.GQA_REGIME_PREFILL) == (tiles != "split")
     check(d, got)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 200, 2 ** 30, 301, 300, 299, 298])
+@pytest.mark.parametrize("dtype,N,Nkv,S,total", [("f16", 16, 4, 150, 150), ("f16", 16, 16, 150, 150), ("f32", 16, 4, 150, 150),
+                                                 ("f32", 4, 4, 150, 150), ("f16", 16, 4, 100, 300), ("f32", 16, 4, 100, 300),
+                                                 ("f16", 4, 2, 1, 300), ("f32", 4, 2, 3, 300), ("f32", 6, 2, 9, 300)])
+def test_windows_that_reach_every_row(dtype, N, Nkv, S, total, window):
+    """Output and weights at windows beside the length and at the attribute's largest values."""
+    d = make((dtype, 2, S, N, Nkv, 128, 320, 64, (total, S), None, window, 0, 1, 1, 1), seed=74)
+    check(d, run_gpu(d))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_the_largest_window_is_none(dtype):
+    case = (dtype, 2, 150, 16, 4, 128, 320, 64, (150, 300), None, 2 ** 31 - 1, 4.0, 1, 1, 1)
+    a, b = (run_gpu(make(case[:10] + (w,) + case[11:], seed=75)) for w in (2 ** 31 - 1, -1))
+    assert np.array_equal(a[0], b[0]) and np.array_equal(a[2], b[2])

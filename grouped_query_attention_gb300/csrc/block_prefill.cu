@@ -900,6 +900,10 @@ cudaError_t launch_block_prefill(const BlockParams& p, cudaStream_t st) {
   // in, so ranges up to 1024 keys are divided by what was added up (100 keys:
   // 2.3e-4 off instead of 4.1e-4, one rounding of the output 2.1e-4). On longer
   // ones the difference falls below 1e-4 and the second sum costs 12 % of the time.
+  // The rule is the call's bound, not what a row sees, so the first rows of a long
+  // prompt keep the 4.1e-4: a choice per CTA put two forms of the softmax into one
+  // kernel and took 4 to 6 % more also where no CTA rounds (664 -> 687 to 708 us,
+  // 394 -> 405 to 412 with 4096-token prompts), inside the steps or around them.
   if (p.T <= 1024) return cap ? launch_one<false, true, 64, true>(p, st) : launch_one<false, false, 128, true>(p, st);
   return cap ? launch_one<false, true, 64>(p, st) : launch_one<false, false, 128>(p, st);
 }

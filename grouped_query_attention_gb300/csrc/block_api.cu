@@ -324,6 +324,8 @@ gqa_status gqa_rotary_axes(gqa_handle* h, const gqa_rotary_inputs* in, const gqa
   for (const gqa_tensor* t : {&in->q_norm_weight, &in->k_norm_weight})
     if (present(*t) && (t->dtype != q.dtype || !shape_is(*t, 1, h1)))
       return fail(GQA_ERR_INVALID_ARGUMENT, "q/k_norm_weight must be (head_size) of the query dtype");
+  if (N * H > (1LL << 30))   // a token's coordinates are counted in 32 bits
+    return fail(GQA_ERR_UNSUPPORTED, "query hidden size %lld: at most 2^30", N * H);
   if (B * S > (1LL << 31) || B * S > kElems / (N * H)) return fail(GQA_ERR_UNSUPPORTED, "query too large");
   if ((s = check_status_word(status)) != GQA_OK) return s;
   const Named read[] = {{&in->query, "query"}, {&in->key, "key"}, {&in->positions, "positions"}, {&in->cos_cache, "cos_cache"},

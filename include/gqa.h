@@ -286,7 +286,8 @@ GQA_API gqa_status gqa_describe_plan(const gqa_handle* handle, const gqa_inputs*
  *   cos/sin_cache  T or float32 (R, D)
  *   q/k_norm_weight T (H): both or neither (without key: q only)
  * Outputs have the inputs' shapes; each may be its input (in place) and may
- * not overlap another tensor. D is a multiple of 8, num_axes 1 .. 8. */
+ * not overlap another tensor. D is a multiple of 8, num_axes 1 .. 8, N*H at
+ * most 2^30. */
 #define GQA_MAX_ROTARY_AXES 8
 typedef struct gqa_rotary_inputs {
   gqa_tensor query, key;

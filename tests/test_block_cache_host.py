@@ -281,6 +281,11 @@ def test_rotary_refuses(change, status):
     refused(c.rotary, status)
 
 
+@pytest.mark.parametrize("N", [(1 << 24) + 1, 1 << 26])
+def test_rotary_refuses_tokens_past_32_bits(N):
+    refused(Call(B=1, S=1, N=N, Nkv=1).rotary, UNSUPPORTED)
+
+
 @pytest.mark.parametrize("sections,interleaved,status", [((8, 12, 13), 0, INVALID), ((0, 0, 0), 0, INVALID),
                                                          ((40, -4, -4), 0, INVALID), ((4, 4, 4), 0, UNSUPPORTED),
                                                          ((8, 8, 16), 1, INVALID)])

@@ -35,6 +35,14 @@ def tensor_desc(t: torch.Tensor | None) -> capi.GqaTensor:
     return capi.describe(t.data_ptr(), _DTYPE_CODE[t.dtype], tuple(t.shape))
 
 
+def _int32(value, name: str) -> int:
+    """`value` as the C int it becomes (a ctypes field would keep its low 32 bits without a word)."""
+    v = int(value)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} {v} does not fit 32 bits")
+    return v
+
+
 class BlockCache:
     """An int8 K/V cache with one scale per block of tokens and KV head (``gqa_block_cache``).
 
@@ -175,7 +183,7 @@ class BlockCacheOps:
                 raise ValueError(f"sections: 1 to {capi.GQA_MAX_ROTARY_AXES} axes")
             inp, out = capi.GqaRotaryInputs(), capi.GqaRotaryOutputs()
             for i, n in enumerate(sec):
-                inp.sections[i] = int(n)
+                inp.sections[i] = _int32(n, "a section")
             inp.num_axes, inp.interleaved = len(sec), int(extra[1])
             return (inp, out), [inp.query, inp.key, inp.positions, inp.cos_cache, inp.sin_cache, inp.q_norm_weight,
                                 inp.k_norm_weight, out.query, out.key]
@@ -202,7 +210,7 @@ class BlockCacheOps:
 
         def build():
             inp, out, c = capi.GqaBlockInputs(), capi.GqaBlockOutputs(), capi.GqaBlockCache()
-            c.block_size = extra
+            c.block_size = _int32(extra, "block_size")
             return (c, inp, out), [inp.query, inp.key, inp.value, inp.seqlens_k, inp.new_lens, inp.head_sink,
                                    inp.past_weights, out.present_weights, out.output, c.key_codes, c.value_codes,
                                    c.key_scales, c.value_scales]
@@ -213,7 +221,7 @@ class BlockCacheOps:
             inp = rec.structs[1]
             if rec.nbytes is None or inp.total_sequence_length != total_sequence_length:
                 rec.nbytes = None
-                inp.total_sequence_length = int(total_sequence_length)
+                inp.total_sequence_length = _int32(total_sequence_length, "total_sequence_length")
                 rec.nbytes = capi.gqa_block_workspace_size(self.handle, *rec.structs)
             stream = _raw_stream(index)
             status = self._block_status_ptr.get(index) or self._status_word(query.device)
@@ -230,7 +238,7 @@ class BlockCacheOps:
             with torch.cuda.device(index):
                 return self.block_evict(cache, weights, seqlens_k, total_sequence_length, keep, into, into_weights,
                                         recent, first, kept, into_seqlens_k)
-        extra = (int(keep), int(recent), int(first), cache.block_size, into.block_size)
+        extra = (_int32(keep, "keep"), int(recent), int(first), cache.block_size, into.block_size)
         if kept is None:
             kept = torch.empty((*weights.shape[:2], max(0, extra[0])), dtype=torch.int32, device=weights.device)
         if into_seqlens_k is None:
@@ -238,7 +246,8 @@ class BlockCacheOps:
 
         def build():
             a = capi.GqaEvictArgs()
-            a.keep, a.recent, a.first, a.source.block_size, a.into.block_size = extra
+            names = ("keep", "recent", "first", "block_size", "block_size of into")
+            a.keep, a.recent, a.first, a.source.block_size, a.into.block_size = map(_int32, extra, names)
             return (a,), [a.weights, a.seqlens_k, a.into_weights, a.kept, a.into_seqlens_k, a.source.key_codes,
                           a.source.value_codes, a.source.key_scales, a.source.value_scales, a.into.key_codes,
                           a.into.value_codes, a.into.key_scales, a.into.value_scales]
@@ -246,7 +255,7 @@ class BlockCacheOps:
         with self._block_lock:
             rec = self._bind("evict", (weights, seqlens_k, into_weights, kept, into_seqlens_k, *cache.tensors(),
                                        *into.tensors()), extra, build)
-            rec.structs[0].total_sequence_length = int(total_sequence_length)
+            rec.structs[0].total_sequence_length = _int32(total_sequence_length, "total_sequence_length")
             status = self._block_status_ptr.get(index) or self._status_word(weights.device)
             capi.gqa_block_evict(self.handle, *rec.refs, status, _raw_stream(index))
         return kept, into_seqlens_k

@@ -351,3 +351,11 @@ def test_scale_attribute_default_is_the_frameworks():
     a, _, _ = ob.step(q, None, None, np.array([9]), None, cache, 16, 1, 1)
     b, _, _ = ob.step(q, None, None, np.array([9]), None, cache, 16, 1, 1, scale=0.25)
     assert np.array_equal(a, b)
+
+
+def test_python_integers_past_32_bits_are_refused():
+    from grouped_query_attention_gb300.block_cache import _int32
+    assert [_int32(v, "x") for v in (-2 ** 31, 0, torch.tensor(5), np.int64(2 ** 31 - 1))] == [-2 ** 31, 0, 5, 2 ** 31 - 1]
+    for v in (2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1):
+        with pytest.raises(ValueError, match="total_sequence_length"):
+            _int32(v, "total_sequence_length")

@@ -209,3 +209,23 @@ def test_captured_prompt_eviction_and_step():
         for x, y in zip(got, (*again, *cache.tensors(), *small.tensors(), w)):
             assert torch.equal(x, y)
     assert op.block_status() == 0
+
+
+def test_arguments_past_32_bits_are_refused():
+    """An integer whose low 32 bits alone would be a valid one."""
+    d = make(CASES["one_token"], seed=60)
+    op = GroupQueryAttention(d["N"], d["Nkv"])
+    run_gpu(d, op)
+    from test_gpu_block_cache import to_gpu_cache
+    cache, into, big = to_gpu_cache(d["cache"], 64), BlockCache.empty(3, 2, 200, 128), 1 << 32
+    q, w, seq = dev(d["q"]), dev(d["past_w"]), dev(d["totals"] - 1)
+    calls = [lambda: op.block_forward(q, None, None, seq, big + 200, cache),
+             lambda: op.block_forward(q, None, None, seq, 200, BlockCache(*cache.tensors(), big + 64)),
+             lambda: op.block_evict(cache, w, seq, big + 200, 20, into),
+             lambda: op.block_evict(cache, w, seq, 200, big + 20, into),
+             lambda: op.block_evict(cache, w, seq, 200, 20, into, recent=big + 1),
+             lambda: op.block_evict(cache, w, seq, 200, 20, into, first=big + 1)]
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
+    check(d, run_gpu(d, op))

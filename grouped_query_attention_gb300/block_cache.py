@@ -232,13 +232,16 @@ class BlockCacheOps:
     def block_evict(self, cache: BlockCache, weights, seqlens_k, total_sequence_length, keep: int, into: BlockCache,
                     into_weights=None, recent: int = 0, first: int = 0, kept=None, into_seqlens_k=None):
         """Copy the rows of `cache` that stay (first, recent, and the largest weights between) to `into`.
-        Returns (kept, into_seqlens_k): the source row of every kept row (-1 behind the last) and the lengths."""
+        Returns (kept, into_seqlens_k): the source row of every kept row (-1 behind the last) and the lengths.
+        For a sequence of a bad length (see block_status) both are -1 where they are made here, and left as they
+        were where they are given."""
         index = weights.get_device()
         if index >= 0 and index != _current_device():
             with torch.cuda.device(index):
                 return self.block_evict(cache, weights, seqlens_k, total_sequence_length, keep, into, into_weights,
                                         recent, first, kept, into_seqlens_k)
-        extra = (_int32(keep, "keep"), int(recent), int(first), cache.block_size, into.block_size)
+        extra = (_int32(keep, "keep"), int(recent), int(first), cache.block_size, into.block_size,
+                 (capi.GQA_FILL_KEPT if kept is None else 0) | (capi.GQA_FILL_SEQLENS if into_seqlens_k is None else 0))
         if kept is None:
             kept = torch.empty((*weights.shape[:2], max(0, extra[0])), dtype=torch.int32, device=weights.device)
         if into_seqlens_k is None:
@@ -246,8 +249,8 @@ class BlockCacheOps:
 
         def build():
             a = capi.GqaEvictArgs()
-            names = ("keep", "recent", "first", "block_size", "block_size of into")
-            a.keep, a.recent, a.first, a.source.block_size, a.into.block_size = map(_int32, extra, names)
+            names = ("keep", "recent", "first", "block_size", "block_size of into", "fill_skipped")
+            a.keep, a.recent, a.first, a.source.block_size, a.into.block_size, a.fill_skipped = map(_int32, extra, names)
             return (a,), [a.weights, a.seqlens_k, a.into_weights, a.kept, a.into_seqlens_k, a.source.key_codes,
                           a.source.value_codes, a.source.key_scales, a.source.value_scales, a.into.key_codes,
                           a.into.value_codes, a.into.key_scales, a.into.value_scales]

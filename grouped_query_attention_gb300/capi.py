@@ -62,6 +62,7 @@ class GqaOutputs(ctypes.Structure):
 
 
 GQA_MAX_ROTARY_AXES = 8
+GQA_FILL_KEPT, GQA_FILL_SEQLENS = 1, 2
 
 
 class GqaRotaryInputs(ctypes.Structure):
@@ -93,7 +94,7 @@ class GqaBlockOutputs(ctypes.Structure):
 class GqaEvictArgs(ctypes.Structure):
     _fields_ = [("source", GqaBlockCache), ("into", GqaBlockCache)] + \
                [(n, GqaTensor) for n in ("weights", "seqlens_k", "into_weights", "kept", "into_seqlens_k")] + \
-               [(n, ctypes.c_int32) for n in ("total_sequence_length", "keep", "recent", "first")]
+               [(n, ctypes.c_int32) for n in ("total_sequence_length", "keep", "recent", "first", "fill_skipped")]
 
 
 class GqaPlanInfo(ctypes.Structure):

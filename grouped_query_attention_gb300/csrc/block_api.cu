@@ -456,6 +456,7 @@ gqa_status gqa_block_evict(gqa_handle* h, const gqa_evict_args* a, void* status,
   if (Cto < (keep < T ? keep : T))
     return fail(GQA_ERR_INVALID_ARGUMENT, "into holds %lld rows; min(keep, total_sequence_length) = %lld are needed", Cto, keep < T ? keep : T);
   if (keep > (1LL << 30)) return fail(GQA_ERR_UNSUPPORTED, "keep too large");
+  if (a->fill_skipped & ~(GQA_FILL_KEPT | GQA_FILL_SEQLENS)) return fail(GQA_ERR_INVALID_ARGUMENT, "unknown fill_skipped bits");
   const int64_t ws[3] = {B, Nkv, C}, wt[3] = {B, Nkv, Cto}, kp[3] = {B, Nkv, keep}, b1[1] = {B};
   if (!present(a->weights) || a->weights.dtype != GQA_F32 || !shape_is(a->weights, 3, ws))
     return fail(GQA_ERR_INVALID_ARGUMENT, "weights must be float32 (B, kv_num_heads, C)");
@@ -482,6 +483,7 @@ gqa_status gqa_block_evict(gqa_handle* h, const gqa_evict_args* a, void* status,
   P.nblk = (int)a->from.key_scales.shape[2];
   P.nblk_to = (int)a->into.key_scales.shape[2];
   P.keep = a->keep; P.recent = a->recent; P.first = a->first;
+  P.fill = a->fill_skipped;
   P.kc = static_cast<const int8_t*>(a->from.key_codes.data);
   P.vc = static_cast<const int8_t*>(a->from.value_codes.data);
   P.ks = static_cast<const float*>(a->from.key_scales.data);

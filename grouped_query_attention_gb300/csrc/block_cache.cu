@@ -3,6 +3,7 @@
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
+#include "../../include/gqa.h"
 #include "block_internal.h"
 #include "common.cuh"
 
@@ -294,13 +295,18 @@ evict_select_kernel(const EvictParams p, int CL) {
   const int bg = blockIdx.x / CL, b = bg / p.Nkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int total = p.seqlens[b] + 1;
   dep_launch();
+  int* kept = p.kept + (long long)bg * p.keep;
+  const int step = CL * kSelThreads, at = rank * kSelThreads + tid;
   if (total < 0 || total > p.C || total > p.T) {   // every CTA of the cluster leaves
-    if (bg % p.Nkv == 0 && rank == 0 && tid == 0 && p.status) atomicOr(p.status, GQA_DEVICE_BAD_SEQLEN_BIT);
+    if (bg % p.Nkv == 0 && rank == 0 && tid == 0) {
+      if (p.status) atomicOr(p.status, GQA_DEVICE_BAD_SEQLEN_BIT);
+      if (p.fill & GQA_FILL_SEQLENS) p.seqlens_to[b] = -1;
+    }
+    if (p.fill & GQA_FILL_KEPT)
+      for (int i = at; i < p.keep; i += step) kept[i] = -1;
     return;
   }
-  int* kept = p.kept + (long long)bg * p.keep;
   if (bg % p.Nkv == 0 && rank == 0 && tid == 0) p.seqlens_to[b] = min(total, p.keep) - 1;
-  const int step = CL * kSelThreads, at = rank * kSelThreads + tid;
   if (total <= p.keep) {
     for (int i = at; i < p.keep; i += step) kept[i] = i < total ? i : -1;
     return;

@@ -120,6 +120,7 @@ struct EvictParams {
   int B, Nkv, H, C, Cto, T;
   int bs_log2, nblk, nblk_to;
   int keep, recent, first;
+  int fill;              // GQA_FILL_* bits: what a skipped sequence's entries become -1 of
   const int8_t *kc, *vc;
   const float *ks, *vs;
   int8_t *kc_to, *vc_to;

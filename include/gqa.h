@@ -408,14 +408,19 @@ GQA_API gqa_status gqa_block_describe_plan(const gqa_handle* handle, const gqa_b
  * rows of a block with that scale keep their codes, the others are rounded
  * anew (nearest, ties to even). Rows and blocks behind the last kept row keep
  * their bytes. A sequence with total_b outside [0, min(C, total_sequence_length)]
- * is skipped and sets GQA_DEVICE_BAD_SEQLEN.
+ * is skipped and sets GQA_DEVICE_BAD_SEQLEN; its entries of kept and
+ * into_seqlens_k keep their values, or become -1 (no row, an empty slot) with
+ * GQA_FILL_KEPT and GQA_FILL_SEQLENS in fill_skipped.
  * 0 <= first, 0 <= recent, 1 <= keep, first + recent <= keep. */
+#define GQA_FILL_KEPT 1
+#define GQA_FILL_SEQLENS 2
 typedef struct gqa_evict_args {
   gqa_block_cache from, into;
   gqa_tensor weights, seqlens_k;
   gqa_tensor into_weights, kept, into_seqlens_k;
   int32_t total_sequence_length;
   int32_t keep, recent, first;
+  int32_t fill_skipped; /* 0, or GQA_FILL_* bits */
 } gqa_evict_args;
 
 /* Two launches on `stream`, no workspace; of the handle's attributes only

@@ -313,6 +313,8 @@ def test_rotary_refuses_sections(sections, interleaved, status):
     (_set("ev.into_weights", lambda c: c.ev.weights), INVALID),
     (_set("ev.into_seqlens_k", lambda c: c.ev.seqlens_k), INVALID),
     (_set("ev.kept", capi.GqaTensor()), INVALID),
+    (_set("ev.fill_skipped", 4), INVALID),
+    (_set("ev.fill_skipped", -1), INVALID),
 ])
 def test_evict_refuses(change, status):
     c = Call()

@@ -229,3 +229,24 @@ def test_arguments_past_32_bits_are_refused():
         with pytest.raises(ValueError):
             call()
     check(d, run_gpu(d, op))
+
+
+@pytest.mark.parametrize("C", [64, 20000, 140000])
+def test_eviction_made_here_holds_no_rows_of_a_skipped_sequence(C):
+    """kept and the lengths that the call allocates are -1 there (the allocator's memory is filled beforehand)."""
+    op, keep = GroupQueryAttention(2, 2), C // 3
+    cache, into = BlockCache.empty(3, 2, C, 16, 16), BlockCache.empty(3, 2, keep, 16, 16)
+    w = torch.rand((3, 2, C), device="cuda")
+    seq = torch.tensor([C, C - 5, -2], dtype=torch.int32, device="cuda")
+    for given in range(4):
+        junk = [torch.full((3, 2, keep), 12345, dtype=torch.int32, device="cuda") for _ in range(4)] + \
+               [torch.full((3,), 12345, dtype=torch.int32, device="cuda") for _ in range(4)]
+        own = (junk[0] if given & 1 else None, junk[4] if given & 2 else None)
+        del junk
+        kept, lens = op.block_evict(cache, w, seq, C, keep, into, recent=3, kept=own[0], into_seqlens_k=own[1])
+        assert op.block_status() == capi.GQA_DEVICE_BAD_SEQLEN
+        for b in (0, 2):
+            assert (kept[b] == (12345 if given & 1 else -1)).all()
+            assert int(lens[b]) == (12345 if given & 2 else -1)
+        assert int(lens[1]) == keep - 1 and bool((kept[1, :, 1:] > kept[1, :, :-1]).all())
+        assert bool((kept[1, :, -3:] == torch.arange(C - 7, C - 4, device="cuda")).all())

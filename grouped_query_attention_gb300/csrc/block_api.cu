@@ -130,11 +130,13 @@ gqa_status check_block_cache(const gqa_block_cache& c, const char* name, long lo
 // per 32 keys and row tile, its merge 0.003 per query row. Measured on both
 // sides: 64 rows a head on 32768 keys 492 against 240 us, 256 rows on 2048 keys
 // 43 against 96, 24 fp32 rows on 25000 keys 836 against 51.
-bool use_prefill(const BlockParams& P, long long rows) {
+bool use_prefill(const BlockParams& P) {
+  const int live = P.S < P.T ? P.S : P.T;   // positions behind total_sequence_length are padding
+  const long long rows = (long long)live * P.G;
   const int rt = gqa::block_row_tile(P.t_type, P.H, rows);
   const double nrt = (double)((rows + rt - 1) / rt), heads = (double)P.B * P.Nkv;
   const double ctas = heads * (double)((rows + 2 * P.tile_rows - 1) / (2 * P.tile_rows)), waves = ceil(ctas / 152.0);
-  double mean = P.T - 0.5 * P.S, most = P.T;   // keys a query row sees
+  double mean = P.T - 0.5 * live, most = P.T;   // keys a query row sees
   if (P.window >= 0) {
     mean = mean < P.window ? mean : P.window;
     most = most < (double)P.window + P.S ? most : (double)P.window + P.S;
@@ -240,7 +242,7 @@ gqa_status plan_block(const gqa_handle* h, const gqa_block_cache* cache, const g
   P.tile_rows = G <= 128 ? (int)(128 / G * G) : 0;
   const long long nqb = G <= 128 ? (rows + 2 * P.tile_rows - 1) / (2 * P.tile_rows) : 0;
   const bool grid_ok = nqb <= 65535 && (T + 127) / 128 <= 65535;
-  pl->prefill = H <= 128 && G <= 128 && P.scale > 0.f && rows > 16 && grid_ok && use_prefill(P, rows);
+  pl->prefill = H <= 128 && G <= 128 && P.scale > 0.f && rows > 16 && grid_ok && use_prefill(P);
   pl->part_o = pl->part_ml = pl->stash = pl->lse = pl->o_acc = 0;
   if (pl->prefill) {
     if (P.t_type == gqa::kF32 && T > gqa::kPrefillFlush)

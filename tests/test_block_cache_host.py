@@ -361,3 +361,14 @@ def test_python_integers_past_32_bits_are_refused():
     for v in (2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1):
         with pytest.raises(ValueError, match="total_sequence_length"):
             _int32(v, "total_sequence_length")
+
+
+@pytest.mark.parametrize("B,Nkv,S,T", [(1, 8, 4096, 300), (1, 1, 4096, 1000), (8, 8, 4096, 1000), (64, 2, 1024, 100)])
+def test_plan_of_padded_prompts(B, Nkv, S, T):
+    """Positions behind total_sequence_length are padding: the plan is that of a prompt of T tokens."""
+    plans = []
+    for s in (S, T):
+        c = Call(B=B, S=s, N=4 * Nkv, Nkv=Nkv, H=128, C=4096, bs=64)
+        c.inp.total_sequence_length = T
+        plans.append(c._run(lambda h: capi.gqa_block_describe_plan(h, c.cache, c.inp, c.out)).regime)
+    assert plans == [capi.GQA_REGIME_PREFILL] * 2

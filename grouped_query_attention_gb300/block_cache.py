@@ -165,7 +165,8 @@ class BlockCacheOps:
                     q_norm_weight=None, k_norm_weight=None, out_query=None, out_key=None):
         """Rotate query (and key, or None) at positions (axes, B, S) on several axes; returns (query, key).
 
-        sections: pairs of each axis. out_query / out_key may be the inputs (in place)."""
+        sections: pairs of each axis. out_query / out_key may be the inputs (in place). A token of a bad position
+        is not written (block_status tells), also not in tensors made here."""
         index = query.get_device()
         if index >= 0 and index != _current_device():
             with torch.cuda.device(index):
@@ -198,7 +199,9 @@ class BlockCacheOps:
     def block_forward(self, query, key, value, seqlens_k, total_sequence_length, cache: BlockCache, new_lens=None,
                       head_sink=None, past_weights=None, present_weights=None, output=None):
         """One step over a block-scaled cache: store key / value (None: already stored), attend, and with
-        present_weights add up the attention weight of every cache row. Returns ``output``."""
+        present_weights add up the attention weight of every cache row. Returns ``output``. total_sequence_length is
+        an upper bound of the lengths. Nothing of a sequence of a bad length is written (block_status tells), also
+        not in an output made here."""
         index = query.get_device()
         if index >= 0 and index != _current_device():
             with torch.cuda.device(index):

@@ -6,7 +6,9 @@ include/gqa.h. This package adds argument marshalling for torch tensors:
 torch's allocator and calls ``gqa_forward`` on the current stream. Its methods
 ``rotary_axes``, ``block_forward`` and ``block_evict`` (block_cache.py) are the
 multi-axis rotary embedding, attention over a block-scaled int8 cache
-(``BlockCache``) and the eviction from one.
+(``BlockCache``) and the eviction from one; ``tree_forward``, ``tree_verify`` and
+``tree_accept`` (tree.py) are attention for drafted tokens over a float cache,
+their verification and moving the accepted rows together.
 """
 
 from __future__ import annotations
@@ -16,6 +18,7 @@ import torch
 from . import capi
 from .block_cache import BlockCache, BlockCacheOps, tensor_desc  # noqa: F401
 from .capi import GqaError, GqaInputs, GqaOutputs, describe, make_attrs  # noqa: F401
+from .tree import TreeOps
 
 def _tensor_key(t: torch.Tensor | None):
     """What a tensor's C descriptor depends on (None for an absent input)."""
@@ -24,7 +27,7 @@ def _tensor_key(t: torch.Tensor | None):
     return t.data_ptr(), t.shape, t.dtype, t.is_contiguous()
 
 
-class GroupQueryAttention(BlockCacheOps):
+class GroupQueryAttention(BlockCacheOps, TreeOps):
     """One operator instance: attributes fixed at construction (section Attributes)."""
 
     def __init__(self, num_heads: int, kv_num_heads: int, **attrs):

@@ -22,16 +22,19 @@ GQA_DTYPE_NONE, GQA_F32, GQA_F16, GQA_I8, GQA_U8, GQA_I32, GQA_BF16 = range(7)
 QUANT = {"NONE": 0, "PER_TENSOR": 1, "PER_CHANNEL": 2}
 # device status bits
 GQA_DEVICE_BAD_SEQLEN, GQA_DEVICE_BAD_ROTARY, GQA_DEVICE_TIMEOUT = 1, 2, 4
+GQA_DEVICE_BAD_TREE, GQA_DEVICE_BAD_PROBS = 8, 16
 
 EXPORTS = ["gqa_attrs_default", "gqa_create", "gqa_workspace_size", "gqa_forward",
            "gqa_read_device_status", "gqa_describe_plan", "gqa_destroy", "gqa_status_string",
            "gqa_last_error", "gqa_forward_noalloc", "gqa_profile_begin", "gqa_profile_end",
            "gqa_set_wait_limit", "gqa_rotary_axes", "gqa_block_workspace_size", "gqa_block_describe_plan",
-           "gqa_block_forward", "gqa_block_evict"]
+           "gqa_block_forward", "gqa_block_evict", "gqa_tree_workspace_size", "gqa_tree_describe_plan",
+           "gqa_tree_forward", "gqa_tree_verify", "gqa_tree_accept"]
 KERNEL_KINDS = {1: "copy_past", 2: "prepass", 3: "decode", 4: "prefill_cuda_core", 5: "prefill_tensor_core",
                 6: "decode_tensor_core", 7: "window_shift", 8: "bias_stage", 9: "rotary_axes", 10: "block_append",
                 11: "block_attention", 12: "block_merge", 13: "block_prefill", 14: "block_weights",
-                15: "evict_select", 16: "evict_gather"}
+                15: "evict_select", 16: "evict_gather", 17: "tree_attention", 18: "tree_merge", 19: "tree_verify",
+                20: "tree_accept"}
 GQA_REGIME_DECODE, GQA_REGIME_PREFILL = 1, 2
 
 
@@ -97,6 +100,29 @@ class GqaEvictArgs(ctypes.Structure):
                [(n, ctypes.c_int32) for n in ("total_sequence_length", "keep", "recent", "first", "fill_skipped")]
 
 
+GQA_MAX_TREE_NODES, GQA_MAX_TREE_LAYERS = 512, 128
+
+
+class GqaTreeInputs(ctypes.Structure):
+    _fields_ = [(n, GqaTensor) for n in ("query", "key", "value", "parents", "seqlens_k", "new_lens", "head_sink")] + \
+               [("total_sequence_length", ctypes.c_int32)]
+
+
+class GqaTreeOutputs(ctypes.Structure):
+    _fields_ = [(n, GqaTensor) for n in ("output", "present_key", "present_value")]
+
+
+class GqaVerifyArgs(ctypes.Structure):
+    _fields_ = [(n, GqaTensor) for n in ("tokens", "parents", "target_probs", "draft_probs", "accept_uniforms",
+                                         "sample_uniforms", "new_lens", "path", "path_lens", "next_token")]
+
+
+class GqaAcceptArgs(ctypes.Structure):
+    _fields_ = [("present_keys", ctypes.POINTER(GqaTensor)), ("present_values", ctypes.POINTER(GqaTensor)),
+                ("num_layers", ctypes.c_int32)] + \
+               [(n, GqaTensor) for n in ("path", "path_lens", "seqlens_k", "new_lens", "into_seqlens_k")]
+
+
 class GqaPlanInfo(ctypes.Structure):
     _fields_ = [("regime", ctypes.c_int32), ("launches", ctypes.c_int32), ("split_len", ctypes.c_int32),
                 ("max_splits", ctypes.c_int32), ("workspace_bytes", ctypes.c_uint64)]
@@ -160,6 +186,16 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.gqa_block_forward.restype = ctypes.c_int
     lib.gqa_block_evict.argtypes = [V, P(GqaEvictArgs), V, V]
     lib.gqa_block_evict.restype = ctypes.c_int
+    lib.gqa_tree_workspace_size.argtypes = [V, P(GqaTreeInputs), P(GqaTreeOutputs), P(ctypes.c_size_t)]
+    lib.gqa_tree_workspace_size.restype = ctypes.c_int
+    lib.gqa_tree_describe_plan.argtypes = [V, P(GqaTreeInputs), P(GqaTreeOutputs), P(GqaPlanInfo)]
+    lib.gqa_tree_describe_plan.restype = ctypes.c_int
+    lib.gqa_tree_forward.argtypes = [V, P(GqaTreeInputs), P(GqaTreeOutputs), V, ctypes.c_size_t, V, V]
+    lib.gqa_tree_forward.restype = ctypes.c_int
+    lib.gqa_tree_verify.argtypes = [V, P(GqaVerifyArgs), V, V]
+    lib.gqa_tree_verify.restype = ctypes.c_int
+    lib.gqa_tree_accept.argtypes = [V, P(GqaAcceptArgs), V, V]
+    lib.gqa_tree_accept.restype = ctypes.c_int
     lib.gqa_destroy.argtypes = [ctypes.c_void_p]
     lib.gqa_destroy.restype = None
     lib.gqa_status_string.argtypes = [ctypes.c_int]
@@ -275,6 +311,37 @@ def gqa_block_forward(handle, cache: GqaBlockCache, inputs: GqaBlockInputs, outp
 
 def gqa_block_evict(handle, args: GqaEvictArgs, status: int, stream: int) -> None:
     st = (_lib or load_library()).gqa_block_evict(handle, args, status, stream)
+    if st != GQA_OK:
+        _check(st)
+
+
+def gqa_tree_workspace_size(handle, inputs: GqaTreeInputs, outputs: GqaTreeOutputs) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().gqa_tree_workspace_size(handle, inputs, outputs, ctypes.byref(n)))
+    return n.value
+
+
+def gqa_tree_describe_plan(handle, inputs: GqaTreeInputs, outputs: GqaTreeOutputs) -> GqaPlanInfo:
+    info = GqaPlanInfo()
+    _check(load_library().gqa_tree_describe_plan(handle, inputs, outputs, ctypes.byref(info)))
+    return info
+
+
+def gqa_tree_forward(handle, inputs: GqaTreeInputs, outputs: GqaTreeOutputs, workspace: int, workspace_bytes: int,
+                     status: int, stream: int) -> None:
+    st = (_lib or load_library()).gqa_tree_forward(handle, inputs, outputs, workspace, workspace_bytes, status, stream)
+    if st != GQA_OK:
+        _check(st)
+
+
+def gqa_tree_verify(handle, args: GqaVerifyArgs, status: int, stream: int) -> None:
+    st = (_lib or load_library()).gqa_tree_verify(handle, args, status, stream)
+    if st != GQA_OK:
+        _check(st)
+
+
+def gqa_tree_accept(handle, args: GqaAcceptArgs, status: int, stream: int) -> None:
+    st = (_lib or load_library()).gqa_tree_accept(handle, args, status, stream)
     if st != GQA_OK:
         _check(st)
 

@@ -239,6 +239,8 @@ GQA_API gqa_status gqa_set_wait_limit(gqa_handle* handle, int64_t cycles, int32_
 #define GQA_DEVICE_BAD_SEQLEN 1u  /* seqlens_k out of range for the cache / total length / S */
 #define GQA_DEVICE_BAD_ROTARY 2u  /* a rotary position is not covered by cos/sin_cache rows */
 #define GQA_DEVICE_TIMEOUT 4u     /* a bounded pipeline wait gave up (kernel returned early) */
+#define GQA_DEVICE_BAD_TREE 8u    /* a parent or a path entry out of range (gqa_tree_*) */
+#define GQA_DEVICE_BAD_PROBS 16u  /* a row without a positive probability to draw from (gqa_tree_verify) */
 GQA_API gqa_status gqa_read_device_status(gqa_handle* handle, void* workspace, void* stream, uint32_t* status);
 
 /* Host-only description of how gqa_forward would run a call: the regime
@@ -427,6 +429,136 @@ typedef struct gqa_evict_args {
  * kv_num_heads applies. */
 GQA_API gqa_status gqa_block_evict(gqa_handle* handle, const gqa_evict_args* args, void* status, void* stream);
 
+/* ---- Drafted tokens: tree attention, verification, accepted rows ----------
+ * Generation that drafts several continuations of every sequence and lets the
+ * model judge all of them in one step. The drafts of a sequence are n_b nodes,
+ * n_b = new_lens[b] (S without new_lens; 0 <= n_b <= S). Node i has the parent
+ * parents[b][i], a node before it, or -1: parents[b][i] < i. Node 0 is the root,
+ * the sequence's newest known token; a chain has parents -1, 0, 1, 2, ... The
+ * caches are float caches as of gqa_forward's shared buffer, T (B, N_kv, C, H);
+ * node i of sequence b is cache row past_b + i, past_b = seqlens_k[b] + 1 - n_b,
+ * and seqlens_k[b] may be -1 with n_b = 0 (an empty slot).
+ *   parents   int32 (B, S), or (1, S): one tree for all sequences
+ * A parent outside [-1, i) counts as -1 and sets GQA_DEVICE_BAD_TREE. Nodes
+ * i >= n_b are padding; their parents are not looked at. */
+#define GQA_MAX_TREE_NODES 512   /* S at most */
+#define GQA_MAX_TREE_LAYERS 128  /* caches of one gqa_tree_accept call at most */
+
+/*   query            T (B, S, N*H), prepared (see gqa_rotary_axes; a node's place
+ *                    in its sequence is past_b + depth, the root's depth is 0)
+ *   key, value       T (B, S, N_kv*H), prepared alike
+ *   head_sink        T (N) or absent
+ *   total_sequence_length  HOST scalar, at least the largest seqlens_k[b] + 1, at most C */
+typedef struct gqa_tree_inputs {
+  gqa_tensor query, key, value;
+  gqa_tensor parents;
+  gqa_tensor seqlens_k, new_lens;
+  gqa_tensor head_sink;
+  int32_t total_sequence_length;
+} gqa_tree_inputs;
+
+/*   output               T (B, S, N*H); padding rows are written as 0
+ *   present_key/value    T (B, N_kv, C, H), updated in place */
+typedef struct gqa_tree_outputs {
+  gqa_tensor output;
+  gqa_tensor present_key, present_value;
+} gqa_tree_outputs;
+
+/* Bytes of workspace gqa_tree_forward needs for these shapes (host-only; runs
+ * every host-side check). */
+GQA_API gqa_status gqa_tree_workspace_size(const gqa_handle* handle, const gqa_tree_inputs* in,
+                                           const gqa_tree_outputs* out, size_t* bytes);
+
+/* Host-only description of how gqa_tree_forward would run a call (same checks):
+ * regime GQA_REGIME_DECODE (warp MMAs) or GQA_REGIME_PREFILL (tensor-core
+ * pipeline); both split the keys over the GPU (split_len keys a unit,
+ * max_splits workers). launches counts the kernels. */
+GQA_API gqa_status gqa_tree_describe_plan(const gqa_handle* handle, const gqa_tree_inputs* in,
+                                          const gqa_tree_outputs* out, gqa_plan_info* info);
+
+/* Attention of drafted nodes over a float cache, on `stream`:
+ *   1. the nodes' key / value rows are stored at cache rows past_b + i, i < n_b;
+ *   2. output[b, i, h] = softmax of scale * q . k (softcap c: c tanh(s / c)) over
+ *      the cached rows j < past_b, the node's ancestors and the node itself,
+ *      times the values; query head h reads KV head h / (N / N_kv). With
+ *      local_window_size W: rows max(0, past_b + depth_i - W) .. past_b - 1, and
+ *      ancestors at most W generations up. head_sink / smooth_softmax add a
+ *      logit to the denominator as in gqa_forward.
+ * Rows of the caches outside [past_b, past_b + n_b) keep their bytes, and what
+ * rows from past_b on held before does not matter. A key or value that is not
+ * finite reaches only the rows that see it (fp32: an infinite key reads as NaN). Attributes used: num_heads,
+ * kv_num_heads, local_window_size, scale, softcap, smooth_softmax; causal must
+ * be 1 and do_rotary, the quant types and sliding_window_cache off.
+ * workspace and status as for gqa_block_forward. A sequence with lengths out of
+ * range (seqlens_k[b] + 1 outside [n_b, total_sequence_length], n_b outside
+ * [0, S]) is skipped, nothing of it is written, and GQA_DEVICE_BAD_SEQLEN set. */
+GQA_API gqa_status gqa_tree_forward(gqa_handle* handle, const gqa_tree_inputs* in, const gqa_tree_outputs* out,
+                                    void* workspace, size_t workspace_bytes, void* status, void* stream);
+
+/* Inputs of a verification: what the target and the draft model thought of the
+ * nodes, and random numbers in [0, 1).
+ *   tokens           int32 (B, S): token of every node (the root's is not used)
+ *   target_probs     float32 or float16 (B, S, V): row i, the target's
+ *                    probabilities of the token behind node i
+ *   draft_probs      as target_probs, or absent: row i, the probabilities node
+ *                    i's children were drawn from (independently of each other)
+ *   accept_uniforms  float32 (B, S): the number node i is tested with
+ *   sample_uniforms  float32 (B): the number the next token is drawn with
+ * Outputs:
+ *   path             int32 (B, S): node 0 and the accepted nodes behind it, -1 behind the last
+ *   path_lens        int32 (B): nodes of the path
+ *   next_token       int32 (B): the token drawn behind the path's last node */
+typedef struct gqa_verify_args {
+  gqa_tensor tokens, parents;
+  gqa_tensor target_probs, draft_probs;
+  gqa_tensor accept_uniforms, sample_uniforms;
+  gqa_tensor new_lens;
+  gqa_tensor path, path_lens, next_token;
+} gqa_verify_args;
+
+/* Verification, one launch on `stream`, no workspace; none of the handle's
+ * attributes apply. From the root on, the children of the path's last node are
+ * tested in their order. With p and q that node's rows, r_0 = p and Z_0 = 1,
+ * child number k + 1 of token x and uniform u is accepted when
+ *   u q(x) Z_k < r_k(x),
+ * and the path continues behind it; otherwise r_k+1 = max(r_k / Z_k - q, 0) and
+ * Z_k+1 = sum r_k+1. Without draft_probs q(x) = 1 and r_k+1 is r_k with r(x) = 0.
+ * When no child is left (to test), next_token is the lowest v with
+ *   r(0) + .. + r(v) > u_sample sum(r)
+ * (the last v of a positive r(v) if there is none), p taking the place of r if
+ * sum(r) = 0. The tokens of the path and next_token are then distributed as if
+ * drawn from the target alone. Values of single nodes are computed in 64 bits,
+ * sums over the vocabulary in at least 46. A probability that is not a positive
+ * finite number counts as 0; so does a token's outside [0, V).
+ * A sequence with n_b = 0, or outside [0, S] (GQA_DEVICE_BAD_SEQLEN), gets path
+ * -1, path_lens 0 and next_token -1; one without a positive probability to draw
+ * from next_token -1 (GQA_DEVICE_BAD_PROBS). status: see gqa_block_forward. */
+GQA_API gqa_status gqa_tree_verify(gqa_handle* handle, const gqa_verify_args* args, void* status, void* stream);
+
+/* Accepted rows moved together, in the caches of all layers:
+ *   present_keys, present_values  HOST arrays of num_layers caches T (B, N_kv, C, H)
+ *                    of one shape and type, 1 <= num_layers <= GQA_MAX_TREE_LAYERS
+ *   path, path_lens  int32 (B, S) and (B), as of gqa_tree_verify
+ *   seqlens_k, new_lens  as they were for gqa_tree_forward
+ *   into_seqlens_k   int32 (B): past_b + path_lens[b] - 1
+ * Row past_b + path[b][i] of every cache moves to row past_b + i, i <
+ * path_lens[b]; other rows keep their bytes (those behind the last accepted one
+ * are free). A sequence with lengths out of range (n_b outside [0, S],
+ * seqlens_k[b] + 1 outside [n_b, C], path_lens[b] outside [0, n_b]:
+ * GQA_DEVICE_BAD_SEQLEN) or whose path does not increase within [0, n_b)
+ * (GQA_DEVICE_BAD_TREE) keeps all rows and gets into_seqlens_k = -1. */
+typedef struct gqa_accept_args {
+  const gqa_tensor *present_keys, *present_values;
+  int32_t num_layers;
+  gqa_tensor path, path_lens;
+  gqa_tensor seqlens_k, new_lens;
+  gqa_tensor into_seqlens_k;
+} gqa_accept_args;
+
+/* One launch on `stream`, no workspace; of the handle's attributes only
+ * kv_num_heads applies. */
+GQA_API gqa_status gqa_tree_accept(gqa_handle* handle, const gqa_accept_args* args, void* status, void* stream);
+
 /* Per-launch timing for measurement tools. gqa_profile_begin creates
  * 2*max_launches CUDA events (host-side driver objects, no device memory);
  * while profiling is on, every call on this handle that launches kernels
@@ -451,6 +583,10 @@ GQA_API gqa_status gqa_block_evict(gqa_handle* handle, const gqa_evict_args* arg
 #define GQA_KERNEL_BLOCK_WEIGHTS 14
 #define GQA_KERNEL_EVICT_SELECT 15
 #define GQA_KERNEL_EVICT_GATHER 16
+#define GQA_KERNEL_TREE_ATTENTION 17
+#define GQA_KERNEL_TREE_MERGE 18
+#define GQA_KERNEL_TREE_VERIFY 19
+#define GQA_KERNEL_TREE_ACCEPT 20
 GQA_API gqa_status gqa_profile_begin(gqa_handle* handle, int32_t max_launches);
 GQA_API gqa_status gqa_profile_end(gqa_handle* handle, int32_t* kinds, float* ms, int32_t capacity, int32_t* count);
 

@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libgqa_gb300.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["gqa_api.cu", "prepass.cu", "decode.cu", "prefill_simt.cu", "prefill_tc.cu", "prefill_tcq.cu", "decode_tc.cu", "tma_host.cu",
            "rotary_axes.cu", "block_cache.cu", "block_attn.cu", "block_prefill.cu", "block_weights.cu", "block_api.cu",
-           "tree_attn.cu", "tree_verify.cu", "tree_api.cu"]
+           "tree_attn.cu", "tree_tc.cu", "tree_verify.cu", "tree_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", CSRC, "-I", INCLUDE]

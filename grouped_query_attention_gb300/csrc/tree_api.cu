@@ -118,8 +118,10 @@ gqa_status plan_tree(const gqa_handle* h, const gqa_tree_inputs* in, const gqa_t
   P.parents = static_cast<const int*>(in->parents.data);
   P.parents_ld = in->parents.shape[0] == B ? (int)S : 0;
   P.sink = in->head_sink.data;
+  P.wait_budget = h->wait_budget;
+  P.withhold_tile = h->withhold_tile;
   gqa::tree_attn_plan(&P);
-  const size_t rows = 2 * (size_t)P.workers * P.rt_rows;   // two slots a worker
+  const size_t rows = 2 * ((size_t)P.workers << P.rt_log2);   // two slots a worker
   pl->part_o = align_up(rows * H * sizeof(float));
   pl->part_ml = align_up(rows * 2 * sizeof(float));
   pl->total = pl->part_o + pl->part_ml;
@@ -145,9 +147,9 @@ gqa_status gqa_tree_describe_plan(const gqa_handle* h, const gqa_tree_inputs* in
   TreePlan pl;
   gqa_status s = plan_tree(h, in, out, &pl);
   if (s != GQA_OK) return s;
-  info->regime = GQA_REGIME_DECODE;
+  info->regime = pl.P.tc ? GQA_REGIME_PREFILL : GQA_REGIME_DECODE;
   info->launches = 2;
-  info->split_len = pl.P.unit;
+  info->split_len = 1 << pl.P.unit_log2;
   info->max_splits = pl.P.workers;
   info->workspace_bytes = pl.total;
   return GQA_OK;

@@ -1,5 +1,6 @@
 // Attention of drafted nodes over a float cache on warp MMAs: every type, head
-// size and group size; the tensor-core pipeline takes over where it is faster.
+// size, group size and scale (fp32, and what the tensor-core pipeline does not
+// take), and the merge of both.
 //
 // Rows of a KV head (b, g): query rows (node, grouped head), in row tiles of 16,
 // 32 or 64. The keys of a row tile are the cached rows and the nodes themselves,
@@ -562,15 +563,19 @@ tree_attn_kernel(const TreeParams p) {
 
 // ------------------------------------------------------------------ merge
 
-constexpr int kMergeRows = 4;   // rows of a merge block, a warp each
+constexpr int kMergeWarps = 8;
 
-// Rows of ranges that several workers share: a warp per row, lanes over the
-// coordinates. A piece's O is in units of its own maximum.
-template <typename T>
-__global__ void __launch_bounds__(32 * kMergeRows)
-tree_merge_kernel(const TreeParams p) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.x * kMergeRows + warp, b = blockIdx.y / p.Nkv, g = blockIdx.y % p.Nkv;
+// Rows of ranges that several workers share: W warps take the pieces of a row in
+// turn, lanes over the coordinates. A piece's O is in units of its own maximum.
+// A block stays within a (b, g), rows [rows blockIdx.x, + rows).
+template <typename T, int W>
+__global__ void __launch_bounds__(32 * kMergeWarps)
+tree_merge_kernel(const TreeParams p, int rows) {
+  constexpr int kTeams = kMergeWarps / W;
+  constexpr int kAhead = 4;                     // pieces of a warp under way
+  __shared__ float4 join[W > 1 ? kMergeWarps : 1][64];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp / W, sub = warp % W;
+  const int b = blockIdx.y / p.Nkv, g = blockIdx.y % p.Nkv;
   long long units = 0, base = 0;
   TreeSeq s;
   for (int x = lane; x < p.B; x += 32) {
@@ -583,48 +588,104 @@ tree_merge_kernel(const TreeParams p) {
     units += __shfl_xor_sync(0xffffffffu, units, o);
     base += __shfl_xor_sync(0xffffffffu, base, o);
   }
-  const bool on = tree_seq(p, b, &s) && r < s.fresh * p.G;
+  const int nrows = tree_seq(p, b, &s) ? s.fresh * p.G : 0;
+  const long long live = tree_live(p, units);
+  const int ld_row = 1 << p.rt_log2;
   long long w0 = 0, w1 = 0;
-  if (on) {
-    const int gr = g * s.nrt + r / p.rt_rows;
-    tree_pieces(base + (long long)gr * s.units, s.units - kTreeRangeCost, tree_live(p, units), units, &w0, &w1);
-  }
+  int rt = -1;
   dep_wait();
-  if (w0 == w1) return;   // padding, or one worker wrote the output
-  const int n = (int)(w1 - w0) + 1, row = r % p.rt_rows, hd = g * p.G + r % p.G;
-  const float lift = sizeof(T) == 2 ? kLiftHalf : 0.f;
-  auto slot = [&](int x) { return tree_slot(w0 + x, x == 0); };
-  const bool has_sink = p.sink || p.smooth;
-  const float sg = has_sink ? (p.sink ? load_t(p.sink, hd, p.t_type) : 0.f) * kLog2e : kNegBig;
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + row;
-  float m = sg, l = 0.f;
-  for (int x = lane; x < n; x += 32) m = fmaxf(m, ml[slot(x) * p.rt_rows].x);
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  for (int x = lane; x < n; x += 32) {
-    const float2 v = ml[slot(x) * p.rt_rows];
-    l = fmaf(v.y, ex2(v.x - m), l);
-  }
-  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (has_sink) l += ex2(sg - m + lift);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const float* src = p.part_o + (long long)row * p.H;
-  T* dst = static_cast<T*>(p.out) + (((long long)b * p.S + r / p.G) * p.N + hd) * p.H;
-  for (int c = 4 * lane; c < p.H; c += 128) {
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int x = 0; x < n; ++x) {
-      const float f = ex2(ml[slot(x) * p.rt_rows].x - m);
-      const float4 v = *reinterpret_cast<const float4*>(src + slot(x) * p.rt_rows * p.H + c);
-      a.x = fmaf(v.x, f, a.x);
-      a.y = fmaf(v.y, f, a.y);
-      a.z = fmaf(v.z, f, a.z);
-      a.w = fmaf(v.w, f, a.w);
+  for (int r0 = blockIdx.x * rows; r0 < min((int)(blockIdx.x + 1) * rows, nrows); r0 += kTeams) {
+    const int r = min(r0 + team, nrows - 1);    // (a team without a row does the last one's work once more)
+    if (r >> p.rt_log2 != rt) {
+      rt = r >> p.rt_log2;
+      tree_pieces(base + (long long)(g * s.nrt + rt) * s.units, s.units - kTreeRangeCost, live, units, &w0, &w1);
     }
-    if constexpr (sizeof(T) == 2)
-      *reinterpret_cast<uint2*>(dst + c) = make_uint2(pack2(a.x * inv, a.y * inv), pack2(a.z * inv, a.w * inv));
-    else
-      *reinterpret_cast<float4*>(dst + c) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    const int n = (int)(w1 - w0) + 1, hd = g * p.G + r % p.G;
+    float4 a[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};   // columns 4 lane .., + 128
+    float l = 0.f;
+    if (n > 1) {                                // (else one worker wrote the output)
+      auto at = [&](int x) { return tree_slot(w0 + x, x == 0) * ld_row + (r & (ld_row - 1)); };
+      const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+      const bool has_sink = p.sink || p.smooth;
+      const float sg = has_sink ? (p.sink ? load_t(p.sink, hd, p.t_type) : 0.f) * kLog2e : kNegBig;
+      const float2 own = lane < n ? ml[at(lane)] : make_float2(kNegBig, 0.f);   // of piece `lane`
+      float m = fmaxf(sg, own.x);
+      for (int x = lane + 32; x < n; x += 32) m = fmaxf(m, ml[at(x)].x);
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int x0 = 0; x0 < n; x0 += 32) {      // 32 pieces a turn: lane x has the factor of piece x0 + x
+        const float2 v = x0 == 0 ? own : x0 + lane < n ? ml[at(x0 + lane)] : make_float2(kNegBig, 0.f);
+        const float f = ex2(v.x - m);
+        l = fmaf(v.y, f, l);
+        for (int x = sub; x < min(32, n - x0); x += W * kAhead) {
+          float4 o[kAhead][2];
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            if (x0 + x + k * W >= n || x + k * W >= 32) continue;
+            const float4* src = reinterpret_cast<const float4*>(p.part_o + at(x0 + x + k * W) * p.H);
+            if (4 * lane < p.H) o[k][0] = src[lane];
+            if (4 * lane + 128 < p.H) o[k][1] = src[lane + 32];
+          }
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            const float fx = __shfl_sync(0xffffffffu, f, (x + k * W) & 31);
+            if (x0 + x + k * W >= n || x + k * W >= 32) continue;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (4 * lane + 128 * h >= p.H) continue;
+              a[h].x = fmaf(o[k][h].x, fx, a[h].x);
+              a[h].y = fmaf(o[k][h].y, fx, a[h].y);
+              a[h].z = fmaf(o[k][h].z, fx, a[h].z);
+              a[h].w = fmaf(o[k][h].w, fx, a[h].w);
+            }
+          }
+        }
+      }
+      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (has_sink) l += ex2(sg - m + p.lift);
+    }
+    if constexpr (W > 1) {
+      __syncthreads();
+      join[warp][lane] = a[0];
+      join[warp][lane + 32] = a[1];
+      __syncthreads();
+      if (sub > 0) continue;
+#pragma unroll
+      for (int x = 1; x < W; ++x)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 v = join[warp + x][lane + 32 * h];
+          a[h] = make_float4(a[h].x + v.x, a[h].y + v.y, a[h].z + v.z, a[h].w + v.w);
+        }
+    }
+    if (n == 1 || r0 + team >= nrows) continue;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    T* dst = static_cast<T*>(p.out) + (((long long)b * p.S + r / p.G) * p.N + hd) * p.H;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = 4 * lane + 128 * h;
+      if (c >= p.H) continue;
+      if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<uint2*>(dst + c) = make_uint2(pack2(a[h].x * inv, a[h].y * inv), pack2(a[h].z * inv, a[h].w * inv));
+      else
+        *reinterpret_cast<float4*>(dst + c) = make_float4(a[h].x * inv, a[h].y * inv, a[h].z * inv, a[h].w * inv);
+    }
   }
+}
+
+template <typename T, int W>
+cudaError_t merge_w(const TreeParams& p, cudaStream_t st) {
+  constexpr int kTeams = kMergeWarps / W;
+  // Rows of a block: so many that the blocks fit the GPU about once beside the attention.
+  const long long all = (long long)p.B * p.Nkv * p.S * p.G;
+  const int rows = (int)((all + 912LL * kTeams - 1) / (912LL * kTeams)) * kTeams;
+  const dim3 grid((unsigned)((p.S * p.G + rows - 1) / rows), (unsigned)(p.B * p.Nkv));
+  return launch_dependent(true, tree_merge_kernel<T, W>, grid, 32 * kMergeWarps, 0, st, p, rows);
+}
+
+template <typename T>
+cudaError_t merge_t(const TreeParams& p, cudaStream_t st) {
+  const long long pieces = p.workers / ((long long)p.B * p.Nkv * p.nrt) + 2;   // of a range, about
+  return pieces <= 4 ? merge_w<T, 1>(p, st) : pieces <= 16 ? merge_w<T, 2>(p, st) : merge_w<T, 8>(p, st);
 }
 
 constexpr int kMaxDevices = 64;
@@ -647,7 +708,7 @@ cudaError_t launch_rw(const TreeParams& p, cudaStream_t st) {
 
 template <typename T, int HP>
 cudaError_t launch_hp(const TreeParams& p, cudaStream_t st) {
-  return p.rt_rows == 16 ? launch_rw<T, HP, 1>(p, st) : p.rt_rows == 32 ? launch_rw<T, HP, 2>(p, st) : launch_rw<T, HP, 4>(p, st);
+  return p.rt_log2 == 4 ? launch_rw<T, HP, 1>(p, st) : p.rt_log2 == 5 ? launch_rw<T, HP, 2>(p, st) : launch_rw<T, HP, 4>(p, st);
 }
 
 template <typename T>
@@ -657,27 +718,40 @@ cudaError_t launch_t(const TreeParams& p, cudaStream_t st) {
 
 }  // namespace
 
+// The tensor-core pipeline where it can: it holds 128 rows as cheaply as 16, and its copies run across the ends of
+// ranges (16 sequences of 1k to 8k rows, 16 query rows: 74 us, the warp MMAs 80; 32 rows 76, 89; 5 nodes on 1030 rows
+// 15, 17). It takes row maxima before the scale, which a negative one would turn.
+bool use_tc(const TreeParams& p) { return p.t_type == kF16 && p.H <= 128 && p.scale > 0.f; }
+
 void tree_attn_plan(TreeParams* p) {
   const int rows = p->S * p->G;
-  p->rt_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  p->unit = p->t_type == kF16 ? 64 : 32;
-  p->nrt = (rows + p->rt_rows - 1) / p->rt_rows;
-  // CTAs an SM holds: two stages of 16 KB (H <= 64), 32 KB, 64 KB.
-  const long long most = 152LL * (p->H <= 64 ? 4 : p->H <= 128 ? 2 : 1);
+  p->tc = use_tc(*p);
+  p->lift = p->tc ? 6.f : p->t_type == kF16 ? kLiftHalf : 0.f;
+  // CTAs an SM holds: one of the pipeline; of the warp MMAs by two stages of 16 KB (H <= 64), 32 KB, 64 KB.
+  long long most = 152;
+  if (p->tc) {
+    p->rt_log2 = rows <= 128 ? 7 : 8;
+    p->unit_log2 = 7;
+  } else {
+    p->rt_log2 = rows <= 16 ? 4 : rows <= 32 ? 5 : 6;
+    p->unit_log2 = p->t_type == kF16 ? 6 : 5;
+    most *= p->H <= 64 ? 4 : p->H <= 128 ? 2 : 1;
+  }
+  p->nrt = (rows + (1 << p->rt_log2) - 1) >> p->rt_log2;
+  const int u = (1 << p->unit_log2) - 1;
   const int keys = p->window >= 0 && p->window < p->T - p->S ? p->window + 16 : p->T;
   const long long ranges = (long long)p->B * p->Nkv * p->nrt;
-  const long long units = ranges * ((keys + p->unit - 1) / p->unit + (p->S + p->unit - 1) / p->unit + kTreeRangeCost);
+  const long long units = ranges * (((keys + u) >> p->unit_log2) + ((p->S + u) >> p->unit_log2) + kTreeRangeCost);
   p->workers = (int)(units < most ? units : most);
 }
 
 cudaError_t launch_tree_attn(const TreeParams& p, cudaStream_t st) {
+  if (p.tc) return launch_tree_tc(p, st);
   return p.t_type == kF16 ? launch_t<__half>(p, st) : launch_t<float>(p, st);
 }
 
 cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t st) {
-  const dim3 grid((unsigned)((p.S * p.G + kMergeRows - 1) / kMergeRows), (unsigned)(p.B * p.Nkv));
-  return p.t_type == kF16 ? launch_dependent(true, tree_merge_kernel<__half>, grid, 32 * kMergeRows, 0, st, p)
-                          : launch_dependent(true, tree_merge_kernel<float>, grid, 32 * kMergeRows, 0, st, p);
+  return p.t_type == kF16 ? merge_t<__half>(p, st) : merge_t<float>(p, st);
 }
 
 }  // namespace gqa

@@ -28,8 +28,12 @@ struct TreeParams {
   int parents_ld;        // S, or 0: one tree for all sequences
   const void* sink;
   uint32_t* status;
+  int tc;                // on the tensor-core pipeline
+  long long wait_budget;
+  int withhold_tile;
+  float lift;            // log2 of what the workspace's probabilities (l and O) are multiplied by
   // split over the keys
-  int rt_rows, unit;     // query rows of a row tile, keys of a unit
+  int rt_log2, unit_log2;   // query rows of a row tile, keys of a unit: powers of two
   int nrt;               // row tiles of S nodes
   int workers;           // shares of the units
   float *part_o, *part_ml;
@@ -66,9 +70,10 @@ struct TreeSeq {
 __device__ __forceinline__ bool tree_seq(const TreeParams& p, int b, TreeSeq* s) {
   if (!tree_lengths(p, b, &s->past, &s->fresh)) s->fresh = 0;
   s->k0 = p.window >= 0 ? max(0, s->past - p.window) & ~15 : 0;   // the root sees furthest back
-  s->np = (s->past - s->k0 + p.unit - 1) / p.unit;
-  s->units = s->np + (s->fresh + p.unit - 1) / p.unit + kTreeRangeCost;
-  s->nrt = (s->fresh * p.G + p.rt_rows - 1) / p.rt_rows;
+  const int u = (1 << p.unit_log2) - 1;
+  s->np = (s->past - s->k0 + u) >> p.unit_log2;
+  s->units = s->np + ((s->fresh + u) >> p.unit_log2) + kTreeRangeCost;
+  s->nrt = (s->fresh * p.G + (1 << p.rt_log2) - 1) >> p.rt_log2;
   return s->fresh > 0;
 }
 
@@ -168,6 +173,8 @@ __device__ __forceinline__ void tree_pieces(long long base, int work, long long 
 }
 
 cudaError_t launch_tree_attn(const TreeParams& p, cudaStream_t st);
+// ... on the tensor cores: fp16, head sizes up to 128.
+cudaError_t launch_tree_tc(const TreeParams& p, cudaStream_t st);
 cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t st);
 // Rows of a row tile, keys of a unit and shares of the split for a call.
 void tree_attn_plan(TreeParams* p);

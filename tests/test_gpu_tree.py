@@ -76,6 +76,12 @@ CASES = {
     "empty_slots": ("f16", 4, 2, 4, 2, 64, 64, (0, 10, 0, 64), (0, 0, 0, 2), -1, 0, 0, 0, "chain", 1),
     "no_cached_rows": ("f16", 2, 64, 8, 2, 128, 64, (64, 30), (64, 30), -1, 0, 0, 0, "tree", 0),
     "group_of_40": ("f16", 1, 7, 40, 1, 128, 300, (300,), None, -1, 0, 0, 0, "tree", 0),
+    "many_units": ("f16", 4, 16, 16, 4, 128, 6000, (6000, 5500, 4100, 5999), None, -1, 0, 0, 0, "tree", 0),
+    "many_units_two_tiles": ("f16", 4, 40, 16, 4, 128, 6000, (6000, 5500, 4100, 5999), (40, 13, 40, 33), -1, 0, 0, 0, "tree", 0),
+    "many_units_h64": ("f16", 3, 12, 20, 4, 64, 12000, (12000, 9000, 11111), None, -1, 8.0, 1, 0, "tree", 0),
+    "many_units_window": ("f16", 4, 50, 16, 4, 96, 6000, (6000, 5500, 4100, 5999), None, 2500, 20.0, 0, 0, "chain", 0),
+    "many_pieces": ("f16", 150, 10, 16, 4, 128, 40, tuple(10 + 31 * i % 31 for i in range(150)), None, -1, 0, 0, 0, "tree", 0),
+    "many_pieces_two_tiles": ("f16", 150, 10, 64, 4, 64, 140, tuple(10 + 37 * i % 131 for i in range(150)), None, -1, 0, 0, 0, "tree", 0),
     "many_sequences": ("f16", 150, 3, 4, 2, 64, 40, tuple(3 + 37 * i % 38 for i in range(150)), None, -1, 0, 0, 0, "tree", 0),
 }
 
@@ -109,9 +115,9 @@ def run_oracle(d):
     return out, mag, reach, pk, pv
 
 
-def operator(d):
+def operator(d, **attrs):
     return GroupQueryAttention(d["N"], d["Nkv"], softcap=float(d["softcap"]), local_window_size=d["window"],
-                               smooth_softmax=1 if d["smooth"] else -1)
+                               smooth_softmax=1 if d["smooth"] else -1, **attrs)
 
 
 def run_gpu(d, op=None, total=None, output=None):
@@ -160,6 +166,18 @@ def test_forward_with_a_loose_bound_is_the_same_on_every_run(name):
     check(d, first, want)
     again = run_gpu(d, op, total=d["C"])
     assert np.array_equal(first[0], again[0])
+
+
+@pytest.mark.parametrize("name", ["tile_16", "tile_32", "tile_64", "tiles_3", "h96_ragged", "window", "forest", "softcap_sink",
+                                  "many_units_h64", "tile_32_f32"])
+@pytest.mark.parametrize("scale", [-0.1, 0.3])
+def test_forward_of_other_scales(name, scale):
+    """A negative scale takes fp16 calls to the warp MMAs."""
+    d = make(CASES[name])
+    pk, pv = d["pk"].copy(), d["pv"].copy()
+    out, mag, reach = ot.forward(d["q"], d["k"], d["v"], d["parents"], d["totals"] - 1, d["news"], pk, pv, d["N"], d["Nkv"],
+                                 scale=scale, softcap=d["softcap"], window=d["window"], sink=d["sink"], smooth=bool(d["smooth"]))
+    check(d, run_gpu(d, operator(d, scale=scale)), (out, mag, reach, pk, pv))
 
 
 def test_bad_lengths_leave_everything():
@@ -231,6 +249,19 @@ def test_a_second_stream_and_a_graph():
     torch.cuda.synchronize()
     for _, o, k2, v2, _ in graphs:
         check(d, (o.cpu().numpy(), k2.cpu().numpy(), v2.cpu().numpy()), want)
+
+
+@pytest.mark.parametrize("name,tile", [("tile_64", 0), ("long_rows", 0), ("many_units", 3), ("many_units_two_tiles", 2)])
+def test_expired_waits_are_reported_and_leave_the_next_call_alone(name, tile):
+    """The copy of a key tile is withheld: the waits for it run out, the call says so, the next one is right."""
+    d = make(CASES[name])
+    op = operator(d)
+    capi.gqa_set_wait_limit(op.handle, 2_000_000, tile)
+    run_gpu(d, op)
+    assert op.block_status() == capi.GQA_DEVICE_TIMEOUT
+    capi.gqa_set_wait_limit(op.handle, 0)
+    check(d, run_gpu(d, op))
+    assert op.block_status() == 0
 
 
 def test_python_refusals():

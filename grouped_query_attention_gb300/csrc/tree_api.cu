@@ -2,6 +2,7 @@
 // workspace plan, launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -251,18 +252,32 @@ gqa_status gqa_tree_accept(gqa_handle* h, const gqa_accept_args* a, void* status
   if ((s = check_ints(a->into_seqlens_k, "into_seqlens_k", false, 1, b1)) != GQA_OK) return s;
   if ((s = check_status_word(status)) != GQA_OK) return s;
   const int caches = 2 * a->num_layers;
-  Named read[] = {{&a->path, "path"}, {&a->path_lens, "path_lens"}, {&a->seqlens_k, "seqlens_k"}, {&a->new_lens, "new_lens"}};
-  Named written[2 * gqa::kTreeLayers + 1] = {{&a->into_seqlens_k, "into_seqlens_k"}};
   gqa::AcceptParams P;
   memset(&P, 0, sizeof(P));
   for (int i = 0; i < caches; ++i) {
     const gqa_tensor& t = i & 1 ? a->present_values[i / 2] : a->present_keys[i / 2];
     if (!present(t) || t.dtype != c.dtype || !shape_is(t, 4, c.shape))
       return fail(GQA_ERR_INVALID_ARGUMENT, "caches must have one shape and dtype (layer %d)", i / 2);
-    written[1 + i] = {&t, "a cache"};
+    if ((s = gqa::check_aligned(t, "a cache")) != GQA_OK) return s;
     P.cache[i] = t.data;
   }
-  if ((s = check_buffers(read, 4, written, caches + 1, nullptr, 0)) != GQA_OK) return s;
+  // Caches of one size overlap when two of their addresses, in order, are nearer than it; the small tensors one by one.
+  const size_t size = gqa::bytes_of(c);
+  void* order[2 * gqa::kTreeLayers];
+  std::copy(P.cache, P.cache + caches, order);
+  std::sort(order, order + caches);
+  for (int i = 1; i < caches; ++i)
+    if (static_cast<char*>(order[i]) - static_cast<char*>(order[i - 1]) < (ptrdiff_t)size)
+      return fail(GQA_ERR_INVALID_ARGUMENT, "a cache overlaps another");
+  const Named small[] = {{&a->path, "path"}, {&a->path_lens, "path_lens"}, {&a->seqlens_k, "seqlens_k"}, {&a->new_lens, "new_lens"}};
+  const Named into[] = {{&a->into_seqlens_k, "into_seqlens_k"}};
+  if ((s = check_buffers(small, 4, into, 1, nullptr, 0)) != GQA_OK) return s;
+  for (const Named& n : {small[0], small[1], small[2], small[3], into[0]})
+    if (present(*n.t))
+      for (int i = 0; i < caches; ++i)
+        if (static_cast<char*>(n.t->data) < static_cast<char*>(P.cache[i]) + size &&
+            static_cast<char*>(P.cache[i]) < static_cast<char*>(n.t->data) + gqa::bytes_of(*n.t))
+          return fail(GQA_ERR_INVALID_ARGUMENT, "a cache overlaps %s", n.name);
   P.B = (int)B; P.S = (int)a->path.shape[1]; P.Nkv = (int)Nkv; P.C = (int)C; P.layers = a->num_layers;
   P.row_bytes = (int)H * (c.dtype == GQA_F16 ? 2 : 4);
   P.path = static_cast<const int*>(a->path.data);

@@ -2,23 +2,23 @@
 //
 // Verification. A node's tests need single probabilities only, and the tokens
 // that were turned down leave the target's row as max(a p - b q, 0) with two
-// scalars, a = 1 / (Z_1 .. Z_k), b = sum of the products that scale each q: no
-// row is ever stored. What has to be read is the row of the node where the path
-// ends (and one row more for every test that failed on the way): the sum of it,
-// and the place where the running sum passes u sum. A cluster of CTAs takes a
-// sequence, each warp an equal run of the vocabulary; the warps' sums travel
-// through distributed shared memory, every CTA adds them in the same order and
-// takes the same decisions, and the warp that holds the place looks it up.
-// Without draft probabilities r is p without the tokens turned down.
+// scalars: no row is ever stored. What has to be read is the row of the node
+// where the path ends, and once more for every test that failed on the way (from
+// L1 then): the sum of what is left, and the place where the running sum passes
+// u sum. A cluster of CTAs takes a sequence, each warp an equal run of the
+// vocabulary; the warps write their sums to every CTA of the cluster, all of
+// them add the sums in one order and take the same decisions, and the warp whose
+// run holds the place looks it up, in three levels. Without draft probabilities
+// r is p without the tokens turned down, whose sum needs no new pass.
 //
 // The token has to be exact, so the sums may not move the place: values and sums
 // are pairs of floats (48 bits; the difference of two floats is exact), as 64-bit
-// arithmetic runs at 1/64 of the rate here; single values use 64 bits.
+// arithmetic runs at 1/64 of the rate here.
 //
-// Bound: latency (a few dependent loads, one pass over a row, two cluster
-// barriers).
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "tree_internal.h"
@@ -30,6 +30,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kVThreads = 512, kVWarps = kVThreads / 32;
 constexpr int kVMaxCluster = 8;
+constexpr int kVMaxWarps = kVWarps * kVMaxCluster;
 
 // A sum of floats as a pair: hi + lo, |lo| at most half a step of hi.
 struct Pair {
@@ -43,20 +44,24 @@ __device__ __forceinline__ Pair quick(float a, float b) {   // |a| >= |b|
   const float s = __fadd_rn(a, b);
   return {s, __fsub_rn(b, __fsub_rn(s, a))};
 }
+// (what the low parts' sum loses is 2^-48 of the whole)
 __device__ __forceinline__ Pair add(Pair a, Pair b) {
-  Pair s = two_sum(a.hi, b.hi);
-  const Pair e = two_sum(a.lo, b.lo);
-  s = quick(s.hi, __fadd_rn(s.lo, e.hi));
-  return quick(s.hi, __fadd_rn(s.lo, e.lo));
+  const Pair s = two_sum(a.hi, b.hi);
+  return quick(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
 }
-__device__ __forceinline__ Pair mul(Pair a, float b) {
-  const float h = __fmul_rn(a.hi, b);
-  return quick(h, __fmaf_rn(a.lo, b, __fmaf_rn(a.hi, b, -h)));
+__device__ __forceinline__ Pair neg(Pair a) { return {-a.hi, -a.lo}; }
+__device__ __forceinline__ Pair product(float a, float b) {   // exact
+  const float h = __fmul_rn(a, b);
+  return {h, __fmaf_rn(a, b, -h)};
 }
-__device__ __forceinline__ double value(Pair a) { return (double)a.hi + (double)a.lo; }
-__device__ __forceinline__ Pair pair_of(double x) {
-  const float h = (float)x;
-  return {h, (float)(x - (double)h)};
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+  const Pair h = product(a.hi, b.hi);
+  return quick(h.hi, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, h.lo)));
+}
+__device__ __forceinline__ Pair reciprocal(Pair a) {
+  const float x = __frcp_rn(a.hi);
+  const float rest = __fmaf_rn(-x, a.lo, __fmaf_rn(-x, a.hi, 1.f));   // 1 - x a
+  return quick(x, __fmul_rn(rest, x));
 }
 __device__ __forceinline__ Pair shfl_xor(Pair a, int o) {
   return {__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)};
@@ -68,18 +73,18 @@ __device__ __forceinline__ Pair shfl_up(Pair a, int o) {
 __device__ __forceinline__ bool above(Pair a, Pair b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
 
 // Probabilities as the definition reads them.
-__device__ __forceinline__ float proper(float p) { return p > 0.f && p < INFINITY ? p : 0.f; }
+// (the bits of negative, infinite and NaN values lie above the finite ones')
+__device__ __forceinline__ float proper(float p) { return __float_as_uint(p) < 0x7f800000u ? p : 0.f; }
 template <bool HALF>
 __device__ __forceinline__ float prob(const void* base, long long i) {
   if constexpr (HALF) return proper(__half2float(static_cast<const __half*>(base)[i]));
   return proper(static_cast<const float*>(base)[i]);
 }
 
-// What is left of a row: max(a p - b q, 0), or p without `n` tokens.
+// What is left of a row behind `round` tokens turned down: max(a p - b q, 0), or p without the tokens of Ctl::gone.
 struct Left {
-  int node, round;   // round 0: p itself
-  double a, b;
-  int turned;        // tokens of Ctl::gone (no draft probabilities)
+  int node, round, turned;
+  Pair a, b;
 };
 
 template <bool HALF>
@@ -88,23 +93,47 @@ struct Row {
   long long at;        // of the row's first element
   long long V;
   int off;             // of it in its group of four
-  // Elements 4 k - off .. of the row; those outside it read 0.
-  __device__ __forceinline__ static float4 four(const void* base, long long at, long long V, int off, long long k) {
-    const long long v = 4 * k - off;
-    if (v >= 0 && v + 4 <= V) {
-      if constexpr (HALF) {
-        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __half*>(base) + at + v);
-        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
-        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
-        return make_float4(proper(x.x), proper(x.y), proper(y.x), proper(y.y));
-      } else {
-        const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at + v);
-        return make_float4(proper(w.x), proper(w.y), proper(w.z), proper(w.w));
-      }
+  // Groups 4 k - off .. of four elements; only those [first(), end()) lie within the row.
+  __device__ __forceinline__ int first() const { return off > 0 ? 1 : 0; }
+  __device__ __forceinline__ int end() const { return (int)((V + off) >> 2); }
+  using Raw = typename std::conditional<HALF, uint2, float4>::type;
+  __device__ __forceinline__ Raw raw(const void* base, int k) const {
+    const long long v = at - off + 4LL * k;
+    if constexpr (HALF) return *reinterpret_cast<const uint2*>(static_cast<const __half*>(base) + v);
+    else return *reinterpret_cast<const float4*>(static_cast<const float*>(base) + v);
+  }
+  __device__ __forceinline__ static float4 values(Raw w) {
+    if constexpr (HALF) {
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+      return make_float4(proper(x.x), proper(x.y), proper(y.x), proper(y.y));
+    } else {
+      return make_float4(proper(w.x), proper(w.y), proper(w.z), proper(w.w));
     }
+  }
+  // The loads of group k (of its neighbour within the row, where it reaches over an end), and its values; elements
+  // outside the row are 0.
+  struct Loaded {
+    Raw p, q;
+  };
+  __device__ __forceinline__ Loaded load(int k) const {
+    Loaded x = {};
+    if (end() > first()) {
+      const int kk = min(max(k, first()), end() - 1);
+      x.p = raw(p, kk);
+      if (q) x.q = raw(q, kk);
+    }
+    return x;
+  }
+  __device__ __forceinline__ float4 four(const void* base, Raw w, int k) const {
+    if (k >= first() && k < end()) return values(w);
     float x[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = v + e >= 0 && v + e < V ? prob<HALF>(base, at + v + e) : 0.f;
+    for (int e = 0; e < 4; ++e) {
+      const long long v = 4LL * k - off + e;
+      x[e] = prob<HALF>(base, at + min(max(v, 0LL), V - 1));
+      if (v < 0 || v >= V) x[e] = 0.f;
+    }
     return make_float4(x[0], x[1], x[2], x[3]);
   }
 };
@@ -115,49 +144,133 @@ struct Ctl {
   float p[kTreeNodes], q[kTreeNodes], u[kTreeNodes];   // of the node's token in its parent's rows; its uniform
   int path[kTreeNodes];
   int gone[kTreeNodes];              // tokens turned down at the current node
-  Pair warp_sum[kVWarps];            // of this CTA (read by the cluster)
-  Pair all_sum[kVWarps * kVMaxCluster];
+  Pair sums[2][kVMaxWarps];          // of every warp of the cluster, two passes in turn
   Left left;
-  double z;
-  int command, path_len, last;
+  int command, path_len;
+  // the draw: the warp that holds the place (-1: no token), the sum before its run, what the running sum has to pass
+  int at;
+  Pair before, edge;
+  Pair part[kVWarps];                // of the run's sixteenths
 };
-enum { kSum = 1, kDraw = 2 };
+// What warp 0 asks for: the sum of the node's row as it is (no draft
+// probabilities), the sum of what is left, or the draw from it; + 4: the sums
+// of what is left are at hand.
+enum { kWhole = 0, kSum = 1, kDraw = 2, kSummed = 4 };
 
-// Four elements of what is left, from v = 4 k - off on.
+// s += d (a value and what rounding left of it), as the sum and its error.
+__device__ __forceinline__ void gather(Pair& s, Pair d) {
+  const Pair t = two_sum(s.hi, d.hi);
+  s.hi = t.hi;
+  s.lo = __fadd_rn(s.lo, __fadd_rn(t.lo, d.lo));
+}
+
+// What is left of one element, a p - b q (exact for a = b = 1), as a value and what rounding left of it.
+__device__ __forceinline__ Pair left_of(float p, float q, Pair a, Pair b) {
+  const float x = __fmul_rn(a.hi, p), y = __fmul_rn(b.hi, q);
+  const float xl = __fmaf_rn(a.lo, p, __fmaf_rn(a.hi, p, -x));
+  const float yl = __fmaf_rn(b.lo, q, __fmaf_rn(b.hi, q, -y));
+  Pair d = two_sum(x, -y);
+  d.lo = __fadd_rn(d.lo, __fsub_rn(xl, yl));
+  return __fadd_rn(d.hi, d.lo) > 0.f ? d : Pair{0.f, 0.f};
+}
+
+// ... of group k.
+// (Not inlined, like the searches below: a call runs each place once, from cold instruction memory.)
 template <bool HALF>
-__device__ __forceinline__ void left_of(const Row<HALF>& row, const Left& f, Pair a, Pair b, const int* gone, long long k,
-                                        Pair* r) {
-  const float4 p4 = Row<HALF>::four(row.p, row.at, row.V, row.off, k);
+__device__ __noinline__ void left_of4(const Row<HALF>& row, typename Row<HALF>::Loaded in, const Left& f, const int* gone,
+                                         int turned, int k, Pair* r) {
+  const float4 p4 = row.four(row.p, in.p, k);
   const float pv[4] = {p4.x, p4.y, p4.z, p4.w};
   if (f.round == 0 || !row.q) {
-    const int v = (int)(4 * k - row.off);
 #pragma unroll
     for (int e = 0; e < 4; ++e) r[e] = {pv[e], 0.f};
-    for (int x = 0; x < f.turned; ++x) {
-      const int d = gone[x] - v;
+    for (int x = 0; x < turned; ++x) {
+      const int d = gone[x] - (4 * k - row.off);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (d == e) r[e].hi = 0.f;
     }
     return;
   }
-  const float4 q4 = Row<HALF>::four(row.q, row.at, row.V, row.off, k);
+  const float4 q4 = row.four(row.q, in.q, k);
   const float qv[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    Pair d;
-    if (f.round == 1) {   // a = b = 1: exact
-      d = two_sum(pv[e], -qv[e]);
-    } else {
-      const Pair x = mul(a, pv[e]), y = mul(b, qv[e]);
-      d = add(x, {-y.hi, -y.lo});
-    }
-    r[e] = d.hi > 0.f ? d : Pair{0.f, 0.f};
+    r[e] = left_of(pv[e], qv[e], f.a, f.b);
+    r[e] = quick(r[e].hi, r[e].lo);
   }
 }
 
+// Sum of what is left of groups g0 + lane, + 32, .. within [first, k1), in four
+// chains, without the turns in `skip`. A turn's loads are all under way before the
+// first is looked at (with a condition around each they came one by one).
+template <bool HALF, bool DRAFT>
+__device__ __forceinline__ void sum_run(const Row<HALF>& row, const Left& f, int g0, int first, int k1, unsigned long long skip, Pair* s) {
+  constexpr int kGroups = 2;   // (3 or 4: the same or slower, as more instructions come from cold memory)
+  if (first >= k1) return;
+  for (int k = g0 + (threadIdx.x & 31); k < k1; k += 32 * kGroups) {
+    typename Row<HALF>::Raw pr[kGroups], qr[kGroups];
+#pragma unroll
+    for (int x = 0; x < kGroups; ++x) {
+      const int kx = min(max(k + 32 * x, first), k1 - 1);
+      pr[x] = row.raw(row.p, kx);
+      if constexpr (DRAFT) qr[x] = row.raw(row.q, kx);
+    }
+#pragma unroll
+    for (int x = 0; x < kGroups; ++x) {
+      const float4 pv = Row<HALF>::values(pr[x]);
+      float4 qv = pv;
+      if constexpr (DRAFT) qv = Row<HALF>::values(qr[x]);
+      const int kx = k + 32 * x;
+      bool on = kx >= first && kx < k1;
+      if constexpr (!DRAFT) on = on && !(skip >> ((kx - g0) >> 5 & 63) & 1u);
+      const float pe[4] = {pv.x, pv.y, pv.z, pv.w}, qe[4] = {qv.x, qv.y, qv.z, qv.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float p1 = on ? pe[e] : 0.f;
+        if constexpr (DRAFT) gather(s[e], left_of(p1, qe[e], f.a, f.b));
+        else gather(s[e], {p1, 0.f});
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ Pair warp_sum(Pair s) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s = add(s, shfl_xor(s, o));
+  return s;
+}
+// Sum over the lanes up to this one.
+__device__ __forceinline__ Pair warp_scan(Pair s) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Pair v = shfl_up(s, o);
+    if (lane >= o) s = add(v, s);
+  }
+  return s;
+}
+
+// One level of the search for the place where the running sum passes `goal`:
+// the first lane whose part does (*before becomes the sum before it), or, if
+// none does, the last lane with something (*spare) and -1. All of a warp.
+__device__ __noinline__ int find_lane(Pair own, Pair goal, Pair* before, int* spare) {
+  const Pair upto = add(*before, warp_scan(own));
+  const unsigned some = __ballot_sync(0xffffffffu, own.hi > 0.f);
+  const unsigned hit = __ballot_sync(0xffffffffu, own.hi > 0.f && above(upto, goal));
+  *spare = some ? 31 - __clz(some) : -1;
+  const int at = hit ? __ffs(hit) - 1 : -1;
+  const int take = hit ? at : 31;   // without a hit: all of it
+  Pair prev = shfl_up(upto, 1);
+  if ((threadIdx.x & 31) == 0) prev = *before;
+  const Pair x = hit ? prev : upto;
+  before->hi = __shfl_sync(0xffffffffu, x.hi, take);
+  before->lo = __shfl_sync(0xffffffffu, x.lo, take);
+  return at;
+}
+
 template <bool HALF>
-__global__ void __launch_bounds__(kVThreads)
+__global__ void __launch_bounds__(kVThreads, 2)
 tree_verify_kernel(const VerifyParams p) {
   cg::cluster_group cluster = cg::this_cluster();
   __shared__ Ctl c;
@@ -177,222 +290,276 @@ tree_verify_kernel(const VerifyParams p) {
     }
     return;
   }
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   // ---- every node's single values
   bool bad = false;
   for (int i = tid; i < n; i += kVThreads) {
     const int par = tree_parent(p.parents[(long long)b * p.parents_ld + i], i, &bad);
     const int tok = p.tokens[(long long)b * p.S + i];
+    const float u = p.accept_u[(long long)b * p.S + i];
     const bool on = par >= 0 && tok >= 0 && tok < p.V;
     const long long at = on ? ((long long)b * p.S + par) * p.V + tok : 0;
     c.parent[i] = i == 0 ? -1 : par;
     c.token[i] = tok;
     c.p[i] = on ? prob<HALF>(p.target, at) : 0.f;
     c.q[i] = !p.draft ? 1.f : on ? prob<HALF>(p.draft, at) : 0.f;
-    c.u[i] = p.accept_u[(long long)b * p.S + i];
+    c.u[i] = u;
   }
   if (__syncthreads_or(bad) && tid == 0 && rank == 0 && p.status) atomicOr(p.status, GQA_DEVICE_BAD_TREE_BIT);
-  if (tid == 0) {
-    c.left = {0, 0, 1.0, 0.0, 0};
-    c.z = 1.0;
-    c.path[0] = 0;
-    c.path_len = 1;
-    c.last = 0;
-  }
-  bool summed = false;   // warp sums of what is left are at hand
-  __syncthreads();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // every CTA has begun: its memory may be written
+
+  const int warps = ranks * kVWarps;
+  // Warp 0's state: what is left at the path's last node, its sum z, the node tested last.
+  int node = 0, round = 0, turned_down = 0;
+  const Pair one = {1.f, 0.f};
+  Pair fa = one, fb = {0.f, 0.f};           // what is left: fa p - fb q
+  Pair z = one, whole = {-1.f, 0.f};        // whole: sum of the node's row (no draft probabilities), once known
+  int last = 0, len = 1, pass = 0, spare;
+  bool summed = false;
+  if (tid == 0) c.path[0] = 0;
   while (true) {
-    // ---- tests, until one fails or no child is left (warp 0)
+    // ---- tests, until a sum is needed or no child is left
     if (warp == 0) {
-      Left f = c.left;
-      double z = c.z;
-      int last = c.last, len = c.path_len, command = kDraw;
+      int command = kDraw;
       while (true) {
-        int next = n;   // the next child of f.node behind node `last`
+        int next = n;   // the next child of `node` behind node `last`
         for (int i = last + 1; i < n; i += 32) {
-          const unsigned m = __ballot_sync(0xffffffffu, i + lane < n && c.parent[i + lane] == f.node);
+          const unsigned m = __ballot_sync(0xffffffffu, i + lane < n && c.parent[i + lane] == node);
           if (m) {
             next = i + __ffs(m) - 1;
             break;
           }
         }
         if (next >= n) break;
-        last = next;
-        const double pv = c.p[next], qv = c.q[next], uv = c.u[next];
-        double r = pv;
-        if (f.round > 0) {
+        const float pv = c.p[next], qv = c.q[next];
+        Pair r = {pv, 0.f};
+        bool dup = false;
+        if (round > 0) {
           if (p.draft) {
-            r = f.a * pv - f.b * qv;
+            r = round == 1 ? two_sum(pv, -qv) : add(mul(fa, {pv, 0.f}), neg(mul(fb, {qv, 0.f})));
           } else {
-            bool dup = false;
-            for (int x = lane; x < f.turned; x += 32) dup |= c.gone[x] == c.token[next];
-            if (__any_sync(0xffffffffu, dup)) r = 0.0;
+            for (int x = lane; x < turned_down; x += 32) dup |= c.gone[x] == c.token[next];
+            dup = __any_sync(0xffffffffu, dup);
+            if (dup) r = {0.f, 0.f};
           }
         }
-        if (z > 0.0 && uv * qv * z < r) {
-          f = {next, 0, 1.0, 0.0, 0};
-          z = 1.0;
+        if (z.hi > 0.f && above(r, mul(product(c.u[next], qv), z))) {
+          node = next;
+          round = turned_down = 0;
+          fa = z = one;
+          fb = {0.f, 0.f};
+          whole.hi = -1.f;
           if (lane == 0) c.path[len] = next;
           ++len;
+          last = next;
           summed = false;
           continue;
         }
-        // turned down: r <- max(r / z - q, 0), whose sum is due
-        if (p.draft) {
-          if (z > 0.0) {   // (nothing left: it stays so)
-            f.a = f.a / z;
-            f.b = f.b / z + 1.0;
-          }
-        } else {
-          if (lane == 0) c.gone[f.turned] = c.token[next];
-          ++f.turned;
+        if (!p.draft && whole.hi < 0.f) {   // (the test stands: come back with the sum)
+          command = kWhole;
+          break;
         }
-        ++f.round;
-        command = kSum;
-        break;
+        // turned down: r <- max(r / z - q, 0), or r without the token
+        last = next;
+        ++round;
+        summed = false;
+        if (p.draft) {
+          if (round == 1) {
+            fb = one;
+          } else if (z.hi > 0.f) {   // (nothing left: it stays so)
+            const Pair over = reciprocal(z);
+            fa = mul(fa, over);
+            fb = add(mul(fb, over), one);
+          }
+          command = kSum;
+          break;
+        }
+        if (lane == 0) c.gone[turned_down] = c.token[next];
+        __syncwarp();
+        ++turned_down;
+        z = turned_down == 1 ? add(whole, {-pv, 0.f}) : dup ? z : add(z, {-pv, 0.f});
+        if (!(z.hi > whole.hi * 0x1p-16f)) {   // too little of the sum for a difference to hold: add it up
+          command = kSum;
+          break;
+        }
+      }
+      if (command == kDraw && summed && !(z.hi > 0.f)) {   // nothing left: the target's own row
+        round = turned_down = 0;
+        summed = false;
       }
       if (lane == 0) {
-        c.left = f;
-        c.z = z;
-        c.last = last;
+        c.left = {node, round, turned_down, fa, fb};
         c.path_len = len;
-        // (2: what warp 0 knows about the sums, for everybody)
-        c.command = command | (summed ? 4 : 0);
+        c.command = command | (summed ? kSummed : 0);
       }
     }
     __syncthreads();
     const int command = c.command & 3;
-    summed = (c.command & 4) != 0;
-    Left f = c.left;
-    if (command == kDraw && summed && !(c.z > 0.0)) {   // nothing left: the target's own row
-      f.round = 0;
-      f.turned = 0;
-      summed = false;
-    }
+    const Left f = c.left;
+    const int turned = command == kWhole ? 0 : f.turned;
     const long long row_at = ((long long)b * p.S + f.node) * p.V;
     const Row<HALF> row = {p.target, p.draft, row_at, p.V, (int)(row_at & 3)};
-    const long long groups = (p.V + row.off + 3) >> 2;          // of four elements
-    const int warps = ranks * kVWarps;
-    const long long run = ((groups + warps - 1) / warps + 31) / 32 * 32;   // of a warp
-    const long long g0 = (rank * kVWarps + warp) * run;
-    const Pair a = pair_of(f.a), bb = pair_of(f.b);
-    if (command == kSum || !summed) {
+    const int groups = (int)((p.V + row.off + 3) >> 2);          // of four elements
+    const int run = (((groups + warps - 1) / warps) + 31) & ~31; // of a warp
+    const int g0 = (rank * kVWarps + warp) * run;
+    if (!(c.command & kSummed)) {
       // ---- the sum of what is left, and every warp's part of it
-      Pair s = {0.f, 0.f};
-      for (long long k = g0 + lane; k < min(g0 + run, groups); k += 32) {
-        Pair r[4];
-        left_of<HALF>(row, f, a, bb, c.gone, k, r);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s = add(s, r[e]);
-      }
-      for (int o = 16; o; o >>= 1) s = add(s, shfl_xor(s, o));
-      if (lane == 0) c.warp_sum[warp] = s;
-      cluster.sync();
-      if (tid < warps) c.all_sum[tid] = *cluster.map_shared_rank(&c.warp_sum[tid % kVWarps], tid / kVWarps);
-      cluster.sync();   // nobody writes the next sums, or leaves, before these are read
-      if (warp == 0) {
-        Pair z = {0.f, 0.f};
-        for (int x = lane; x < warps; x += 32) z = add(z, c.all_sum[x]);
-        for (int o = 16; o; o >>= 1) z = add(z, shfl_xor(z, o));
-        if (lane == 0) c.z = value(z);
-      }
-      summed = true;
-      __syncthreads();
-      if (command == kSum) continue;
-    }
-    // ---- the draw
-    const double z = c.z;
-    if (!(z > 0.0)) {
-      if (rank == 0 && tid == 0) {
-        p.next[b] = -1;
-        if (p.status) atomicOr(p.status, GQA_DEVICE_BAD_PROBS_BIT);
-      }
-    } else {
-      // The warp's run that holds the place, by every warp 0 alike.
-      if (warp == 0) {
-        const Pair goal = pair_of((double)p.sample_u[b] * z);
-        Pair before = {0.f, 0.f};
-        int at = -1, filled = -1;
-        Pair start = before;
-        for (int x0 = 0; x0 < warps && at < 0; x0 += 32) {
-          const Pair own = x0 + lane < warps ? c.all_sum[x0 + lane] : Pair{0.f, 0.f};
-          Pair s = own;
-          for (int o = 1; o < 32; o <<= 1) {
-            const Pair v = shfl_up(s, o);
-            if (lane >= o) s = add(v, s);
-          }
-          s = add(before, s);
-          const unsigned hit = __ballot_sync(0xffffffffu, own.hi > 0.f && above(s, goal));
-          const unsigned any = __ballot_sync(0xffffffffu, own.hi > 0.f);
-          // sums before each run
-          Pair prev = shfl_up(s, 1);
-          if (lane == 0) prev = before;
-          const int pick = hit ? __ffs(hit) - 1 : any ? 31 - __clz(any) : 0;
-          if (hit || any) {
-            filled = x0 + pick;
-            start.hi = __shfl_sync(0xffffffffu, prev.hi, pick);
-            start.lo = __shfl_sync(0xffffffffu, prev.lo, pick);
-          }
-          if (hit) at = x0 + pick;
-          before.hi = __shfl_sync(0xffffffffu, s.hi, 31);
-          before.lo = __shfl_sync(0xffffffffu, s.lo, 31);
+      Pair s[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+      const int k0 = max(g0, row.first()), k1 = min(g0 + run, row.end());
+      if (f.round > 0 && row.q) {
+        sum_run<HALF, true>(row, f, g0, k0, k1, 0, s);
+      } else {
+        // Groups of this lane with a token turned down: one by one (all of them where the run is too long for the mask).
+        unsigned long long skip = run > 32 * 64 && turned > 0 ? ~0ull : 0ull;
+        for (int x = 0; x < turned; ++x) {
+          const long long k = (((long long)c.gone[x] + row.off) >> 2) - g0;
+          if (k >= 0 && k < run && (k & 31) == lane) skip |= 1ull << (k >> 5 & 63);
         }
-        if (at < 0) at = filled;   // a number of 1 or more, or a rounding at the very end
-        if (at / kVWarps == rank) {
-          const long long b0 = (long long)at * run;
-          int token = -1, spare = -1;
-          Pair sum = start;
-          for (long long k0 = b0; k0 < min(b0 + run, groups) && token < 0; k0 += 32) {
+        sum_run<HALF, false>(row, f, g0, k0, k1, skip, s);
+        if (skip)
+          for (int k = g0 + lane; k < k1; k += 32) {
+            if (k < k0 || !(skip >> ((k - g0) >> 5 & 63) & 1u)) continue;
             Pair r[4];
-            const bool on = k0 + lane < groups;
-            if (on) left_of<HALF>(row, f, a, bb, c.gone, k0 + lane, r);
-            else r[0] = r[1] = r[2] = r[3] = {0.f, 0.f};
-            Pair s = {0.f, 0.f};
+            left_of4<HALF>(row, row.load(k), f, c.gone, turned, k, r);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s = add(s, r[e]);
-            const Pair own = s;
-            for (int o = 1; o < 32; o <<= 1) {
-              const Pair v = shfl_up(s, o);
-              if (lane >= o) s = add(v, s);
-            }
-            const Pair incl = add(sum, s);
-            const unsigned hit = __ballot_sync(0xffffffffu, own.hi > 0.f && above(incl, goal));
-            const unsigned any = __ballot_sync(0xffffffffu, own.hi > 0.f);
-            Pair prev = shfl_up(incl, 1);
-            if (lane == 0) prev = sum;
-            const int pick = hit ? __ffs(hit) - 1 : any ? 31 - __clz(any) : -1;
-            int found = -1, positive = -1;
-            if (lane == pick) {   // the element within the four
-              Pair run_sum = prev;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                run_sum = add(run_sum, r[e]);
-                if (r[e].hi > 0.f) {
-                  const int v = (int)(4 * (k0 + lane) - row.off) + e;
-                  positive = v;
-                  if (found < 0 && above(run_sum, goal)) found = v;
-                }
-              }
-            }
-            if (pick >= 0) {
-              found = __shfl_sync(0xffffffffu, found, pick);
-              positive = __shfl_sync(0xffffffffu, positive, pick);
-              spare = positive;
-              if (hit) token = found >= 0 ? found : positive;
-            }
-            sum.hi = __shfl_sync(0xffffffffu, incl.hi, 31);
-            sum.lo = __shfl_sync(0xffffffffu, incl.lo, 31);
+            for (int e = 0; e < 4; ++e) gather(s[e], r[e]);
           }
-          if (lane == 0) p.next[b] = token >= 0 ? token : spare;
+      }
+      // Elements of the groups that reach over the row's ends, a lane each: those before the first whole group (lanes
+      // 0..), those behind the last (16..).
+      if (g0 == 0 || (g0 < groups && g0 + run >= groups)) {
+        const long long head = min((long long)((4 - row.off) & 3), p.V);
+        const long long tail = max(4LL * row.end() - row.off, head);
+        const long long v = lane < 16 ? lane : tail + lane - 16;
+        const bool on = lane < 16 ? g0 == 0 && v < head : g0 + run >= groups && v < p.V;
+        if (on) {
+          const float pe = prob<HALF>(row.p, row.at + v), qe = row.q ? prob<HALF>(row.q, row.at + v) : 0.f;
+          Pair r = f.round == 0 || !row.q ? Pair{pe, 0.f} : left_of(pe, qe, f.a, f.b);
+          for (int x = 0; x < turned; ++x)
+            if (c.gone[x] == v) r.hi = 0.f;
+          gather(s[0], r);
         }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] = quick(s[e].hi, s[e].lo);
+      const Pair t = warp_sum(add(add(s[0], s[1]), add(s[2], s[3])));
+      Pair* dst = &c.sums[pass & 1][rank * kVWarps + warp];
+      if (lane < ranks) *cluster.map_shared_rank(dst, lane) = t;
+      cluster.sync();   // (two sets: the next pass writes the other one, and its barrier comes before this one's turn)
+      if (warp == 0) {
+        Pair w = {0.f, 0.f};
+        for (int x = lane; x < warps; x += 32) w = add(w, c.sums[pass & 1][x]);
+        const Pair sum = warp_sum(w);
+        if (command == kWhole) {
+          whole = sum;
+        } else {
+          z = sum;
+          summed = true;
+        }
+      }
+      ++pass;
+      if (command != kDraw) continue;
+    }
+    // ---- the draw: every warp 0 finds the warp whose run holds the place
+    if (warp == 0) {
+      int at = -1;
+      Pair before = {0.f, 0.f}, edge = {INFINITY, 0.f};   // nothing passes the edge: the last element with something
+      if (z.hi > 0.f) {
+        const Pair* sums = c.sums[(pass - 1) & 1];
+        const Pair goal = mul({p.sample_u[b], 0.f}, z);
+        // Four warps a lane, then the one of the four.
+        constexpr int kPer = kVMaxWarps / 32;
+        Pair part[kPer], own = {0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+          const int w = lane * kPer + x;
+          part[x] = w < warps ? sums[w] : Pair{0.f, 0.f};
+          own = add(own, part[x]);
+        }
+        int l0 = find_lane(own, goal, &before, &spare);
+        const bool beyond = l0 < 0;   // a number of 1 or more, or a rounding at the very end
+        if (beyond) l0 = spare;
+        int in = -1, filled = 0;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+          Pair v;
+          v.hi = __shfl_sync(0xffffffffu, part[x].hi, l0);
+          v.lo = __shfl_sync(0xffffffffu, part[x].lo, l0);
+          if (in >= 0 || !(v.hi > 0.f)) continue;
+          filled = x;
+          const Pair upto = add(before, v);
+          if (!beyond && above(upto, goal)) in = x;
+          else before = upto;
+        }
+        if (in >= 0) edge = goal;
+        at = l0 * kPer + (in >= 0 ? in : filled);
+      } else if (rank == 0 && lane == 0 && p.status) {
+        atomicOr(p.status, GQA_DEVICE_BAD_PROBS_BIT);
+      }
+      if (lane == 0) {
+        c.at = at;
+        c.before = before;
+        c.edge = edge;
+        if (at < 0 && rank == 0) p.next[b] = -1;
+      }
+    }
+    __syncthreads();
+    if (c.at >= 0 && c.at / kVWarps == rank) {
+      // ---- its run again, a sixteenth of it a warp (the row is in L1 or L2 by now)
+      const int sub = run / kVWarps;
+      const int b0 = c.at * run + warp * sub, b1 = min(b0 + sub, groups);
+      Pair sum = {0.f, 0.f};
+      for (int k = b0 + lane; k < b1; k += 32) {
+        Pair r[4];
+        left_of4<HALF>(row, row.load(k), f, c.gone, turned, k, r);
+        sum = add(sum, add(add(r[0], r[1]), add(r[2], r[3])));
+      }
+      sum = warp_sum(sum);
+      if (lane == 0) c.part[warp] = sum;
+      __syncthreads();
+      Pair before = c.before, edge = c.edge;
+      int mine = find_lane(lane < kVWarps ? c.part[lane] : Pair{0.f, 0.f}, edge, &before, &spare);
+      if (mine < 0) {
+        mine = spare;
+        edge = {INFINITY, 0.f};
+      }
+      if (warp == mine) {
+        int token = -1, behind = -1;   // behind: the last element with something so far
+        for (int k0 = b0; k0 < b1 && token < 0; k0 += 32) {
+          const int k = k0 + lane;
+          Pair r[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+          if (k < b1) left_of4<HALF>(row, row.load(k), f, c.gone, turned, k, r);
+          Pair upto = before;
+          const int hit = find_lane(add(add(r[0], r[1]), add(r[2], r[3])), edge, &upto, &spare);
+          const int pick = hit >= 0 ? hit : spare;
+          before = upto;
+          if (pick < 0) continue;
+          // The element of the four: where it passes, else the last one with something.
+          int found = -1, positive = -1;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            upto = add(upto, r[e]);
+            if (r[e].hi > 0.f) {
+              positive = 4 * k - row.off + e;
+              if (found < 0 && above(upto, edge)) found = positive;
+            }
+          }
+          found = __shfl_sync(0xffffffffu, found, pick);
+          positive = __shfl_sync(0xffffffffu, positive, pick);
+          behind = hit >= 0 && found >= 0 ? found : positive;
+          if (hit >= 0) token = behind;
+        }
+        if (lane == 0) p.next[b] = behind;
       }
     }
     break;
   }
   if (rank == 0) {
-    const int len = c.path_len;
-    for (int i = tid; i < p.S; i += kVThreads) path[i] = i < len ? c.path[i] : -1;
-    if (tid == 0) p.path_lens[b] = len;
+    const int path_len = c.path_len;
+    for (int i = tid; i < p.S; i += kVThreads) path[i] = i < path_len ? c.path[i] : -1;
+    if (tid == 0) p.path_lens[b] = path_len;
   }
+  cluster.sync();   // nobody leaves while its sums may still be written
 }
 
 // ------------------------------------------------------------------ accepted rows
@@ -456,7 +623,9 @@ cudaError_t launch_verify(const VerifyParams& p, int ranks, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_tree_verify(const VerifyParams& p, cudaStream_t st) {
-  const int ranks = p.V <= 4096 ? 1 : p.V <= 16384 ? 4 : kVMaxCluster;
+  // CTAs of a sequence: as many as have 4096 elements each and find room at once (two an SM).
+  int ranks = kVMaxCluster;
+  while (ranks > 1 && (p.V / ranks < 4096 || (long long)p.B * ranks > 304)) ranks /= 2;
   return p.half ? launch_verify<true>(p, ranks, st) : launch_verify<false>(p, ranks, st);
 }
 

@@ -319,6 +319,10 @@ def test_verify_refuses(change, status):
     (_set("acc.into_seqlens_k", lambda c: c.acc.seqlens_k), INVALID),                   # overlap
     (lambda c: c.keys.__setitem__(1, c.keys[0]), INVALID),                              # one cache twice
     (lambda c: c.values.__setitem__(0, c.keys[1]), INVALID),
+    (lambda c: setattr(c.values[0], "data", c.keys[1].data + 2 * 2 * 100 * 64 * 2 - 16), INVALID),   # its last bytes
+    (lambda c: setattr(c.acc.path, "data", c.keys[1].data + 64), INVALID),
+    (lambda c: setattr(c.acc.into_seqlens_k, "data", c.values[1].data), INVALID),
+    (lambda c: setattr(c.keys[1], "data", c.keys[1].data + 8), INVALID),                # alignment
     (lambda c: c.keys.__setitem__(0, c.t(capi.GQA_I8, (2, 2, 100, 64))), INVALID),
     (lambda c: c.keys.__setitem__(1, c.t(capi.GQA_F32, (2, 2, 100, 64))), INVALID),
     (lambda c: c.values.__setitem__(1, c.t(capi.GQA_F16, (2, 2, 99, 64))), INVALID),

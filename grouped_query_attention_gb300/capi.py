@@ -118,8 +118,8 @@ class GqaVerifyArgs(ctypes.Structure):
 
 
 class GqaAcceptArgs(ctypes.Structure):
-    _fields_ = [("present_keys", ctypes.POINTER(GqaTensor)), ("present_values", ctypes.POINTER(GqaTensor)),
-                ("num_layers", ctypes.c_int32)] + \
+    _fields_ = [("cache", GqaTensor), ("present_keys", ctypes.POINTER(ctypes.c_void_p)),
+                ("present_values", ctypes.POINTER(ctypes.c_void_p)), ("num_layers", ctypes.c_int32)] + \
                [(n, GqaTensor) for n in ("path", "path_lens", "seqlens_k", "new_lens", "into_seqlens_k")]
 
 

@@ -232,10 +232,9 @@ gqa_status gqa_tree_accept(gqa_handle* h, const gqa_accept_args* a, void* status
   if (!h || !a || !a->present_keys || !a->present_values) return fail(GQA_ERR_INVALID_ARGUMENT, "NULL handle, arguments or caches");
   if (a->num_layers < 1 || a->num_layers > GQA_MAX_TREE_LAYERS)
     return fail(GQA_ERR_INVALID_ARGUMENT, "num_layers must be in [1, %d]", GQA_MAX_TREE_LAYERS);
-  const gqa_tensor& c = a->present_keys[0];
+  const gqa_tensor& c = a->cache;
   gqa_status s;
-  if (!present(c)) return fail(GQA_ERR_INVALID_ARGUMENT, "present_keys[0] is missing");
-  if ((s = check_float(c, "present_keys")) != GQA_OK) return s;
+  if ((s = check_float(c, "cache")) != GQA_OK) return s;
   const long long Nkv = h->attrs.kv_num_heads;
   if (c.ndim != 4 || c.shape[0] < 1 || c.shape[1] != Nkv || c.shape[2] < 1 || c.shape[3] < 1)
     return fail(GQA_ERR_INVALID_ARGUMENT, "caches must be non-empty (B, kv_num_heads, C, head_size)");
@@ -255,11 +254,10 @@ gqa_status gqa_tree_accept(gqa_handle* h, const gqa_accept_args* a, void* status
   gqa::AcceptParams P;
   memset(&P, 0, sizeof(P));
   for (int i = 0; i < caches; ++i) {
-    const gqa_tensor& t = i & 1 ? a->present_values[i / 2] : a->present_keys[i / 2];
-    if (!present(t) || t.dtype != c.dtype || !shape_is(t, 4, c.shape))
-      return fail(GQA_ERR_INVALID_ARGUMENT, "caches must have one shape and dtype (layer %d)", i / 2);
-    if ((s = gqa::check_aligned(t, "a cache")) != GQA_OK) return s;
-    P.cache[i] = t.data;
+    void* data = i & 1 ? a->present_values[i / 2] : a->present_keys[i / 2];
+    if (!data || (reinterpret_cast<uintptr_t>(data) & 15u) != 0)
+      return fail(GQA_ERR_INVALID_ARGUMENT, "a cache of layer %d is missing or not 16-byte aligned", i / 2);
+    P.cache[i] = data;
   }
   // Caches of one size overlap when two of their addresses, in order, are nearer than it; the small tensors one by one.
   const size_t size = gqa::bytes_of(c);

@@ -7,9 +7,8 @@
 // in units of 64 (fp16) or 32 (fp32); all units are laid end to end and a CTA
 // takes an equal share, so a single long sequence fills the GPU as well as many
 // short ones. A CTA streams its units through shared memory (cp.async, two
-// stages). Its four warps hold 16 rows each; a tile of 16 or 32 rows has the
-// warps left over share the keys of a unit instead, and they join their results
-// at the end. The nodes' keys and values come from the call's own key and value
+// stages). Its warps hold 16 rows each; those left over share the keys of a unit
+// and join their results at the end. The nodes' keys and values come from the call's own key and value
 // tensors, so nothing waits for the append, which the same launch does.
 //
 // fp16: m16n8k16, fp32 sums; probabilities enter as 2^15 p (the row maximum is
@@ -26,13 +25,15 @@
 namespace gqa {
 namespace {
 
-constexpr int kThreads = 128;
 constexpr float kLiftHalf = 15.f;   // log2 of what fp16 probabilities are multiplied by
 
 template <typename T, int HP, int RW>
 struct Cfg {
   static constexpr bool kHalf = sizeof(T) == 2;
-  static constexpr int KW = 4 / RW;                      // warps that share a unit's keys
+  // Four warps; eight where registers leave an SM room for one CTA of four anyway (fp32 heads of 256: 199 -> 156 us).
+  static constexpr int kWarps = !kHalf && HP > 128 && RW > 1 ? 8 : 4;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int KW = kWarps / RW;                 // warps that share a unit's keys
   static constexpr int RT = 16 * RW;
   static constexpr int KT = kHalf ? 64 : 32;             // keys of a unit
   static constexpr int WK = KT / KW;                     // ... of a warp
@@ -102,10 +103,11 @@ __device__ __forceinline__ float2 unpack2(uint32_t h) { return __half22float2(*r
 __device__ __forceinline__ float capped(float s, float softcap) { return softcap * kLog2e * tanhf(s / softcap); }
 
 template <typename T, int HP, int RW>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(Cfg<T, HP, RW>::kThreads)
 tree_attn_kernel(const TreeParams p) {
   using K = Cfg<T, HP, RW>;
   constexpr bool kHalf = K::kHalf;
+  constexpr int kThreads = K::kThreads;
   constexpr int KT = K::KT, WK = K::WK, NT = WK / 8, ND = HP / 8;
   constexpr int kE = 16 / (int)sizeof(T);              // elements of a 16-byte chunk
   extern __shared__ __align__(128) uint8_t smem[];
@@ -284,7 +286,15 @@ tree_attn_kernel(const TreeParams p) {
       } else {
         const T* q0 = qs + (16 * rw + gq) * K::QS + 4 * t;
         const T* k0 = kt + (kw * WK + gq) * K::KS + 4 * t;
-#pragma unroll 2
+        // The products with a lo part add up on their own, hi ones over 16 coordinates at a time: short chains of MMAs
+        // (one of 6 for 16 coordinates: 279 us, this 240), whose rounding towards zero stays small (a single one of 48
+        // was 3.1e-6 off).
+        float cl[2][NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) cl[0][n][e] = cl[1][n][e] = 0.f;
+#pragma unroll 4
         for (int j = 0; j < HP / 16; ++j) {   // coordinates 16 j + 4 t ..: two MMA steps
           const float4 x0 = *reinterpret_cast<const float4*>(q0 + 16 * j);
           const float4 x1 = *reinterpret_cast<const float4*>(q0 + 8 * K::QS + 16 * j);
@@ -305,19 +315,21 @@ tree_attn_kernel(const TreeParams p) {
             split_tf32(y.y, &bh[0][1], &bl[0][1]);
             split_tf32(y.z, &bh[1][0], &bl[1][0]);
             split_tf32(y.w, &bh[1][1], &bl[1][1]);
-            // Small products first, and a sum of its own for 16 coordinates: a chain of 48 MMAs that round towards
-            // zero was 3.1e-6 off.
             float c[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_tf32(c, al[0], bh[0]);
-            mma_tf32(c, ah[0], bl[0]);
-            mma_tf32(c, al[1], bh[1]);
-            mma_tf32(c, ah[1], bl[1]);
-            mma_tf32(c, ah[0], bh[0]);
-            mma_tf32(c, ah[1], bh[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              mma_tf32(c, ah[h], bh[h]);
+              mma_tf32(cl[0][n], al[h], bh[h]);
+              mma_tf32(cl[1][n], ah[h], bl[h]);
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) sc[n][e] += c[e];
           }
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[n][e] += cl[0][n][e] + cl[1][n][e];
       }
       // ---- log2 domain, masks
 #pragma unroll
@@ -703,7 +715,7 @@ cudaError_t launch_rw(const TreeParams& p, cudaStream_t st) {
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
     done[dev] = true;
   }
-  return launch_dependent(false, kern, dim3((unsigned)p.workers), kThreads, (size_t)smem, st, p);
+  return launch_dependent(false, kern, dim3((unsigned)p.workers), Cfg<T, HP, RW>::kThreads, (size_t)smem, st, p);
 }
 
 template <typename T, int HP>
@@ -727,7 +739,8 @@ void tree_attn_plan(TreeParams* p) {
   const int rows = p->S * p->G;
   p->tc = use_tc(*p);
   p->lift = p->tc ? 6.f : p->t_type == kF16 ? kLiftHalf : 0.f;
-  // CTAs an SM holds: one of the pipeline; of the warp MMAs by two stages of 16 KB (H <= 64), 32 KB, 64 KB.
+  // CTAs an SM holds: one of the pipeline; of the warp MMAs by their registers and shared memory (two stages of 64 KB
+  // above a head size of 128).
   long long most = 152;
   if (p->tc) {
     p->rt_log2 = rows <= 128 ? 7 : 8;
@@ -735,7 +748,7 @@ void tree_attn_plan(TreeParams* p) {
   } else {
     p->rt_log2 = rows <= 16 ? 4 : rows <= 32 ? 5 : 6;
     p->unit_log2 = p->t_type == kF16 ? 6 : 5;
-    most *= p->H <= 64 ? 4 : p->H <= 128 ? 2 : 1;
+    most *= p->H <= 128 ? 2 : 1;
   }
   p->nrt = (rows + (1 << p->rt_log2) - 1) >> p->rt_log2;
   const int u = (1 << p->unit_log2) - 1;

@@ -536,8 +536,9 @@ typedef struct gqa_verify_args {
 GQA_API gqa_status gqa_tree_verify(gqa_handle* handle, const gqa_verify_args* args, void* status, void* stream);
 
 /* Accepted rows moved together, in the caches of all layers:
- *   present_keys, present_values  HOST arrays of num_layers caches T (B, N_kv, C, H)
- *                    of one shape and type, 1 <= num_layers <= GQA_MAX_TREE_LAYERS
+ *   cache            shape T (B, N_kv, C, H) and type of every cache (its data is not used)
+ *   present_keys, present_values  HOST arrays of the num_layers caches' device
+ *                    addresses, 1 <= num_layers <= GQA_MAX_TREE_LAYERS
  *   path, path_lens  int32 (B, S) and (B), as of gqa_tree_verify
  *   seqlens_k, new_lens  as they were for gqa_tree_forward
  *   into_seqlens_k   int32 (B): past_b + path_lens[b] - 1
@@ -548,7 +549,8 @@ GQA_API gqa_status gqa_tree_verify(gqa_handle* handle, const gqa_verify_args* ar
  * GQA_DEVICE_BAD_SEQLEN) or whose path does not increase within [0, n_b)
  * (GQA_DEVICE_BAD_TREE) keeps all rows and gets into_seqlens_k = -1. */
 typedef struct gqa_accept_args {
-  const gqa_tensor *present_keys, *present_values;
+  gqa_tensor cache;
+  void *const *present_keys, *const *present_values;
   int32_t num_layers;
   gqa_tensor path, path_lens;
   gqa_tensor seqlens_k, new_lens;

@@ -2,6 +2,7 @@
 the verification against the distribution it has to keep, and the host-side checks of the entry points (every refused
 call returns before any CUDA call; device pointers are fake aligned addresses)."""
 
+import ctypes
 import os
 
 import numpy as np
@@ -161,8 +162,8 @@ class Call:
         v.accept_uniforms, v.sample_uniforms = self.t(f, (B, S)), self.t(f, (B,))
         v.path, v.path_lens, v.next_token = self.t(i, (B, S)), self.t(i, (B,)), self.t(i, (B,))
         a = self.acc = capi.GqaAcceptArgs()
-        self.keys = (capi.GqaTensor * layers)(*(self.t(t, (B, Nkv, C, H)) for _ in range(layers)))
-        self.values = (capi.GqaTensor * layers)(*(self.t(t, (B, Nkv, C, H)) for _ in range(layers)))
+        a.cache = self.t(t, (B, Nkv, C, H))
+        self.keys, self.values = ((ctypes.c_void_p * layers)(*(self.t(t, (1,)).data for _ in range(layers))) for _ in range(2))
         a.present_keys, a.present_values, a.num_layers = self.keys, self.values, layers
         a.path, a.path_lens, a.seqlens_k, a.into_seqlens_k = self.t(i, (B, S)), self.t(i, (B,)), self.t(i, (B,)), self.t(i, (B,))
 
@@ -319,16 +320,16 @@ def test_verify_refuses(change, status):
     (_set("acc.into_seqlens_k", lambda c: c.acc.seqlens_k), INVALID),                   # overlap
     (lambda c: c.keys.__setitem__(1, c.keys[0]), INVALID),                              # one cache twice
     (lambda c: c.values.__setitem__(0, c.keys[1]), INVALID),
-    (lambda c: setattr(c.values[0], "data", c.keys[1].data + 2 * 2 * 100 * 64 * 2 - 16), INVALID),   # its last bytes
-    (lambda c: setattr(c.acc.path, "data", c.keys[1].data + 64), INVALID),
-    (lambda c: setattr(c.acc.into_seqlens_k, "data", c.values[1].data), INVALID),
-    (lambda c: setattr(c.keys[1], "data", c.keys[1].data + 8), INVALID),                # alignment
-    (lambda c: c.keys.__setitem__(0, c.t(capi.GQA_I8, (2, 2, 100, 64))), INVALID),
-    (lambda c: c.keys.__setitem__(1, c.t(capi.GQA_F32, (2, 2, 100, 64))), INVALID),
-    (lambda c: c.values.__setitem__(1, c.t(capi.GQA_F16, (2, 2, 99, 64))), INVALID),
-    (lambda c: c.values.__setitem__(1, capi.GqaTensor()), INVALID),
-    (lambda c: c.keys.__setitem__(0, c.t(capi.GQA_F16, (2, 4, 100, 64))), INVALID),
-    (lambda c: c.keys.__setitem__(0, c.t(capi.GQA_F16, (2, 2, 100, 24))), UNSUPPORTED),
+    (lambda c: c.values.__setitem__(0, c.keys[1] + 2 * 2 * 100 * 64 * 2 - 16), INVALID),   # another's last bytes
+    (lambda c: setattr(c.acc.path, "data", c.keys[1] + 64), INVALID),
+    (lambda c: setattr(c.acc.into_seqlens_k, "data", c.values[1]), INVALID),
+    (lambda c: c.keys.__setitem__(1, c.keys[1] + 8), INVALID),                          # alignment
+    (lambda c: c.values.__setitem__(1, None), INVALID),
+    (_set("acc.cache", lambda c: c.t(capi.GQA_I8, (2, 2, 100, 64))), INVALID),
+    (_set("acc.cache", lambda c: c.t(capi.GQA_BF16, (2, 2, 100, 64))), UNSUPPORTED),
+    (_set("acc.cache", lambda c: c.t(capi.GQA_F16, (2, 4, 100, 64))), INVALID),
+    (_set("acc.cache", lambda c: c.t(capi.GQA_F16, (2, 2, 100, 24))), UNSUPPORTED),
+    (_set("acc.cache", lambda c: c.t(capi.GQA_F16, (2, 2, 6400))), INVALID),
 ])
 def test_accept_refuses(change, status):
     c = Call()
@@ -362,6 +363,9 @@ def test_python_refuses_tensors_off_the_gpu_and_odd_lists():
         op.tree_verify(i, i, torch.zeros(1, 1, 8), torch.zeros(1, 1), torch.zeros(1))
     with pytest.raises(ValueError):
         op.tree_accept([(cache, cache)], i, i[0], i[0])
-    for caches in ([], [(cache,)], [(cache, cache)] * 129):
+    for caches in ([], [(cache,)], [(cache, cache)] * 129, [(cache, cache, cache), (cache,)], [(cache, cache[..., :32].contiguous())],
+                   [(cache, cache.half())]):
         with pytest.raises(ValueError, match="caches"):
             op.tree_accept(caches, i, i[0], i[0])
+    with pytest.raises(ValueError, match="contiguous"):
+        op.tree_accept([(cache, cache.transpose(2, 3))], i, i[0], i[0])

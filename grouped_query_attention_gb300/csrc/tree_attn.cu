@@ -577,16 +577,18 @@ tree_attn_kernel(const TreeParams p) {
 
 constexpr int kMergeWarps = 8;
 
-// Rows of ranges that several workers share: W warps take the pieces of a row in
-// turn, lanes over the coordinates. A piece's O is in units of its own maximum.
-// A block stays within a (b, g), rows [rows blockIdx.x, + rows).
-template <typename T, int W>
+// Rows of ranges that several workers share, four at a time: W warps take their
+// pieces in turn, a lane four (H / 32) groups of four coordinates of one row. A
+// piece's O is in units of its own maximum. A block stays within a (b, g), rows
+// [rows blockIdx.x, + rows). HG: 32-coordinate groups of a row.
+template <typename T, int W, int HG>
 __global__ void __launch_bounds__(32 * kMergeWarps)
 tree_merge_kernel(const TreeParams p, int rows) {
   constexpr int kTeams = kMergeWarps / W;
-  constexpr int kAhead = 4;                     // pieces of a warp under way
-  __shared__ float4 join[W > 1 ? kMergeWarps : 1][64];
+  constexpr int kAhead = HG > 4 ? 2 : 4;        // pieces of a warp under way
+  __shared__ float4 join[W > 1 ? kMergeWarps : 1][HG][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp / W, sub = warp % W;
+  const int ri = lane & 3, c8 = lane >> 2;      // row of the four; coordinates 4 (c8 + 8 k) ..
   const int b = blockIdx.y / p.Nkv, g = blockIdx.y % p.Nkv;
   long long units = 0, base = 0;
   TreeSeq s;
@@ -602,96 +604,115 @@ tree_merge_kernel(const TreeParams p, int rows) {
   }
   const int nrows = tree_seq(p, b, &s) ? s.fresh * p.G : 0;
   const long long live = tree_live(p, units);
-  const int ld_row = 1 << p.rt_log2;
+  const int tile = 1 << p.rt_log2;
+  // Rows of a slot's O side by side (the pipeline's threads hold one each), or its coordinates.
+  const int row_ld = p.tc ? 4 : p.H, col_ld = p.tc ? 4 * tile : 4;
   long long w0 = 0, w1 = 0;
   int rt = -1;
   dep_wait();
-  for (int r0 = blockIdx.x * rows; r0 < min((int)(blockIdx.x + 1) * rows, nrows); r0 += kTeams) {
-    const int r = min(r0 + team, nrows - 1);    // (a team without a row does the last one's work once more)
-    if (r >> p.rt_log2 != rt) {
-      rt = r >> p.rt_log2;
+  for (int r0 = blockIdx.x * rows; r0 < min((int)(blockIdx.x + 1) * rows, nrows); r0 += 4 * kTeams) {
+    // (A row behind the last, and a team without rows, does the last one's work once more. Four rows share a tile.)
+    const int r = min(r0 + 4 * team + ri, nrows - 1), first = min(r0 + 4 * team, nrows - 1);
+    if (first >> p.rt_log2 != rt) {
+      rt = first >> p.rt_log2;
       tree_pieces(base + (long long)(g * s.nrt + rt) * s.units, s.units - kTreeRangeCost, live, units, &w0, &w1);
     }
-    const int n = (int)(w1 - w0) + 1, hd = g * p.G + r % p.G;
-    float4 a[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};   // columns 4 lane .., + 128
+    const int n = (int)(w1 - w0) + 1, hd = g * p.G + r % p.G, row = r & (tile - 1);
+    float4 a[HG];
+#pragma unroll
+    for (int k = 0; k < HG; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
     if (n > 1) {                                // (else one worker wrote the output)
-      auto at = [&](int x) { return tree_slot(w0 + x, x == 0) * ld_row + (r & (ld_row - 1)); };
-      const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+      const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + row;
       const bool has_sink = p.sink || p.smooth;
       const float sg = has_sink ? (p.sink ? load_t(p.sink, hd, p.t_type) : 0.f) * kLog2e : kNegBig;
-      const float2 own = lane < n ? ml[at(lane)] : make_float2(kNegBig, 0.f);   // of piece `lane`
+      const float* src = p.part_o + (long long)row * row_ld + c8 * col_ld;
+      float4 o[kAhead][HG];
+      float f[kAhead];
+      auto load = [&](int x) {   // pieces x, x + W, ..: O and maximum
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+          const int at = min(x + y * W, n - 1);
+          const long long slot = tree_slot(w0 + at, at == 0) * tile;
+          f[y] = x + y * W < n ? ml[slot].x : -INFINITY;
+#pragma unroll
+          for (int k = 0; k < HG; ++k)
+            if (4 * (c8 + 8 * k) < p.H) o[y][k] = *reinterpret_cast<const float4*>(src + slot * p.H + 8 * k * col_ld);
+        }
+      };
+      load(sub);   // on their way while the row's maximum and sum are worked out, by the eight lanes that share it
+      const float2 own = c8 < n ? ml[tree_slot(w0 + c8, c8 == 0) * tile] : make_float2(kNegBig, 0.f);
       float m = fmaxf(sg, own.x);
-      for (int x = lane + 32; x < n; x += 32) m = fmaxf(m, ml[at(x)].x);
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      for (int x0 = 0; x0 < n; x0 += 32) {      // 32 pieces a turn: lane x has the factor of piece x0 + x
-        const float2 v = x0 == 0 ? own : x0 + lane < n ? ml[at(x0 + lane)] : make_float2(kNegBig, 0.f);
-        const float f = ex2(v.x - m);
-        l = fmaf(v.y, f, l);
-        for (int x = sub; x < min(32, n - x0); x += W * kAhead) {
-          float4 o[kAhead][2];
+      for (int x = c8 + 8; x < n; x += 8) m = fmaxf(m, ml[tree_slot(w0 + x, false) * tile].x);
 #pragma unroll
-          for (int k = 0; k < kAhead; ++k) {
-            if (x0 + x + k * W >= n || x + k * W >= 32) continue;
-            const float4* src = reinterpret_cast<const float4*>(p.part_o + at(x0 + x + k * W) * p.H);
-            if (4 * lane < p.H) o[k][0] = src[lane];
-            if (4 * lane + 128 < p.H) o[k][1] = src[lane + 32];
-          }
+      for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
+      l = own.y * ex2(own.x - m);
+      for (int x = c8 + 8; x < n; x += 8) {
+        const float2 v = ml[tree_slot(w0 + x, false) * tile];
+        l = fmaf(v.y, ex2(v.x - m), l);
+      }
 #pragma unroll
-          for (int k = 0; k < kAhead; ++k) {
-            const float fx = __shfl_sync(0xffffffffu, f, (x + k * W) & 31);
-            if (x0 + x + k * W >= n || x + k * W >= 32) continue;
+      for (int z = 4; z < 32; z <<= 1) l += __shfl_xor_sync(0xffffffffu, l, z);
+      if (has_sink) l += ex2(sg - m + p.lift);
+      for (int x = sub; x < n; x += W * kAhead) {
+        if (x != sub) load(x);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (4 * lane + 128 * h >= p.H) continue;
-              a[h].x = fmaf(o[k][h].x, fx, a[h].x);
-              a[h].y = fmaf(o[k][h].y, fx, a[h].y);
-              a[h].z = fmaf(o[k][h].z, fx, a[h].z);
-              a[h].w = fmaf(o[k][h].w, fx, a[h].w);
-            }
+        for (int y = 0; y < kAhead; ++y) {
+          const float fy = ex2(f[y] - m);
+          if (fy == 0.f) continue;              // (a piece without weight: whatever its O, or one counted already)
+#pragma unroll
+          for (int k = 0; k < HG; ++k) {
+            if (4 * (c8 + 8 * k) >= p.H) continue;
+            a[k].x = fmaf(o[y][k].x, fy, a[k].x);
+            a[k].y = fmaf(o[y][k].y, fy, a[k].y);
+            a[k].z = fmaf(o[y][k].z, fy, a[k].z);
+            a[k].w = fmaf(o[y][k].w, fy, a[k].w);
           }
         }
       }
-      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      if (has_sink) l += ex2(sg - m + p.lift);
     }
     if constexpr (W > 1) {
       __syncthreads();
-      join[warp][lane] = a[0];
-      join[warp][lane + 32] = a[1];
+#pragma unroll
+      for (int k = 0; k < HG; ++k) join[warp][k][lane] = a[k];
       __syncthreads();
       if (sub > 0) continue;
 #pragma unroll
       for (int x = 1; x < W; ++x)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 v = join[warp + x][lane + 32 * h];
-          a[h] = make_float4(a[h].x + v.x, a[h].y + v.y, a[h].z + v.z, a[h].w + v.w);
+        for (int k = 0; k < HG; ++k) {
+          const float4 v = join[warp + x][k][lane];
+          a[k] = make_float4(a[k].x + v.x, a[k].y + v.y, a[k].z + v.z, a[k].w + v.w);
         }
     }
-    if (n == 1 || r0 + team >= nrows) continue;
+    if (n == 1 || r0 + 4 * team + ri >= nrows) continue;
     const float inv = l > 0.f ? 1.f / l : 0.f;
     T* dst = static_cast<T*>(p.out) + (((long long)b * p.S + r / p.G) * p.N + hd) * p.H;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = 4 * lane + 128 * h;
+    for (int k = 0; k < HG; ++k) {
+      const int c = 4 * (c8 + 8 * k);
       if (c >= p.H) continue;
       if constexpr (sizeof(T) == 2)
-        *reinterpret_cast<uint2*>(dst + c) = make_uint2(pack2(a[h].x * inv, a[h].y * inv), pack2(a[h].z * inv, a[h].w * inv));
+        *reinterpret_cast<uint2*>(dst + c) = make_uint2(pack2(a[k].x * inv, a[k].y * inv), pack2(a[k].z * inv, a[k].w * inv));
       else
-        *reinterpret_cast<float4*>(dst + c) = make_float4(a[h].x * inv, a[h].y * inv, a[h].z * inv, a[h].w * inv);
+        *reinterpret_cast<float4*>(dst + c) = make_float4(a[k].x * inv, a[k].y * inv, a[k].z * inv, a[k].w * inv);
     }
   }
 }
 
+template <typename T, int W, int HG>
+cudaError_t merge_hg(const TreeParams& p, cudaStream_t st) {
+  constexpr int kStep = 4 * kMergeWarps / W;   // rows of a turn
+  // Rows of a block: so many that the blocks fit the GPU about once beside the attention.
+  const long long per_head = ((long long)p.S * p.G + kStep - 1) / kStep, all = per_head * p.B * p.Nkv;
+  const int rows = (int)((all + 911) / 912) * kStep;
+  const dim3 grid((unsigned)((p.S * p.G + rows - 1) / rows), (unsigned)(p.B * p.Nkv));
+  return launch_dependent(true, tree_merge_kernel<T, W, HG>, grid, 32 * kMergeWarps, 0, st, p, rows);
+}
+
 template <typename T, int W>
 cudaError_t merge_w(const TreeParams& p, cudaStream_t st) {
-  constexpr int kTeams = kMergeWarps / W;
-  // Rows of a block: so many that the blocks fit the GPU about once beside the attention.
-  const long long all = (long long)p.B * p.Nkv * p.S * p.G;
-  const int rows = (int)((all + 912LL * kTeams - 1) / (912LL * kTeams)) * kTeams;
-  const dim3 grid((unsigned)((p.S * p.G + rows - 1) / rows), (unsigned)(p.B * p.Nkv));
-  return launch_dependent(true, tree_merge_kernel<T, W>, grid, 32 * kMergeWarps, 0, st, p, rows);
+  return p.H <= 64 ? merge_hg<T, W, 2>(p, st) : p.H <= 128 ? merge_hg<T, W, 4>(p, st) : merge_hg<T, W, 8>(p, st);
 }
 
 template <typename T>

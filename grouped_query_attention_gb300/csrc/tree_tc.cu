@@ -625,7 +625,8 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk, cons
           const float den = fmaf(l, fm, extra);
           so = den > 0.f ? fm / den : 0.f;
         }
-        const long long row = tree_slot(blockIdx.x, w.off == 0) * kRows + (NQ == 2 ? q * 128 : 0) + rl;
+        const int rl_tile = (NQ == 2 ? q * 128 : 0) + rl;
+        const long long row = tree_slot(blockIdx.x, w.off == 0) * kRows + rl_tile;
         if (!whole && live_row && (NQ == 2 || q == 0)) *reinterpret_cast<float2*>(p.part_ml + row * 2) = make_float2(m, l);
         const volatile unsigned* odd = sm.odd[piece % kOddSets];   // (written before the P V that o_done stands for)
         const bool any_odd = odd[kOddNodes + kOddEdge] != 0u;
@@ -690,10 +691,11 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk, cons
               if (d0 + e < p.H) *reinterpret_cast<uint4*>(dst + e) = make_uint4(u[0], u[1], u[2], u[3]);
             }
           } else {
-            float* dst = p.part_o + row * p.H + d0;
+            // a slot's rows side by side: a warp writes 512 bytes in a row
+            float* dst = p.part_o + (row - rl_tile) * p.H + 4 * rl_tile;
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              if (d0 + e < p.H) *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              if (d0 + e < p.H) *reinterpret_cast<float4*>(dst + (d0 + e) * kRows) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
         }
       }

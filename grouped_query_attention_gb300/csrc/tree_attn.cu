@@ -520,7 +520,7 @@ tree_attn_kernel(const TreeParams p) {
       }
     }
     // ---- write: all of a range to the output, a part of it to the workspace
-    const bool whole = n_units == s.units - kTreeRangeCost;
+    const bool whole = n_units == s.work;
     if (kw == 0) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -538,7 +538,7 @@ tree_attn_kernel(const TreeParams p) {
             extra = ex2(sg - mf + (kHalf ? kLiftHalf : 0.f));
           }
           const float den = fmaf(l[h], fm, extra);
-          so = den > 0.f ? fm / den : 0.f;
+          so = den == 0.f ? 0.f : fm / den;
         } else if (t == 0) {
           *reinterpret_cast<float2*>(p.part_ml + (slot * K::RT + rl) * 2) = make_float2(m[h], l[h]);
         }
@@ -615,7 +615,7 @@ tree_merge_kernel(const TreeParams p, int rows) {
     const int r = min(r0 + 4 * team + ri, nrows - 1), first = min(r0 + 4 * team, nrows - 1);
     if (first >> p.rt_log2 != rt) {
       rt = first >> p.rt_log2;
-      tree_pieces(base + (long long)(g * s.nrt + rt) * s.units, s.units - kTreeRangeCost, live, units, &w0, &w1);
+      tree_pieces(base + (long long)(g * s.nrt + rt) * s.units, s.work, live, units, &w0, &w1);
     }
     const int n = (int)(w1 - w0) + 1, hd = g * p.G + r % p.G, row = r & (tile - 1);
     float4 a[HG];
@@ -686,7 +686,7 @@ tree_merge_kernel(const TreeParams p, int rows) {
         }
     }
     if (n == 1 || r0 + 4 * team + ri >= nrows) continue;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;   // (a NaN goes on, also from a piece without weight)
     T* dst = static_cast<T*>(p.out) + (((long long)b * p.S + r / p.G) * p.N + hd) * p.H;
 #pragma unroll
     for (int k = 0; k < HG; ++k) {
@@ -764,9 +764,11 @@ void tree_attn_plan(TreeParams* p) {
   // above a head size of 128).
   long long most = 152;
   if (p->tc) {
+    p->cost = 4;   // (16 sequences of 1k to 8k rows with a softcap: 85 us, 91 with 2)
     p->rt_log2 = rows <= 128 ? 7 : 8;
     p->unit_log2 = 7;
   } else {
+    p->cost = 2;
     p->rt_log2 = rows <= 16 ? 4 : rows <= 32 ? 5 : 6;
     p->unit_log2 = p->t_type == kF16 ? 6 : 5;
     most *= p->H <= 128 ? 2 : 1;
@@ -775,7 +777,7 @@ void tree_attn_plan(TreeParams* p) {
   const int u = (1 << p->unit_log2) - 1;
   const int keys = p->window >= 0 && p->window < p->T - p->S ? p->window + 16 : p->T;
   const long long ranges = (long long)p->B * p->Nkv * p->nrt;
-  const long long units = ranges * (((keys + u) >> p->unit_log2) + ((p->S + u) >> p->unit_log2) + kTreeRangeCost);
+  const long long units = ranges * (((keys + u) >> p->unit_log2) + ((p->S + u) >> p->unit_log2) + p->cost);
   p->workers = (int)(units < most ? units : most);
 }
 

@@ -34,6 +34,7 @@ struct TreeParams {
   float lift;            // log2 of what the workspace's probabilities (l and O) are multiplied by
   // split over the keys
   int rt_log2, unit_log2;   // query rows of a row tile, keys of a unit: powers of two
+  int cost;              // units that the start and the end of a range count as
   int nrt;               // row tiles of S nodes
   int workers;           // shares of the units
   float *part_o, *part_ml;
@@ -56,13 +57,12 @@ __device__ __forceinline__ int tree_parent(int a, int i, bool* bad) {
 
 // ---- the units of all ranges (sequence b, KV head g, row tile rt), laid end
 // to end: a range has the cached rows' units from the first a row sees on, the
-// nodes' units, and kTreeRangeCost more for its start and end.
-constexpr int kTreeRangeCost = 2;
+// nodes' units, and `cost` more for its start and end.
 
 struct TreeSeq {
   int past, fresh;   // cached rows, nodes
   int k0;            // first cached row of the first unit
-  int np, units;     // units of cached rows; of a range
+  int np, work, units;   // units of cached rows; of all a range's keys; and with the cost of its ends
   int nrt;           // row tiles
 };
 
@@ -72,7 +72,8 @@ __device__ __forceinline__ bool tree_seq(const TreeParams& p, int b, TreeSeq* s)
   s->k0 = p.window >= 0 ? max(0, s->past - p.window) & ~15 : 0;   // the root sees furthest back
   const int u = (1 << p.unit_log2) - 1;
   s->np = (s->past - s->k0 + u) >> p.unit_log2;
-  s->units = s->np + ((s->fresh + u) >> p.unit_log2) + kTreeRangeCost;
+  s->work = s->np + ((s->fresh + u) >> p.unit_log2);
+  s->units = s->work + p.cost;
   s->nrt = (s->fresh * p.G + (1 << p.rt_log2) - 1) >> p.rt_log2;
   return s->fresh > 0;
 }
@@ -122,7 +123,7 @@ struct TreeWalk {
   }
   // Past the end of a range: the next one.
   __device__ void settle(const TreeParams& p) {
-    while (left > 0 && off >= s.units - kTreeRangeCost) {
+    while (left > 0 && off >= s.work) {
       left -= s.units - off;
       off = 0;
       if (++rt == s.nrt) {
@@ -136,7 +137,7 @@ struct TreeWalk {
     }
   }
   // Units of this range in the share.
-  __device__ int piece() const { return (int)min(left, (long long)(s.units - kTreeRangeCost - off)); }
+  __device__ int piece() const { return (int)min(left, (long long)(s.work - off)); }
   __device__ void next(const TreeParams& p, int n) {
     off += n;
     left -= n;

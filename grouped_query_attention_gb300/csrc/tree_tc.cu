@@ -612,7 +612,7 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk, cons
       }
       tc_fence_after();
       if (ok) {
-        const bool whole = n == s.units - kTreeRangeCost;
+        const bool whole = n == s.work;
         float so = 1.f;
         if (whole) {
           float extra = 0.f, fm = 1.f;
@@ -623,7 +623,7 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk, cons
             extra = ex2(sg - mf + kLift);
           }
           const float den = fmaf(l, fm, extra);
-          so = den > 0.f ? fm / den : 0.f;
+          so = den == 0.f ? 0.f : fm / den;
         }
         const int rl_tile = (NQ == 2 ? q * 128 : 0) + rl;
         const long long row = tree_slot(blockIdx.x, w.off == 0) * kRows + rl_tile;

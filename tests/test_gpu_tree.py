@@ -223,6 +223,58 @@ def test_infinite_and_nan_values_reach_only_who_sees_them():
                 assert (~np.isfinite(row)).all() if spoiled else (np.abs(row - ref[b, i]) <= tol[b, i]).all()
 
 
+@pytest.mark.parametrize("name", ["tile_64", "tile_64_f32", "h256", "window"])
+def test_a_nan_score_is_not_lost(name):
+    """The root's key is NaN: every node sees it, the root (whose other keys are in other units) too."""
+    d = make(CASES[name])
+    d["k"][:, 0] = np.nan
+    assert np.isnan(run_gpu(d)[0]).all()
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_forward_random(seed):
+    """Sizes, masks and types drawn over the range of a call."""
+    rng = np.random.default_rng([seed, 17])
+    H = int(rng.choice([16, 64, 80, 96, 128, 128, 256]))
+    Nkv, B = int(rng.choice([1, 2, 3])), int(rng.choice([1, 2, 3, 5]))
+    N, S = Nkv * int(rng.choice([1, 2, 3, 4, 7, 8])), int(rng.choice([1, 2, 5, 11, 33, 70, 130]))
+    C = S + int(rng.choice([0, 1, 40, 127, 128, 300, 900]))
+    news = tuple(int(x) for x in rng.integers(0, S + 1, B)) if rng.random() < 0.5 else None
+    totals = tuple(int(rng.integers(S if news is None else news[b], C + 1)) for b in range(B))
+    case = (str(rng.choice(["f16", "f16", "f32"])), B, S, N, Nkv, H, C, totals, news, int(rng.choice([-1, -1, 0, 3, 60, C])),
+            float(rng.choice([0, 0, 2.0, 30.0])), int(rng.integers(0, 2)), int(rng.integers(0, 2)),
+            str(rng.choice(["tree", "chain", "star", "forest"])), int(rng.integers(0, 2)))
+    d = make(case, seed)
+    got = run_gpu(d, total=C if rng.random() < 0.5 else None)
+    check(d, got)
+    assert got[3].block_status() == 0
+
+
+@pytest.mark.parametrize("dtype,H,rows", [("f16", 128, 17_500_000), ("f32", 128, 9_000_000)])
+def test_rows_behind_two_gigabytes(dtype, H, rows):
+    """Offsets of a cache past 2^31 elements (fp16) and 2^32 bytes (fp32): a window at its end, and the move of its rows."""
+    rng = np.random.default_rng(8)
+    S, N, W = 6, 4, 200
+    t = NP[dtype]
+    tail = [rng.standard_normal((1, 1, 400, H)).astype(t) for _ in range(2)]
+    q, k, v = (rng.standard_normal((1, S, n * H)).astype(t) for n in (N, 1, 1))
+    par = np.array([[-1, 0, 0, 1, 3, 2]], np.int32)
+    op = GroupQueryAttention(N, 1, local_window_size=W)
+    big = [torch.empty((1, 1, rows, H), dtype=getattr(torch, "float16" if dtype == "f16" else "float32"), device="cuda") for _ in range(2)]
+    for b, x in zip(big, tail):
+        b[:, :, rows - 400:] = dev(x)
+    out = op.tree_forward(dev(q), dev(k), dev(v), dev(par), dev(np.array([rows - 1], np.int32)), rows, *big)
+    d = dict(dtype=dtype, H=H, softcap=0, totals=np.array([400]), v=v, pv=tail[1])
+    want, mag, reach = ot.forward(q, k, v, par, np.array([399]), None, *tail, N, 1, window=W)
+    assert (np.abs(out.cpu().numpy() - want) <= tolerance(d, want, mag, reach)).all()
+    path, lens = np.array([[0, 1, 3, 4, -1, -1]], np.int32), np.array([4], np.int32)
+    got = op.tree_accept([tuple(big)], dev(path), dev(lens), dev(np.array([rows - 1], np.int32)))
+    ot.accept(tail, path, lens, np.array([399]))
+    assert got.tolist() == [rows - S + 3] and op.block_status() == 0
+    for b, x in zip(big, tail):
+        assert np.array_equal(b[:, :, rows - 400:].cpu().numpy(), x)
+
+
 def test_a_second_stream_and_a_graph():
     d = make(CASES["tile_32"])
     want = run_oracle(d)

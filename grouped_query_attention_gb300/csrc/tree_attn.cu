@@ -30,8 +30,8 @@ constexpr float kLiftHalf = 15.f;   // log2 of what fp16 probabilities are multi
 template <typename T, int HP, int RW>
 struct Cfg {
   static constexpr bool kHalf = sizeof(T) == 2;
-  // Four warps; eight where registers leave an SM room for one CTA of four anyway (fp32 heads of 256: 199 -> 156 us).
-  static constexpr int kWarps = !kHalf && HP > 128 && RW > 1 ? 8 : 4;
+  // Four warps; eight where shared memory leaves an SM room for one CTA anyway (heads of 256: fp32 199 -> 156 us).
+  static constexpr int kWarps = HP > 128 && RW > 1 ? 8 : 4;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int KW = kWarps / RW;                 // warps that share a unit's keys
   static constexpr int RT = 16 * RW;
@@ -119,6 +119,8 @@ tree_attn_kernel(const TreeParams p) {
   T* ring = qs + K::RT * K::QS;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, t = lane & 3;
   const int rw = warp % RW, kw = warp / RW;
+  constexpr int kFetchRows = kThreads / (HP / kE);     // of a unit that the CTA copies at a time: this thread's, its chunk
+  const int fr = tid / (HP / kE), fc = tid % (HP / kE);
 
   // ---- status, padding rows, the append: every CTA a part
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -184,17 +186,17 @@ tree_attn_kernel(const TreeParams p) {
       const int n = min(KT, cached ? s.past - first : s.fresh - first);
       const long long ld = cached ? p.H : (long long)p.Nkv * p.H;
       const long long at = cached ? (bg * p.C + first) * p.H : (((long long)w.b * p.S + first) * p.Nkv + w.g) * p.H;
-      const T* ksrc = static_cast<const T*>(cached ? p.kc : p.k) + at;
-      const T* vsrc = static_cast<const T*>(cached ? p.vc : p.v) + at;
-      T* kd = ring + st * (K::kStage / (int)sizeof(T));
-      T* vd = kd + KT * K::KS;
-#pragma unroll 4
-      for (int x = tid; x < KT * (HP / kE); x += kThreads) {
-        const int r = x / (HP / kE), c = x % (HP / kE);
-        const bool on = r < n && c * kE < p.H;
-        const long long o = on ? r * ld + c * kE : 0;
-        cp16(saddr(kd + r * K::KS + c * kE), ksrc + o, on);
-        cp16(saddr(vd + r * K::VS + c * kE), vsrc + o, on);
+      const T* ksrc = static_cast<const T*>(cached ? p.kc : p.k) + at + fr * ld + fc * kE;
+      const T* vsrc = static_cast<const T*>(cached ? p.vc : p.v) + at + fr * ld + fc * kE;
+      const uint32_t kd = saddr(ring) + st * K::kStage + (fr * K::KS + fc * kE) * (uint32_t)sizeof(T);
+      const uint32_t vd = saddr(ring) + st * K::kStage + (KT * K::KS + fr * K::VS + fc * kE) * (uint32_t)sizeof(T);
+#pragma unroll
+      for (int i = 0; i < KT; i += kFetchRows) {
+        const bool on = fr + i < n && fc * kE < p.H;
+        cp16(kd + i * K::KS * (uint32_t)sizeof(T), ksrc, on);
+        cp16(vd + i * K::VS * (uint32_t)sizeof(T), vsrc, on);
+        ksrc += kFetchRows * ld;
+        vsrc += kFetchRows * ld;
       }
     };
     fetch(w.off, 0);

@@ -297,7 +297,7 @@ tree_attn_kernel(const TreeParams p) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) cl[0][n][e] = cl[1][n][e] = 0.f;
 #pragma unroll 4
-        for (int j = 0; j < HP / 16; ++j) {   // coordinates 16 j + 4 t ..: two MMA steps
+        for (int j = 0; j < (HP > 64 ? p.H / 16 : HP / 16); ++j) {   // coordinates 16 j + 4 t ..: two MMA steps
           const float4 x0 = *reinterpret_cast<const float4*>(q0 + 16 * j);
           const float4 x1 = *reinterpret_cast<const float4*>(q0 + 8 * K::QS + 16 * j);
           uint32_t ah[2][4], al[2][4];
@@ -389,6 +389,7 @@ tree_attn_kernel(const TreeParams p) {
         const uint32_t va = saddr(vt + (kw * WK + (lane & 15)) * K::VS + (lane >> 4) * 8);
 #pragma unroll
         for (int d = 0; d < ND; d += 2) {
+          if (HP > 64 && 8 * d >= p.H) break;
           float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
           for (int n = 0; n < NT; n += 2) {
@@ -417,6 +418,7 @@ tree_attn_kernel(const TreeParams p) {
         const T* v0 = vt + (kw * WK + 2 * t) * K::VS + 4 * gq;
 #pragma unroll
         for (int d = 0; d < ND; d += 4) {   // coordinates 8 d + 4 gq + e of MMA d + e
+          if (HP > 64 && 8 * d >= p.H) break;
           float c[4][4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) c[y][0] = c[y][1] = c[y][2] = c[y][3] = 0.f;

@@ -15,6 +15,12 @@
 // are pairs of floats (48 bits; the difference of two floats is exact), as 64-bit
 // arithmetic runs at 1/64 of the rate here.
 //
+// What bounds it: the steps one behind the other. A pass over a row is loads, two
+// dozen operations a pair of probabilities, a cluster barrier; every token turned
+// down is one more pass, and the draw reads a warp's run again. 16 chains of 8 over
+// 131072 tokens: 19 us for 14 MB; 16 trees of 64 nodes over 100003 31 us. Clusters
+// of 8 CTAs of 512 threads were the fastest (256 and 1024 threads, one CTA an SM,
+// at most 152 or 608 CTAs: slower or the same).
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
@@ -202,10 +208,11 @@ __device__ __noinline__ void left_of4(const Row<HALF>& row, typename Row<HALF>::
 }
 
 // Sum of what is left of groups g0 + lane, + 32, .. within [first, k1), in four
-// chains, without the turns in `skip`. A turn's loads are all under way before the
+// chains, without the turns in `skip` (a bit stands for 2^fold of them). A turn's loads are all under way before the
 // first is looked at (with a condition around each they came one by one).
 template <bool HALF, bool DRAFT>
-__device__ __forceinline__ void sum_run(const Row<HALF>& row, const Left& f, int g0, int first, int k1, unsigned long long skip, Pair* s) {
+__device__ __forceinline__ void sum_run(const Row<HALF>& row, const Left& f, int g0, int first, int k1, unsigned long long skip, int fold,
+                                        Pair* s) {
   constexpr int kGroups = 2;   // (3 or 4: the same or slower, as more instructions come from cold memory)
   if (first >= k1) return;
   for (int k = g0 + (threadIdx.x & 31); k < k1; k += 32 * kGroups) {
@@ -223,7 +230,7 @@ __device__ __forceinline__ void sum_run(const Row<HALF>& row, const Left& f, int
       if constexpr (DRAFT) qv = Row<HALF>::values(qr[x]);
       const int kx = k + 32 * x;
       bool on = kx >= first && kx < k1;
-      if constexpr (!DRAFT) on = on && !(skip >> ((kx - g0) >> 5 & 63) & 1u);
+      if constexpr (!DRAFT) on = on && !(skip >> ((kx - g0) >> fold & 63) & 1u);
       const float pe[4] = {pv.x, pv.y, pv.z, pv.w}, qe[4] = {qv.x, qv.y, qv.z, qv.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -407,18 +414,19 @@ tree_verify_kernel(const VerifyParams p) {
       Pair s[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
       const int k0 = max(g0, row.first()), k1 = min(g0 + run, row.end());
       if (f.round > 0 && row.q) {
-        sum_run<HALF, true>(row, f, g0, k0, k1, 0, s);
+        sum_run<HALF, true>(row, f, g0, k0, k1, 0, 5, s);
       } else {
-        // Groups of this lane with a token turned down: one by one (all of them where the run is too long for the mask).
-        unsigned long long skip = run > 32 * 64 && turned > 0 ? ~0ull : 0ull;
+        // Groups of this lane with a token turned down, and those that share a bit of the mask with one: one by one.
+        const int fold = run > 32 * 64 ? 32 - __clz((run - 1) >> 6) : 5;   // run <= 64 << fold
+        unsigned long long skip = 0ull;
         for (int x = 0; x < turned; ++x) {
           const long long k = (((long long)c.gone[x] + row.off) >> 2) - g0;
-          if (k >= 0 && k < run && (k & 31) == lane) skip |= 1ull << (k >> 5 & 63);
+          if (k >= 0 && k < run && (k & 31) == lane) skip |= 1ull << (k >> fold);
         }
-        sum_run<HALF, false>(row, f, g0, k0, k1, skip, s);
+        sum_run<HALF, false>(row, f, g0, k0, k1, skip, fold, s);
         if (skip)
           for (int k = g0 + lane; k < k1; k += 32) {
-            if (k < k0 || !(skip >> ((k - g0) >> 5 & 63) & 1u)) continue;
+            if (k < k0 || !(skip >> ((k - g0) >> fold) & 1u)) continue;
             Pair r[4];
             left_of4<HALF>(row, row.load(k), f, c.gone, turned, k, r);
 #pragma unroll
@@ -569,7 +577,9 @@ constexpr int kAhead = 8;   // rows of a thread under way
 
 // A thread owns one 16-byte column of a (cache, sequence, KV head) and moves its
 // rows in order. A path increases, so row path[i] >= i, and what a group of rows
-// writes lies below everything later groups read.
+// writes lies below everything later groups read. Rows that stay are not read.
+// Bound: the two dependent loads, of the path and of the rows (16 layers of 16
+// sequences, trees of 64 nodes: 10.5 us for 12 MB).
 __global__ void __launch_bounds__(kAThreads)
 tree_accept_kernel(const AcceptParams p) {
   __shared__ short path[kTreeNodes];

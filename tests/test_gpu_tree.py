@@ -396,6 +396,17 @@ def test_verify(name):
         assert op.block_status() == 0
 
 
+@pytest.mark.parametrize("drafts", [True, False])
+def test_verify_vocabulary_past_a_warps_mask(drafts):
+    """More than 2^20 tokens: a warp's run has more turns than the 64 bits that mark those with a token turned down."""
+    for seed in range(2):
+        v = make_verify(2, 6, 1100003, drafts=drafts, kind="star", seed=seed)
+        v["accept_uniforms"][:, 1:] = 1.0 - 2.0 ** -24   # (turns most drafts down)
+        if not drafts:
+            v["tokens"][:, 1:3] = [[0, 1100002], [524287, 7]]
+        same(run_verify(v), ot.verify(**v))
+
+
 def test_verify_takes_one_tree_for_all():
     v = make_verify(4, 9, 500, kind="star")
     v["parents"] = v["parents"][:1]

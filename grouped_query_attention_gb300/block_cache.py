@@ -150,7 +150,7 @@ class BlockCacheOps:
 
     def block_status(self, device=None) -> int:
         """Synchronise the current stream, then return and clear the GQA_DEVICE_* bits that ``rotary_axes``,
-        ``block_forward`` and ``block_evict`` calls of this operator set on `device` since the last reading."""
+        ``block_*`` and ``tree_*`` calls of this operator set on `device` since the last reading."""
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         index = torch.cuda.current_device() if dev.index is None else dev.index
         s = self._block_status.get(index)

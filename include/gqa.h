@@ -229,7 +229,8 @@ GQA_API gqa_status gqa_forward_noalloc(gqa_handle* handle, const gqa_inputs* in,
  *     conversion), so the waits for that tile expire: a test of the timeout
  *     path that faults nothing.
  * Applies to the following gqa_forward / gqa_forward_noalloc calls on the
- * handle. Host-only; INVALID_ARGUMENT for a NULL handle or a value out of range. */
+ * handle, and to gqa_tree_forward where it runs on the tensor-core pipeline.
+ * Host-only; INVALID_ARGUMENT for a NULL handle or a value out of range. */
 GQA_API gqa_status gqa_set_wait_limit(gqa_handle* handle, int64_t cycles, int32_t withhold_copy);
 
 /* Synchronise `stream`, read and clear the status word that the kernels of
@@ -486,9 +487,10 @@ GQA_API gqa_status gqa_tree_describe_plan(const gqa_handle* handle, const gqa_tr
  *      logit to the denominator as in gqa_forward.
  * Rows of the caches outside [past_b, past_b + n_b) keep their bytes, and what
  * rows from past_b on held before does not matter. A key or value that is not
- * finite reaches only the rows that see it (fp32: an infinite key reads as NaN). Attributes used: num_heads,
- * kv_num_heads, local_window_size, scale, softcap, smooth_softmax; causal must
- * be 1 and do_rotary, the quant types and sliding_window_cache off.
+ * finite reaches only the rows that see it (fp32: an infinite key reads as NaN).
+ * Attributes used: num_heads, kv_num_heads, local_window_size, scale, softcap,
+ * smooth_softmax; causal must be 1 and do_rotary, the quant types and
+ * sliding_window_cache off.
  * workspace and status as for gqa_block_forward. A sequence with lengths out of
  * range (seqlens_k[b] + 1 outside [n_b, total_sequence_length], n_b outside
  * [0, S]) is skipped, nothing of it is written, and GQA_DEVICE_BAD_SEQLEN set. */

@@ -407,6 +407,23 @@ def test_verify_vocabulary_past_a_warps_mask(drafts):
         same(run_verify(v), ot.verify(**v))
 
 
+def test_verify_rows_behind_two_billion_elements():
+    """A chain of certain rows (every draft passes), the last of which lies behind 2^31 elements: it holds two tokens."""
+    S, V = 512, 4200003
+    tokens = torch.from_numpy(np.random.default_rng(8).integers(0, V, (1, S)).astype(np.int32)).cuda()
+    p = torch.zeros((1, S, V), dtype=torch.float16, device="cuda")
+    p[0, torch.arange(S - 1), tokens[0, 1:].long()] = 1.0
+    p[0, S - 1, 7], p[0, S - 1, V - 1] = 0.25, 0.75
+    op = GroupQueryAttention(1, 1)
+    for draft in (None, p):
+        for u, want in ((0.125, 7), (0.5, V - 1)):
+            path, lens, token = op.tree_verify(tokens, dev(np.arange(-1, S - 1, dtype=np.int32)[None]), p,
+                                               torch.full((1, S), 0.75, device="cuda"), torch.full((1,), u, device="cuda"),
+                                               draft_probs=draft)
+            assert torch.equal(path[0].cpu(), torch.arange(S, dtype=torch.int32)) and (int(lens), int(token)) == (S, want)
+    assert op.block_status() == 0
+
+
 def test_verify_takes_one_tree_for_all():
     v = make_verify(4, 9, 500, kind="star")
     v["parents"] = v["parents"][:1]

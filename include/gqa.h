@@ -432,7 +432,7 @@ GQA_API gqa_status gqa_block_evict(gqa_handle* handle, const gqa_evict_args* arg
 
 /* ---- Drafted tokens: tree attention, verification, accepted rows ----------
  * Generation that drafts several continuations of every sequence and lets the
- * model judge all of them in one step. The drafts of a sequence are n_b nodes,
+ * model weigh all of them in one step. The drafts of a sequence are n_b nodes,
  * n_b = new_lens[b] (S without new_lens; 0 <= n_b <= S). Node i has the parent
  * parents[b][i], a node before it, or -1: parents[b][i] < i. Node 0 is the root,
  * the sequence's newest known token; a chain has parents -1, 0, 1, 2, ... The

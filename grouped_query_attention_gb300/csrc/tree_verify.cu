@@ -13,7 +13,12 @@
 //
 // The token has to be exact, so the sums may not move the place: values and sums
 // are pairs of floats (48 bits; the difference of two floats is exact), as 64-bit
-// arithmetic runs at 1/64 of the rate here.
+// arithmetic runs at 1/64 of the rate here. a p - b q gives some of those bits away
+// to the difference; a node where that comes to more than 8 (close drafts, turned
+// down one behind the other) is worked out anew by the definition's own steps, from
+// the sums of all rounds. It costs the passes once more and a step a round in
+// each, at few nodes (a target certain of a token, nine drafts turned down; drafts
+// with logits 0.7 off stay below 5 bits for 12 rounds).
 //
 // What bounds it: the steps one behind the other. A pass over a row is loads, two
 // dozen operations a pair of probabilities, a cluster barrier; every token turned
@@ -87,11 +92,16 @@ __device__ __forceinline__ float prob(const void* base, long long i) {
   return proper(static_cast<const float*>(base)[i]);
 }
 
-// What is left of a row behind `round` tokens turned down: max(a p - b q, 0), or p without the tokens of Ctl::gone.
+// What is left of a row behind `round` tokens turned down: max(a p - b q, 0), or by the definition's own steps, the
+// sums of which are in Ctl::over (fine); without draft probabilities p without the tokens of Ctl::gone.
 struct Left {
-  int node, round, turned;
+  int node, round, turned, fine;
   Pair a, b;
 };
+// a p - b q loses log2(a) bits to the difference, a = 1 / (Z_1 .. Z_k-1), and as many as the sum Z_k lies below 1. Where
+// both come to more than 8 the definition's own steps take over: they divide every element by the sum of those very
+// elements, so that what the row leaves, however little of it, goes on with its bits.
+constexpr float kCoarse = 0x1p-8f;
 
 template <bool HALF>
 struct Row {
@@ -150,6 +160,7 @@ struct Ctl {
   float p[kTreeNodes], q[kTreeNodes], u[kTreeNodes];   // of the node's token in its parent's rows; its uniform
   int path[kTreeNodes];
   int gone[kTreeNodes];              // tokens turned down at the current node
+  Pair over[kTreeNodes];             // 1 / Z of every round there (Left::fine); 0: nothing was left
   Pair sums[2][kVMaxWarps];          // of every warp of the cluster, two passes in turn
   Left left;
   int command, path_len;
@@ -180,6 +191,17 @@ __device__ __forceinline__ Pair left_of(float p, float q, Pair a, Pair b) {
   return __fadd_rn(d.hi, d.lo) > 0.f ? d : Pair{0.f, 0.f};
 }
 
+// ... by the definition's steps, r <- max(r / Z - q, 0).
+__device__ __noinline__ Pair left_fine(float p, float q, const Pair* over, int round) {
+  Pair r = two_sum(p, -q);
+  for (int j = 0; j + 1 < round && r.hi > 0.f; ++j) {
+    const Pair t = mul(r, over[j]);
+    r = two_sum(t.hi, -q);
+    r = two_sum(r.hi, __fadd_rn(r.lo, t.lo));
+  }
+  return r.hi > 0.f ? r : Pair{0.f, 0.f};
+}
+
 // ... of group k.
 // (Not inlined, like the searches below: a call runs each place once, from cold instruction memory.)
 template <bool HALF>
@@ -205,6 +227,15 @@ __device__ __noinline__ void left_of4(const Row<HALF>& row, typename Row<HALF>::
     r[e] = left_of(pv[e], qv[e], f.a, f.b);
     r[e] = quick(r[e].hi, r[e].lo);
   }
+}
+// ... by the definition's steps. (On its own: few calls come here, and the one above stays without calls.)
+template <bool HALF>
+__device__ __noinline__ void left_fine4(const Row<HALF>& row, typename Row<HALF>::Loaded in, const Left& f, const Ctl& c, int k,
+                                        Pair* r) {
+  const float4 p4 = row.four(row.p, in.p, k), q4 = row.four(row.q, in.q, k);
+  const float pv[4] = {p4.x, p4.y, p4.z, p4.w}, qv[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll 1
+  for (int e = 0; e < 4; ++e) r[e] = left_fine(pv[e], qv[e], c.over, f.round);
 }
 
 // Sum of what is left of groups g0 + lane, + 32, .. within [first, k1), in four
@@ -240,6 +271,18 @@ __device__ __forceinline__ void sum_run(const Row<HALF>& row, const Left& f, int
       }
     }
   }
+}
+
+// ... of groups g0 + lane, + 32, .. below k1 one by one, the row's ends among them (Left::fine).
+template <bool HALF>
+__device__ __noinline__ Pair sum_fine(const Row<HALF>& row, const Left& f, const Ctl& c, int g0, int k1) {
+  Pair s = {0.f, 0.f};
+  for (int k = g0 + (threadIdx.x & 31); k < k1; k += 32) {
+    Pair r[4];
+    left_fine4<HALF>(row, row.load(k), f, c, k, r);
+    s = add(s, add(add(r[0], r[1]), add(r[2], r[3])));
+  }
+  return s;
 }
 
 __device__ __forceinline__ Pair warp_sum(Pair s) {
@@ -316,10 +359,11 @@ tree_verify_kernel(const VerifyParams p) {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // every CTA has begun: its memory may be written
 
   const int warps = ranks * kVWarps;
-  // Warp 0's state: what is left at the path's last node, its sum z, the node tested last.
+  // Warp 0's state: what is left at the path's last node, its sum z, the node tested last. (What does not fit beside a
+  // pass's registers is kept in shared memory: a, b of Left and the sums of Ctl::over.)
   int node = 0, round = 0, turned_down = 0;
+  int fine = 0;                             // Left::fine: the rounds began anew, up to this one
   const Pair one = {1.f, 0.f};
-  Pair fa = one, fb = {0.f, 0.f};           // what is left: fa p - fb q
   Pair z = one, whole = {-1.f, 0.f};        // whole: sum of the node's row (no draft probabilities), once known
   int last = 0, len = 1, pass = 0, spare;
   bool summed = false;
@@ -328,60 +372,82 @@ tree_verify_kernel(const VerifyParams p) {
     // ---- tests, until a sum is needed or no child is left
     if (warp == 0) {
       int command = kDraw;
-      while (true) {
-        int next = n;   // the next child of `node` behind node `last`
-        for (int i = last + 1; i < n; i += 32) {
-          const unsigned m = __ballot_sync(0xffffffffu, i + lane < n && c.parent[i + lane] == node);
-          if (m) {
-            next = i + __ffs(m) - 1;
+      bool again = false;        // behind a sum of the rounds that began anew: the next of them
+      if (summed && p.draft) {   // (z is from the last pass)
+        if (!fine && round > 1 && !(z.hi >= kCoarse * c.left.a.hi)) {   // (p - q of the first round is exact)
+          fine = round;
+          round = 1;
+          summed = false;
+          command = kSum;
+        } else {
+          again = round < fine;
+        }
+      }
+      while (command == kDraw) {
+        float pv = 0.f;
+        bool dup = false;
+        if (!again) {
+          int next = n;   // the next child of `node` behind node `last`
+          for (int i = last + 1; i < n; i += 32) {
+            const unsigned m = __ballot_sync(0xffffffffu, i + lane < n && c.parent[i + lane] == node);
+            if (m) {
+              next = i + __ffs(m) - 1;
+              break;
+            }
+          }
+          if (next >= n) break;
+          const float qv = c.q[next];
+          pv = c.p[next];
+          Pair r = {pv, 0.f};
+          if (round > 0) {
+            if (p.draft) {
+              if (fine) r = left_fine(pv, qv, c.over, round);
+              else r = round == 1 ? two_sum(pv, -qv) : add(mul(c.left.a, {pv, 0.f}), neg(mul(c.left.b, {qv, 0.f})));
+            } else {
+              for (int x = lane; x < turned_down; x += 32) dup |= c.gone[x] == c.token[next];
+              dup = __any_sync(0xffffffffu, dup);
+              if (dup) r = {0.f, 0.f};
+            }
+          }
+          if (z.hi > 0.f && above(r, mul(product(c.u[next], qv), z))) {
+            node = next;
+            round = turned_down = 0;
+            z = one;
+            whole.hi = -1.f;
+            if (lane == 0) c.path[len] = next;
+            ++len;
+            last = next;
+            summed = false;
+            fine = 0;
+            continue;
+          }
+          if (!p.draft && whole.hi < 0.f) {   // (the test stands: come back with the sum)
+            command = kWhole;
             break;
           }
-        }
-        if (next >= n) break;
-        const float pv = c.p[next], qv = c.q[next];
-        Pair r = {pv, 0.f};
-        bool dup = false;
-        if (round > 0) {
-          if (p.draft) {
-            r = round == 1 ? two_sum(pv, -qv) : add(mul(fa, {pv, 0.f}), neg(mul(fb, {qv, 0.f})));
-          } else {
-            for (int x = lane; x < turned_down; x += 32) dup |= c.gone[x] == c.token[next];
-            dup = __any_sync(0xffffffffu, dup);
-            if (dup) r = {0.f, 0.f};
-          }
-        }
-        if (z.hi > 0.f && above(r, mul(product(c.u[next], qv), z))) {
-          node = next;
-          round = turned_down = 0;
-          fa = z = one;
-          fb = {0.f, 0.f};
-          whole.hi = -1.f;
-          if (lane == 0) c.path[len] = next;
-          ++len;
           last = next;
-          summed = false;
-          continue;
-        }
-        if (!p.draft && whole.hi < 0.f) {   // (the test stands: come back with the sum)
-          command = kWhole;
-          break;
         }
         // turned down: r <- max(r / z - q, 0), or r without the token
-        last = next;
-        ++round;
         summed = false;
         if (p.draft) {
-          if (round == 1) {
-            fb = one;
-          } else if (z.hi > 0.f) {   // (nothing left: it stays so)
-            const Pair over = reciprocal(z);
-            fa = mul(fa, over);
-            fb = add(mul(fb, over), one);
+          if (lane == 0) {
+            if (round == 0) {
+              c.left.a = c.left.b = one;
+            } else if (fine) {
+              c.over[round - 1] = z.hi > 0.f ? reciprocal(z) : Pair{0.f, 0.f};
+            } else if (z.hi > 0.f) {   // (nothing left: it stays so)
+              const Pair over = reciprocal(z);
+              c.left.a = mul(c.left.a, over);
+              c.left.b = add(mul(c.left.b, over), one);
+            }
           }
+          __syncwarp();
+          ++round;
           command = kSum;
           break;
         }
-        if (lane == 0) c.gone[turned_down] = c.token[next];
+        ++round;
+        if (lane == 0) c.gone[turned_down] = c.token[last];
         __syncwarp();
         ++turned_down;
         z = turned_down == 1 ? add(whole, {-pv, 0.f}) : dup ? z : add(z, {-pv, 0.f});
@@ -391,11 +457,14 @@ tree_verify_kernel(const VerifyParams p) {
         }
       }
       if (command == kDraw && summed && !(z.hi > 0.f)) {   // nothing left: the target's own row
-        round = turned_down = 0;
+        round = turned_down = fine = 0;
         summed = false;
       }
       if (lane == 0) {
-        c.left = {node, round, turned_down, fa, fb};
+        c.left.node = node;
+        c.left.round = round;
+        c.left.turned = turned_down;
+        c.left.fine = fine > 0;
         c.path_len = len;
         c.command = command | (summed ? kSummed : 0);
       }
@@ -413,7 +482,9 @@ tree_verify_kernel(const VerifyParams p) {
       // ---- the sum of what is left, and every warp's part of it
       Pair s[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
       const int k0 = max(g0, row.first()), k1 = min(g0 + run, row.end());
-      if (f.round > 0 && row.q) {
+      if (f.fine) {
+        s[0] = sum_fine<HALF>(row, f, c, g0, min(g0 + run, groups));
+      } else if (f.round > 0 && row.q) {
         sum_run<HALF, true>(row, f, g0, k0, k1, 0, 5, s);
       } else {
         // Groups of this lane with a token turned down, and those that share a bit of the mask with one: one by one.
@@ -435,7 +506,7 @@ tree_verify_kernel(const VerifyParams p) {
       }
       // Elements of the groups that reach over the row's ends, a lane each: those before the first whole group (lanes
       // 0..), those behind the last (16..).
-      if (g0 == 0 || (g0 < groups && g0 + run >= groups)) {
+      if (!f.fine && (g0 == 0 || (g0 < groups && g0 + run >= groups))) {
         const long long head = min((long long)((4 - row.off) & 3), p.V);
         const long long tail = max(4LL * row.end() - row.off, head);
         const long long v = lane < 16 ? lane : tail + lane - 16;
@@ -519,7 +590,8 @@ tree_verify_kernel(const VerifyParams p) {
       Pair sum = {0.f, 0.f};
       for (int k = b0 + lane; k < b1; k += 32) {
         Pair r[4];
-        left_of4<HALF>(row, row.load(k), f, c.gone, turned, k, r);
+        if (f.fine) left_fine4<HALF>(row, row.load(k), f, c, k, r);
+        else left_of4<HALF>(row, row.load(k), f, c.gone, turned, k, r);
         sum = add(sum, add(add(r[0], r[1]), add(r[2], r[3])));
       }
       sum = warp_sum(sum);
@@ -536,7 +608,10 @@ tree_verify_kernel(const VerifyParams p) {
         for (int k0 = b0; k0 < b1 && token < 0; k0 += 32) {
           const int k = k0 + lane;
           Pair r[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-          if (k < b1) left_of4<HALF>(row, row.load(k), f, c.gone, turned, k, r);
+          if (k < b1) {
+            if (f.fine) left_fine4<HALF>(row, row.load(k), f, c, k, r);
+            else left_of4<HALF>(row, row.load(k), f, c.gone, turned, k, r);
+          }
           Pair upto = before;
           const int hit = find_lane(add(add(r[0], r[1]), add(r[2], r[3])), edge, &upto, &spare);
           const int pick = hit >= 0 ? hit : spare;

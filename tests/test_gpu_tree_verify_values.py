@@ -1,0 +1,69 @@
+"""Verification of drafted tokens where the numbers are hard. Paths and tokens are equal to those of the 64-bit
+definition (oracle/tree.py)."""
+
+import numpy as np
+import pytest
+
+from oracle import tree as ot
+from test_gpu_tree import NP, make_verify, run_verify, same
+
+pytestmark = pytest.mark.gpu
+
+
+def star(tokens, rows, draft, u, us, dtype=np.float32):
+    """A root with children of these tokens; the root's rows (B, V) or (V,), every other node's uniform."""
+    tokens = np.atleast_2d(np.asarray(tokens, np.int32))
+    B, S = tokens.shape[0], tokens.shape[1] + 1
+
+    def spread(row):
+        row = np.broadcast_to(np.asarray(row, np.float64), (B, np.asarray(row).shape[-1]))
+        x = np.full((B, S, row.shape[-1]), 1.0 / row.shape[-1])
+        x[:, 0] = row
+        return x.astype(dtype)
+
+    return dict(tokens=np.concatenate([np.zeros((B, 1), np.int32), tokens], 1),
+                parents=np.array([[-1] + [0] * (S - 1)], np.int32), target_probs=spread(rows),
+                draft_probs=None if draft is None else spread(draft),
+                accept_uniforms=np.broadcast_to(np.float32(u), (B, S)).copy(),
+                sample_uniforms=np.broadcast_to(np.float32(us), (B,)).copy(), new_lens=None)
+
+
+# ------------------------------------------------------------------ many drafts turned down
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("V", [3000, 40001])
+@pytest.mark.parametrize("qt,refused", [(0.99, 2), (0.99, 9), (0.9, 16), (0.6, 45), (0.97, 300)])
+def test_a_certain_target_behind_many_refusals(qt, refused, V, dtype):
+    """The target is certain of one token, the draft almost: what is left is that token after every refusal, and its
+    child, the last one, passes. Without that child it is drawn."""
+    t, rng = V // 3, np.random.default_rng(9)
+    p, q = np.zeros(V), rng.random(V)
+    q[t] = 0.0
+    q *= (1.0 - qt) / q.sum()
+    p[t], q[t] = 1.0, qt
+    others = rng.choice(np.delete(np.arange(V), t), refused, replace=V < refused)
+    for children, nodes, token in ((list(others) + [t], 2, None), (others, 1, t)):
+        v = star(children, p, q, 0.5, 0.25, NP[dtype])
+        got = run_verify(v)
+        same(got, ot.verify(**v))
+        assert got[1].tolist() == [nodes] and (token is None or got[2].tolist() == [token])
+
+
+@pytest.mark.parametrize("drafts", [True, False])
+@pytest.mark.parametrize("noise", [0.5, 0.05, 0.005])
+def test_close_drafts_turned_down_by_force(noise, drafts):
+    """Uniforms near 1 turn down drafts of rows that hardly differ: remainders of 0.2 to 0.002 of the rows, one behind
+    the other."""
+    for seed in range(4):
+        v = make_verify(4, 12, 2003, drafts=drafts, kind="star", noise=noise, std=2.0, seed=seed)
+        v["accept_uniforms"][:] = 1.0 - 2.0 ** -24 if seed % 2 else 1.0
+        same(run_verify(v), ot.verify(**v))
+
+
+def test_refusals_on_the_way_down():
+    """Nodes of a path that turn several close drafts down before one passes, then the next node anew."""
+    rng = np.random.default_rng(12)
+    for seed in range(6):
+        v = make_verify(3, 60, 1009, kind="tree", noise=0.02, std=2.0, seed=seed)
+        v["accept_uniforms"][:] = np.where(rng.random((3, 60)) < 0.7, 1.0, rng.random((3, 60)))
+        same(run_verify(v), ot.verify(**v))

@@ -364,7 +364,7 @@ tree_verify_kernel(const VerifyParams p) {
   int node = 0, round = 0, turned_down = 0;
   int fine = 0;                             // Left::fine: the rounds began anew, up to this one
   const Pair one = {1.f, 0.f};
-  Pair z = one, whole = {-1.f, 0.f};        // whole: sum of the node's row (no draft probabilities), once known
+  Pair z = one, whole = {-1.f, 0.f};        // whole (no draft probabilities): the node's last sum that was added up
   int last = 0, len = 1, pass = 0, spare;
   bool summed = false;
   if (tid == 0) c.path[0] = 0;
@@ -451,7 +451,7 @@ tree_verify_kernel(const VerifyParams p) {
         __syncwarp();
         ++turned_down;
         z = turned_down == 1 ? add(whole, {-pv, 0.f}) : dup ? z : add(z, {-pv, 0.f});
-        if (!(z.hi > whole.hi * 0x1p-16f)) {   // too little of the sum for a difference to hold: add it up
+        if (!(z.hi > whole.hi * kCoarse)) {   // too little of that sum for a difference to hold: add it up
           command = kSum;
           break;
         }
@@ -529,9 +529,8 @@ tree_verify_kernel(const VerifyParams p) {
         Pair w = {0.f, 0.f};
         for (int x = lane; x < warps; x += 32) w = add(w, c.sums[pass & 1][x]);
         const Pair sum = warp_sum(w);
-        if (command == kWhole) {
-          whole = sum;
-        } else {
+        whole = sum;
+        if (command != kWhole) {
           z = sum;
           summed = true;
         }

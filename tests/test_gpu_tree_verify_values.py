@@ -1,5 +1,8 @@
 """Verification of drafted tokens where the numbers are hard. Paths and tokens are equal to those of the 64-bit
-definition (oracle/tree.py)."""
+definition (oracle/tree.py); where a border is placed on purpose, it stands further from the numbers that meet it than
+the 64-bit sums round (math.fsum and one product: 2^-52)."""
+
+import math
 
 import numpy as np
 import pytest
@@ -67,3 +70,34 @@ def test_refusals_on_the_way_down():
         v = make_verify(3, 60, 1009, kind="tree", noise=0.02, std=2.0, seed=seed)
         v["accept_uniforms"][:] = np.where(rng.random((3, 60)) < 0.7, 1.0, rng.random((3, 60)))
         same(run_verify(v), ot.verify(**v))
+
+
+# ------------------------------------------------------------------ the last bits
+
+def bordered(rest, least, most, rng):
+    """A uniform u and a float x: u (sum(rest) + x) lies a relative distance in [least, most] below x, or above it."""
+    base = math.fsum(rest)
+    while True:
+        u = np.float32(rng.uniform(0.2, 0.8))
+        x = np.float32(float(u) * base / (1.0 - float(u)))   # u (base + x) = x, but for its rounding
+        for c in (x, np.nextafter(x, np.float32(np.inf)), np.nextafter(x, np.float32(0))):
+            edge = float(u) * (base + float(c))
+            if least <= abs(float(c) - edge) / edge <= most:
+                return u, c
+
+
+def test_sums_of_certain_drafts_keep_their_bits():
+    """A first token of almost everything is turned down; the sum of the rest, 2^-15 of the row, meets a token's
+    probability at 2^-38 to 2^-36 of it."""
+    rng = np.random.default_rng(21)
+    B, V = 64, 900
+    v = star(np.tile([0, 1], (B, 1)), np.zeros((B, V)), None, 1.0, 0.5)
+    for b in range(B):
+        rest = (rng.random(V - 2) * 2.0 ** -25).astype(np.float32)
+        u, x = bordered(rest.astype(np.float64), 2.0 ** -38, 2.0 ** -36, rng)
+        v["target_probs"][b, 0, 1], v["target_probs"][b, 0, 2:] = x, rest
+        v["target_probs"][b, 0, 0] = 1.0 - 2.0 ** -15
+        v["accept_uniforms"][b, 2] = u
+    want = ot.verify(**v)
+    assert 10 < (want[1] == 2).sum() < 54
+    same(run_verify(v), want)

@@ -270,6 +270,9 @@ __device__ __forceinline__ void sum_run(const Row<HALF>& row, const Left& f, int
         else gather(s[e], {p1, 0.f});
       }
     }
+    // (A low part that grew with the run would round ever more of itself away.)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] = quick(s[e].hi, s[e].lo);
   }
 }
 

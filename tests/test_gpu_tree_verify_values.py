@@ -6,9 +6,11 @@ import math
 
 import numpy as np
 import pytest
+import torch
 
+from grouped_query_attention_gb300 import GroupQueryAttention
 from oracle import tree as ot
-from test_gpu_tree import NP, make_verify, run_verify, same
+from test_gpu_tree import NP, dev, make_verify, run_verify, same
 
 pytestmark = pytest.mark.gpu
 
@@ -74,7 +76,7 @@ def test_refusals_on_the_way_down():
 
 # ------------------------------------------------------------------ the last bits
 
-def bordered(rest, least, most, rng):
+def bordered(rest, least, most, rng, below):
     """A uniform u and a float x: u (sum(rest) + x) lies a relative distance in [least, most] below x, or above it."""
     base = math.fsum(rest)
     while True:
@@ -82,7 +84,7 @@ def bordered(rest, least, most, rng):
         x = np.float32(float(u) * base / (1.0 - float(u)))   # u (base + x) = x, but for its rounding
         for c in (x, np.nextafter(x, np.float32(np.inf)), np.nextafter(x, np.float32(0))):
             edge = float(u) * (base + float(c))
-            if least <= abs(float(c) - edge) / edge <= most:
+            if least <= (float(c) - edge) / edge * (1 if below else -1) <= most:
                 return u, c
 
 
@@ -94,10 +96,33 @@ def test_sums_of_certain_drafts_keep_their_bits():
     v = star(np.tile([0, 1], (B, 1)), np.zeros((B, V)), None, 1.0, 0.5)
     for b in range(B):
         rest = (rng.random(V - 2) * 2.0 ** -25).astype(np.float32)
-        u, x = bordered(rest.astype(np.float64), 2.0 ** -38, 2.0 ** -36, rng)
+        u, x = bordered(rest.astype(np.float64), 2.0 ** -38, 2.0 ** -36, rng, b % 2)
         v["target_probs"][b, 0, 1], v["target_probs"][b, 0, 2:] = x, rest
         v["target_probs"][b, 0, 0] = 1.0 - 2.0 ** -15
         v["accept_uniforms"][b, 2] = u
     want = ot.verify(**v)
-    assert 10 < (want[1] == 2).sum() < 54
+    assert want[1].tolist() == [1, 2] * (B // 2)
     same(run_verify(v), want)
+
+
+def test_sums_of_large_vocabularies_keep_their_bits():
+    """A CTA a sequence (153 of them, 149 empty) and 2^20 tokens: 512 numbers a chain of the sum, two of about 1 and then
+    510 of 2^-26 and a bit that a float sum of them near 2^-17 cannot hold (each loses 2^-42, all the same way: 2^-35 of
+    the whole). The sum meets a token's probability at 2^-38 to 2^-36 of it."""
+    rng = np.random.default_rng(22)
+    B, V, live = 153, 1 << 20, 8
+    rows = np.full((live, 3, V), 2.0 ** -26 * (1 + 0.49 * 2.0 ** -15), np.float32)
+    u = np.ones((B, 3), np.float32)
+    for b in range(live):
+        rest = rows[b, 0].reshape(16, -1)              # a warp's run
+        rest[:, :256] = 0.75 + 0.25 * rng.random((16, 256))
+        rows[b, 0, [0, V - 1]] = 0.0                   # token 0 is turned down first, so that the sum counts
+        u[b, 2], rows[b, 0, V - 1] = bordered(rows[b, 0].astype(np.float64), 2.0 ** -38, 2.0 ** -36, rng, b % 2)
+    p = torch.zeros((B, 3, V), device="cuda")
+    p[:live] = dev(rows)
+    tokens, par = np.tile(np.array([[0, 0, V - 1]], np.int32), (B, 1)), np.array([[-1, 0, 0]], np.int32)
+    us, news = np.full(B, 0.001, np.float32), np.where(np.arange(B) < live, 3, 0).astype(np.int32)
+    got = GroupQueryAttention(1, 1).tree_verify(dev(tokens), dev(par), p, dev(u), dev(us), new_lens=dev(news))
+    want = ot.verify(tokens[:live], par, rows, u[:live], us[:live])
+    assert want[1].tolist() == [1, 2] * (live // 2)
+    same([x[:live].cpu().numpy() for x in got], want)

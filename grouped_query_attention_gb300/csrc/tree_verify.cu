@@ -102,6 +102,10 @@ struct Left {
 // both come to more than 8 the definition's own steps take over: they divide every element by the sum of those very
 // elements, so that what the row leaves, however little of it, goes on with its bits.
 constexpr float kCoarse = 0x1p-8f;
+// Products of numbers near the smallest float have no room for their low parts. All sums are of values times kUp: the
+// smallest float is 2^-93 there, and a row's sum far below the largest. So are fine values.
+constexpr float kUp = 0x1p56f;
+__device__ __forceinline__ Pair raised(Pair a) { return {a.hi * kUp, a.lo * kUp}; }
 
 template <bool HALF>
 struct Row {
@@ -160,7 +164,7 @@ struct Ctl {
   float p[kTreeNodes], q[kTreeNodes], u[kTreeNodes];   // of the node's token in its parent's rows; its uniform
   int path[kTreeNodes];
   int gone[kTreeNodes];              // tokens turned down at the current node
-  Pair over[kTreeNodes];             // 1 / Z of every round there (Left::fine); 0: nothing was left
+  Pair over[kTreeNodes];             // 1 / (Z kUp) of every round there (Left::fine); 0: nothing was left
   Pair sums[2][kVMaxWarps];          // of every warp of the cluster, two passes in turn
   Left left;
   int command, path_len;
@@ -191,11 +195,11 @@ __device__ __forceinline__ Pair left_of(float p, float q, Pair a, Pair b) {
   return __fadd_rn(d.hi, d.lo) > 0.f ? d : Pair{0.f, 0.f};
 }
 
-// ... by the definition's steps, r <- max(r / Z - q, 0).
+// ... by the definition's steps, r <- max(r / Z - q, 0), of a p and a q times kUp.
 __device__ __noinline__ Pair left_fine(float p, float q, const Pair* over, int round) {
   Pair r = two_sum(p, -q);
   for (int j = 0; j + 1 < round && r.hi > 0.f; ++j) {
-    const Pair t = mul(r, over[j]);
+    const Pair t = mul(raised(r), over[j]);
     r = two_sum(t.hi, -q);
     r = two_sum(r.hi, __fadd_rn(r.lo, t.lo));
   }
@@ -235,7 +239,7 @@ __device__ __noinline__ void left_fine4(const Row<HALF>& row, typename Row<HALF>
   const float4 p4 = row.four(row.p, in.p, k), q4 = row.four(row.q, in.q, k);
   const float pv[4] = {p4.x, p4.y, p4.z, p4.w}, qv[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll 1
-  for (int e = 0; e < 4; ++e) r[e] = left_fine(pv[e], qv[e], c.over, f.round);
+  for (int e = 0; e < 4; ++e) r[e] = left_fine(pv[e] * kUp, qv[e] * kUp, c.over, f.round);
 }
 
 // Sum of what is left of groups g0 + lane, + 32, .. within [first, k1), in four
@@ -367,7 +371,7 @@ tree_verify_kernel(const VerifyParams p) {
   int node = 0, round = 0, turned_down = 0;
   int fine = 0;                             // Left::fine: the rounds began anew, up to this one
   const Pair one = {1.f, 0.f};
-  Pair z = one, whole = {-1.f, 0.f};        // whole (no draft probabilities): the node's last sum that was added up
+  Pair z = raised(one), whole = {-1.f, 0.f};        // whole (no draft probabilities): the node's last sum that was added up
   int last = 0, len = 1, pass = 0, spare;
   bool summed = false;
   if (tid == 0) c.path[0] = 0;
@@ -377,7 +381,7 @@ tree_verify_kernel(const VerifyParams p) {
       int command = kDraw;
       bool again = false;        // behind a sum of the rounds that began anew: the next of them
       if (summed && p.draft) {   // (z is from the last pass)
-        if (!fine && round > 1 && !(z.hi >= kCoarse * c.left.a.hi)) {   // (p - q of the first round is exact)
+        if (!fine && round > 1 && !(z.hi >= kCoarse * kUp * c.left.a.hi)) {   // (p - q of the first round is exact)
           fine = round;
           round = 1;
           summed = false;
@@ -399,8 +403,8 @@ tree_verify_kernel(const VerifyParams p) {
             }
           }
           if (next >= n) break;
-          const float qv = c.q[next];
-          pv = c.p[next];
+          const float qv = c.q[next] * kUp;
+          pv = c.p[next] * kUp;
           Pair r = {pv, 0.f};
           if (round > 0) {
             if (p.draft) {
@@ -412,10 +416,10 @@ tree_verify_kernel(const VerifyParams p) {
               if (dup) r = {0.f, 0.f};
             }
           }
-          if (z.hi > 0.f && above(r, mul(product(c.u[next], qv), z))) {
+          if (z.hi > 0.f && above(raised(r), mul(product(c.u[next], qv), z))) {
             node = next;
             round = turned_down = 0;
-            z = one;
+            z = raised(one);
             whole.hi = -1.f;
             if (lane == 0) c.path[len] = next;
             ++len;
@@ -439,7 +443,7 @@ tree_verify_kernel(const VerifyParams p) {
             } else if (fine) {
               c.over[round - 1] = z.hi > 0.f ? reciprocal(z) : Pair{0.f, 0.f};
             } else if (z.hi > 0.f) {   // (nothing left: it stays so)
-              const Pair over = reciprocal(z);
+              const Pair over = raised(reciprocal(z));
               c.left.a = mul(c.left.a, over);
               c.left.b = add(mul(c.left.b, over), one);
             }
@@ -524,7 +528,8 @@ tree_verify_kernel(const VerifyParams p) {
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[e] = quick(s[e].hi, s[e].lo);
-      const Pair t = warp_sum(add(add(s[0], s[1]), add(s[2], s[3])));
+      Pair t = warp_sum(add(add(s[0], s[1]), add(s[2], s[3])));
+      if (!f.fine) t = raised(t);
       Pair* dst = &c.sums[pass & 1][rank * kVWarps + warp];
       if (lane < ranks) *cluster.map_shared_rank(dst, lane) = t;
       cluster.sync();   // (two sets: the next pass writes the other one, and its barrier comes before this one's turn)
@@ -597,7 +602,7 @@ tree_verify_kernel(const VerifyParams p) {
         sum = add(sum, add(add(r[0], r[1]), add(r[2], r[3])));
       }
       sum = warp_sum(sum);
-      if (lane == 0) c.part[warp] = sum;
+      if (lane == 0) c.part[warp] = f.fine ? sum : raised(sum);
       __syncthreads();
       Pair before = c.before, edge = c.edge;
       int mine = find_lane(lane < kVWarps ? c.part[lane] : Pair{0.f, 0.f}, edge, &before, &spare);
@@ -613,6 +618,10 @@ tree_verify_kernel(const VerifyParams p) {
           if (k < b1) {
             if (f.fine) left_fine4<HALF>(row, row.load(k), f, c, k, r);
             else left_of4<HALF>(row, row.load(k), f, c.gone, turned, k, r);
+          }
+          if (!f.fine) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r[e] = raised(r[e]);
           }
           Pair upto = before;
           const int hit = find_lane(add(add(r[0], r[1]), add(r[2], r[3])), edge, &upto, &spare);

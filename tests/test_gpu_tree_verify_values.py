@@ -74,6 +74,53 @@ def test_refusals_on_the_way_down():
         same(run_verify(v), ot.verify(**v))
 
 
+# ------------------------------------------------------------------ next to nothing
+
+TINY = 2.0 ** -149
+
+
+def test_draws_from_rows_of_the_smallest_floats():
+    """Rows of a few smallest floats: the place u sum is between two of their multiples."""
+    row = np.zeros(700)
+    row[[5, 300, 301, 699]] = np.array([3, 5, 7, 1]) * TINY
+    us = np.array([0.1, 0.19, 0.2, 0.21, 0.5, 0.53, 0.5333, 0.54, 0.9, 0.93, 0.935, 0.96], np.float32)
+    for draft in (None, np.full(700, 1.0 / 700)):
+        v = star(np.full((12, 1), 7), row, draft, 1.0, us)
+        if draft is not None:
+            v["new_lens"] = np.full(12, 1, np.int32)     # the draw alone: round 0
+        want = ot.verify(**v)
+        assert set(want[2].tolist()) == {5, 300, 301, 699}
+        same(run_verify(v), want)
+
+
+def test_tests_of_the_smallest_floats():
+    """u q(x) < r(x) where both are a few smallest floats."""
+    u = np.linspace(0.05, 0.95, 19, dtype=np.float32)
+    for pu, qu in ((1, 1), (1, 2), (2, 3), (5, 7), (1, 3)):
+        p, q = np.full(600, 1.0 / 600), np.full(600, 1.0 / 600)
+        p[17], q[17] = pu * TINY, qu * TINY
+        v = star(np.full((19, 1), 17), p, q, 0.0, 0.5)
+        v["accept_uniforms"][:, 1] = u
+        want = ot.verify(**v)
+        assert (want[1] == 2).tolist() == [float(x) * qu < pu for x in u]
+        same(run_verify(v), want)
+
+
+@pytest.mark.parametrize("tiny", [1e-38, 1e-41, 2.0 ** -149, 1e-30, 1e-20])
+def test_remainders_of_almost_nothing(tiny):
+    """Target and draft agree but for tokens of almost no probability: what a refusal leaves is those."""
+    V = 5000
+    p, q = np.zeros(V), np.zeros(V)
+    p[100] = q[100] = 1.0
+    p[[7, 2000, 4999]] = np.array([2.0, 5.0, 3.0]) * tiny
+    q[[7, 3000]] = np.array([1.0, 4.0]) * tiny
+    for children in ([3000], [3000, 100], [3000, 100, 7, 2000], [3000, 3000, 3000, 4999], [3000, 4999, 2000, 7, 100]):
+        for u in (0.05, 0.3, 0.7, 1.0):
+            us = np.array([0.05, 0.15, 0.5, 0.8], np.float32)
+            v = star(np.tile(children, (4, 1)), p, q, u, us)
+            same(run_verify(v), ot.verify(**v))
+
+
 # ------------------------------------------------------------------ the last bits
 
 def bordered(rest, least, most, rng, below):

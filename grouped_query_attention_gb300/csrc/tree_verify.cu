@@ -83,9 +83,9 @@ __device__ __forceinline__ Pair shfl_up(Pair a, int o) {
 // a > b
 __device__ __forceinline__ bool above(Pair a, Pair b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
 
-// Probabilities as the definition reads them.
-// (the bits of negative, infinite and NaN values lie above the finite ones')
-__device__ __forceinline__ float proper(float p) { return __float_as_uint(p) < 0x7f800000u ? p : 0.f; }
+// Probabilities as the definition reads them: numbers from 2^15 on are none, so that no sum or product of theirs overflows.
+// (The bits of negative, infinite and NaN values lie above those of the positive ones.)
+__device__ __forceinline__ float proper(float p) { return __float_as_uint(p) < 0x47000000u ? p : 0.f; }
 template <bool HALF>
 __device__ __forceinline__ float prob(const void* base, long long i) {
   if constexpr (HALF) return proper(__half2float(static_cast<const __half*>(base)[i]));

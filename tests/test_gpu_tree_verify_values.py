@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 import torch
 
-from grouped_query_attention_gb300 import GroupQueryAttention
+from grouped_query_attention_gb300 import GroupQueryAttention, capi
 from oracle import tree as ot
 from test_gpu_tree import NP, dev, make_verify, run_verify, same
 
@@ -173,3 +173,22 @@ def test_sums_of_large_vocabularies_keep_their_bits():
     want = ot.verify(tokens[:live], par, rows, u[:live], us[:live])
     assert want[1].tolist() == [1, 2] * (live // 2)
     same([x[:live].cpu().numpy() for x in got], want)
+
+
+# ------------------------------------------------------------------ numbers that are no probabilities
+
+@pytest.mark.parametrize("drafts", [True, False])
+def test_numbers_too_large_for_a_probability(drafts):
+    """Numbers from 2^15 on count as none, whatever their sum; just below it they count. A row without another is reported."""
+    rng = np.random.default_rng(31)
+    p = rng.random((6, 3000)) / 3000
+    p[:4, [3, 200, 1700, 2999]] = np.array([[2e38], [3e4], [2.0 ** 15], [1e30]])
+    p[4] = 0.0
+    p[4, [3, 200]] = 2e38
+    q = np.full(3000, 1.0 / 3000)
+    q[[3, 77]] = 3e38
+    v = star(np.tile([3, 77, 1000, 2999], (6, 1)), p, q if drafts else None, 1.0, [0.05, 0.1, 0.5, 0.7, 0.7, 0.9])
+    op = GroupQueryAttention(1, 1)
+    got = run_verify(v, op)
+    same(got, ot.verify(**v))
+    assert got[2].min() == got[2][4] == -1 and op.block_status() == capi.GQA_DEVICE_BAD_PROBS

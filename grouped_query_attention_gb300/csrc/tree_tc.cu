@@ -531,7 +531,7 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk, cons
         mt *= mul;
         if constexpr (CAP) {
           ua *= mul;
-          if (mt > kNegBig) mt = cap_far(mt, c2);   // a reference: any rounding serves
+          if (mt > kNegBig) mt = cap_far(mt, c2);   // a reference: any rounding serves (softcap_fits)
         }
         // ---- rescale O when a maximum outgrew its reference (P V of the unit before is over: S came behind it)
         const bool grow = mt > m_run + kLazy;

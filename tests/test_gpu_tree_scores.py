@@ -1,0 +1,44 @@
+"""Tree attention on scores and values at the ends of their ranges, against oracle/tree.py.
+
+Tolerances as in test_gpu_tree.py, but for a softcap c: c tanh(s / c) is worked out to 2^-20 of itself (its quotient and
+product, tanh or the fit: 2^-24 and two or three steps of 2^-24 each), whatever c is, which adds 2^-20 of the largest
+|score| to what a score may be off."""
+
+import numpy as np
+import pytest
+
+from test_gpu_tree import CASES, check, make, operator, run_gpu, run_oracle
+
+pytestmark = pytest.mark.gpu
+
+FORMS = {   # as test_gpu_tree.CASES: the tensor-core pipeline with one and two row tiles a piece, the warp MMAs
+    "one_tile": CASES["tile_32"],
+    "two_tiles": ("f16", 1, 40, 8, 2, 64, 900, (877,), None, -1, 0, 0, 0, "tree", 0),
+    "split": ("f16", 1, 11, 4, 2, 128, 3000, (2990,), None, -1, 0, 0, 0, "tree", 0),
+    "mma_h256": CASES["h256"], "mma_f32": CASES["tile_32_f32"], "mma_h256_f32": CASES["h256_f32"],
+}
+
+
+def capped_check(d, softcap):
+    d["softcap"] = softcap
+    out, mag, reach, rk, rv = run_oracle(d)
+    d["softcap"] = float(2.0 * min(softcap, reach.max()))   # tolerance(): 2^-21 of it
+    got = run_gpu(d, operator(dict(d, softcap=softcap)))
+    assert got[3].block_status() == 0
+    check(d, got, (out, mag, reach, rk, rv))
+
+
+@pytest.mark.parametrize("name", list(FORMS))
+@pytest.mark.parametrize("softcap", [1e4, 5e5, 1e6, 3e7, 1e8, 1e10, 1e30])
+def test_softcaps_far_above_the_scores(name, softcap):
+    """c tanh(s / c) is s."""
+    capped_check(make(FORMS[name], seed=3), softcap)
+
+
+@pytest.mark.parametrize("name", list(FORMS))
+@pytest.mark.parametrize("softcap", [1e-3, 1e-10, 1e-38, 1e-45])
+def test_softcaps_far_below_the_scores(name, softcap):
+    """Every score is c, -c or (of a zero product) 0: all visible rows weigh the same."""
+    d = make(FORMS[name], seed=3)
+    d["k"][:, 0] = 0
+    capped_check(d, softcap)

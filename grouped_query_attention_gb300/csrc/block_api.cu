@@ -7,6 +7,7 @@
 
 #include "../../include/gqa.h"
 #include "block_internal.h"
+#include "block_tc.cuh"
 #include "gqa_host.h"
 #include "gqa_internal.h"
 #include "host_checks.h"
@@ -174,11 +175,11 @@ gqa_status plan_block(const gqa_handle* h, const gqa_block_cache* cache, const g
   P.withhold_tile = h->withhold_tile;
 
   const long long rows = S * G;
-  // (The prefill takes row maxima and masks before the scale: a negative one would turn them.)
+  // (The prefill takes row maxima and masks before the scale: a negative one would turn them. Its softcaps have a range.)
   P.tile_rows = G <= 128 ? (int)(128 / G * G) : 0;
   const long long nqb = G <= 128 ? (rows + 2 * P.tile_rows - 1) / (2 * P.tile_rows) : 0;
   const bool grid_ok = nqb <= 65535 && (T + 127) / 128 <= 65535;
-  pl->prefill = H <= 128 && G <= 128 && P.scale > 0.f && rows > 16 && grid_ok && use_prefill(P);
+  pl->prefill = H <= 128 && G <= 128 && P.scale > 0.f && gqa::softcap_fits(P.softcap) && rows > 16 && grid_ok && use_prefill(P);
   pl->part_o = pl->part_ml = pl->stash = pl->lse = pl->o_acc = 0;
   if (pl->prefill) {
     if (P.t_type == gqa::kF32 && T > gqa::kPrefillFlush)

@@ -647,7 +647,7 @@ block_prefill_kernel(const BlockParams p, const __grid_constant__ CUtensorMap tm
       }
       if (kHalves == 2 && !full) tmem_st_wait();
       if constexpr (CAP) {
-        if (mt > kNegBig) mt = cap_far(mt, c2);   // a reference: any rounding serves
+        if (mt > kNegBig) mt = cap_far(mt, c2);   // a reference: any rounding serves (softcap_fits)
       }
       // Lazy rescale: O_q holds P.V up to the last step once that is done.
       const bool grow = mt > m_run + kLazy;

@@ -158,7 +158,7 @@ gqa_status plan_block(const gqa_handle* h, const gqa_block_cache* cache, const g
   // A window that reaches every row hides none; what remains is below 2^30, so the kernels' sums fit 32 bits.
   P.window = a.local_window_size < T ? a.local_window_size : -1;
   P.scale = a.scale != 0.f ? a.scale : 1.0f / sqrtf((float)H);
-  P.softcap = a.softcap;
+  P.softcap = gqa::kernel_softcap(a.softcap);
   P.smooth = a.smooth_softmax == 1 ? 1 : 0;
   P.q = q.data; P.k = in->key.data; P.v = in->value.data;
   P.out = out->output.data;

@@ -75,4 +75,8 @@ inline gqa_status check_status_word(const void* status) {
   return GQA_OK;
 }
 
+// A softcap as the kernels take it: c log2(e) has to be a float, below the stand-in for minus infinity of their running
+// maxima. (c tanh(s / c) is s here for every |s| below 2^87, and still grows with s beyond.)
+inline float kernel_softcap(float c) { return c < 0x1p99f ? c : 0x1p99f; }
+
 }  // namespace gqa

@@ -47,3 +47,11 @@ def test_softcaps_far_below_the_scores(dtype, form, softcap):
     def zeros(d):
         d["k"][:, 0] = 0
     softcap_check(dtype, form, softcap, zeros)
+
+
+@pytest.mark.parametrize("softcap", [1e38, 2.4e38, 3.4e38])
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_the_largest_softcaps(dtype, form, softcap):
+    """c log2(e) is no float any more."""
+    softcap_check(dtype, form, softcap)

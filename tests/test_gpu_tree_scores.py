@@ -42,3 +42,10 @@ def test_softcaps_far_below_the_scores(name, softcap):
     d = make(FORMS[name], seed=3)
     d["k"][:, 0] = 0
     capped_check(d, softcap)
+
+
+@pytest.mark.parametrize("name", list(FORMS))
+@pytest.mark.parametrize("softcap", [1e38, 2.4e38, 3.4e38])
+def test_the_largest_softcaps(name, softcap):
+    """c log2(e) is no float any more."""
+    capped_check(make(FORMS[name], seed=3), softcap)

@@ -386,7 +386,8 @@ tree_attn_kernel(const TreeParams p) {
         m[h] = mx;
         l[h] *= f[h];
       }
-      const float ref[2] = {kHalf ? m[0] - kLiftHalf : m[0], kHalf ? m[1] - kLiftHalf : m[1]};
+      // (Rounded up: of a maximum from 2^24 on, m - 15 could be m - 16, and 2^16 is no fp16 number.)
+      const float ref[2] = {kHalf ? __fsub_ru(m[0], kLiftHalf) : m[0], kHalf ? __fsub_ru(m[1], kLiftHalf) : m[1]};
       if constexpr (kHalf) {
         uint32_t pa[NT][2];   // rows gq, gq + 8
 #pragma unroll

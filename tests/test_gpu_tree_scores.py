@@ -2,11 +2,14 @@
 
 Tolerances as in test_gpu_tree.py, but for a softcap c: c tanh(s / c) is worked out to 2^-20 of itself (its quotient and
 product, tanh or the fit: 2^-24 and two or three steps of 2^-24 each), whatever c is, which adds 2^-20 of the largest
-|score| to what a score may be off."""
+|score| to what a score may be off. Where every score is exact, equal ones are the only ones with weight and a score is
+off by nothing."""
 
 import numpy as np
 import pytest
 
+from grouped_query_attention_gb300 import GroupQueryAttention
+from oracle import tree as ot
 from test_gpu_tree import CASES, check, make, operator, run_gpu, run_oracle
 
 pytestmark = pytest.mark.gpu
@@ -49,3 +52,35 @@ def test_softcaps_far_below_the_scores(name, softcap):
 def test_the_largest_softcaps(name, softcap):
     """c log2(e) is no float any more."""
     capped_check(make(FORMS[name], seed=3), softcap)
+
+
+def exact_scores(d, scale, softcap=0.0):
+    """Queries and keys of whole numbers times a power of two: equal scores are equal in every bit, unequal ones are worlds
+    apart, and the output is the mean of the values of the largest."""
+    d["softcap"] = 0.0
+    d["q"], d["pk"], d["k"] = (np.sign(np.nan_to_num(d[x])).astype(d[x].dtype) for x in ("q", "pk", "k"))
+    d["q"][..., 1::2] = 0
+    pk, pv = d["pk"].copy(), d["pv"].copy()
+    out, mag, reach = ot.forward(d["q"], d["k"], d["v"], d["parents"], d["totals"] - 1, d["news"], pk, pv, d["N"], d["Nkv"],
+                                 scale=scale, softcap=softcap, window=d["window"])
+    op = GroupQueryAttention(d["N"], d["Nkv"], scale=scale, softcap=softcap, local_window_size=d["window"])
+    got = run_gpu(d, op)
+    assert op.block_status() == 0
+    check(d, got, (out, mag, 0 * reach, pk, pv))
+
+
+MMA = [x for x in FORMS if x.startswith("mma")]
+
+
+@pytest.mark.parametrize("power", [17, 20, 22, 23, 24, 25, 27, 31, 40, 60])
+@pytest.mark.parametrize("name,sign", [(x, 1) for x in MMA] + [(x, -1) for x in FORMS])
+def test_scores_of_any_size_on_warp_mmas(name, sign, power):
+    """(Negative scales take every call there.)"""
+    exact_scores(make(FORMS[name], seed=5), sign * 2.0 ** power)
+
+
+@pytest.mark.parametrize("name", list(FORMS))
+@pytest.mark.parametrize("softcap", [3e7, 1e9, 1e12])
+def test_scores_as_large_as_a_large_softcap(name, softcap):
+    """Scores up to about 4 c, where floats are 2 to 2^16 apart."""
+    exact_scores(make(FORMS[name], seed=4), 2.0 ** round(np.log2(softcap / 16)), softcap)

@@ -454,6 +454,9 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk, cons
         lo_key = s.past + d - p.window;
       }
       float m_run = kNegBig, l_run = 0.f;
+      // Exponents are s mul + base, the product exact (fma). base less kLift is -m_run but for roundings, which `far` takes
+      // out where scores are so large (2^23) that they matter.
+      [[maybe_unused]] float base = kLift - kNegBig, far = 0.f;
       int mine = 0;   // units of this group in the piece
       for (int j = NQ == 2 ? 0 : q; j < n && ok; j += NQ == 2 ? 1 : 2, ++job, ++mine) {
         const Unit x = unit_of(p, s, w.off + j);
@@ -528,13 +531,15 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk, cons
           }
         }
         if (!full) tmem_st_wait();
+        // The largest exponent's growth over the reference, by the steps of the exponents: none can pass it.
+        [[maybe_unused]] const float top = mt, over = fmaf(mt, mul, base) - far - kLift;
         mt *= mul;
         if constexpr (CAP) {
           ua *= mul;
           if (mt > kNegBig) mt = cap_far(mt, c2);   // a reference: any rounding serves (softcap_fits)
         }
         // ---- rescale O when a maximum outgrew its reference (P V of the unit before is over: S came behind it)
-        const bool grow = mt > m_run + kLazy;
+        const bool grow = CAP ? mt > m_run + kLazy : over > kLazy;
         if (__any_sync(0xffffffffu, grow)) {
           const float m_new = grow ? mt : m_run;
           if (mine > 0) {
@@ -551,11 +556,17 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk, cons
             l_run *= f;
           }
           m_run = m_new;
+          if (!CAP && grow) {
+            base = kLift - m_run;
+            far = fmaf(top, mul, base) - kLift;
+            if (fabsf(far) < 2.f) far = 0.f;
+          }
         }
-        // ---- P, 64 columns at a time. MODE 0: no softcap; 3, 7: its fit of that degree; 9: any size.
+        // ---- P, 64 columns at a time. MODE 0, 1: no softcap (1: with far); 3, 7: its fit of that degree; 9: any size.
         auto exponents = [&](auto mode) {
           constexpr int MODE = decltype(mode)::value;
-          const float2 kk = make_float2(mul, mul), cc = make_float2(kLift - m_run, kLift - m_run);
+          const float c0 = CAP ? kLift - m_run : base;
+          const float2 kk = make_float2(mul, mul), cc = make_float2(c0, c0);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             tmem_ld32(s_addr + hf * 64, v);
@@ -566,8 +577,9 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk, cons
             for (int e = 0; e < 64; e += 2) {
               const float2 x2 = make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
               float2 arg;
-              if constexpr (MODE == 0) {
+              if constexpr (MODE <= 1) {
                 arg = ffma2(x2, kk, cc);
+                if constexpr (MODE == 1) arg = fadd2(arg, make_float2(-far, -far));
               } else {
                 const float2 u = ffma2(x2, kk, make_float2(0.f, 0.f));
                 if constexpr (MODE == 9) {
@@ -604,8 +616,10 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk, cons
             exponents(std::integral_constant<int, 7>());
           else
             exponents(std::integral_constant<int, 9>());
-        } else {
+        } else if (__builtin_expect(__all_sync(0xffffffffu, far == 0.f), 1)) {
           exponents(std::integral_constant<int, 0>());
+        } else {
+          exponents(std::integral_constant<int, 1>());
         }
       }
       // ---- the piece ends: O / l to the output, or m, l and O to the workspace

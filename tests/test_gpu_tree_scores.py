@@ -79,6 +79,14 @@ def test_scores_of_any_size_on_warp_mmas(name, sign, power):
     exact_scores(make(FORMS[name], seed=5), sign * 2.0 ** power)
 
 
+@pytest.mark.parametrize("power", [17, 19, 20, 22, 23, 24, 25, 27, 31, 40, 60])
+@pytest.mark.parametrize("name", ["one_tile", "two_tiles", "split", "h64_window"])
+def test_scores_of_any_size(name, power):
+    """(... of the tensor-core pipeline.)"""
+    case = ("f16", 2, 20, 4, 2, 64, 500, (490, 333), None, 100, 0, 0, 0, "tree", 0) if name == "h64_window" else FORMS[name]
+    exact_scores(make(case, seed=5), 2.0 ** power)
+
+
 @pytest.mark.parametrize("name", list(FORMS))
 @pytest.mark.parametrize("softcap", [3e7, 1e9, 1e12])
 def test_scores_as_large_as_a_large_softcap(name, softcap):

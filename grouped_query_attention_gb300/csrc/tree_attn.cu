@@ -468,8 +468,10 @@ tree_attn_kernel(const TreeParams p) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
               if (n == (kk - kw * WK) >> 3) x1 = kk & 1 ? sc[n][2 * h + 1] : sc[n][2 * h];
-            const float pr = ex2(__shfl_sync(0xffffffffu, x1, own) - ref[h]);
-            if (pr == 0.f) continue;   // a row that does not see it (the quad shares the row)
+            x1 = __shfl_sync(0xffffffffu, x1, own);
+            if (x1 == -INFINITY) continue;   // a row that does not see it (the quad shares the row)
+            // (a weight too small for a float counts: what it weighs is not finite)
+            const float pr = fmaxf(ex2(x1 - ref[h]), 0x1p-126f);
 #pragma unroll
             for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -650,7 +652,7 @@ tree_merge_kernel(const TreeParams p, int rows) {
         for (int y = 0; y < kAhead; ++y) {
           const int at = min(x + y * W, n - 1);
           const long long slot = tree_slot(w0 + at, at == 0) * tile;
-          f[y] = x + y * W < n ? ml[slot].x : -INFINITY;
+          f[y] = x + y * W < n ? ml[slot].x : INFINITY;
 #pragma unroll
           for (int k = 0; k < HG; ++k)
             if (4 * (c8 + 8 * k) < p.H) o[y][k] = *reinterpret_cast<const float4*>(src + slot * p.H + 8 * k * col_ld);
@@ -674,8 +676,8 @@ tree_merge_kernel(const TreeParams p, int rows) {
         if (x != sub) load(x);
 #pragma unroll
         for (int y = 0; y < kAhead; ++y) {
-          const float fy = ex2(f[y] - m);
-          if (fy == 0.f) continue;              // (a piece without weight: whatever its O, or one counted already)
+          if (f[y] == INFINITY) continue;       // (counted already)
+          const float fy = ex2(f[y] - m);       // (0 too: what is not finite in its O goes on)
 #pragma unroll
           for (int k = 0; k < HG; ++k) {
             if (4 * (c8 + 8 * k) >= p.H) continue;

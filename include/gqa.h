@@ -487,7 +487,9 @@ GQA_API gqa_status gqa_tree_describe_plan(const gqa_handle* handle, const gqa_tr
  *      logit to the denominator as in gqa_forward.
  * Rows of the caches outside [past_b, past_b + n_b) keep their bytes, and what
  * rows from past_b on held before does not matter. A key or value that is not
- * finite reaches only the rows that see it (fp32: an infinite key reads as NaN).
+ * finite reaches only the rows that see it, and a value all of them, however small
+ * its weight: there the output is infinite or NaN. (fp32: an infinite key reads as
+ * NaN, and so may a key or value within 2^-12 of the largest float.)
  * Attributes used: num_heads, kv_num_heads, local_window_size, scale, softcap,
  * smooth_softmax; causal must be 1 and do_rotary, the quant types and
  * sliding_window_cache off.

@@ -10,7 +10,7 @@ import pytest
 
 from grouped_query_attention_gb300 import GroupQueryAttention
 from oracle import tree as ot
-from test_gpu_tree import CASES, check, make, operator, run_gpu, run_oracle
+from test_gpu_tree import CASES, check, make, operator, run_gpu, run_oracle, tolerance
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +92,56 @@ def test_scores_of_any_size(name, power):
 def test_scores_as_large_as_a_large_softcap(name, softcap):
     """Scores up to about 4 c, where floats are 2 to 2^16 apart."""
     exact_scores(make(FORMS[name], seed=4), 2.0 ** round(np.log2(softcap / 16)), softcap)
+
+
+# ------------------------------------------------------------------ values that are not finite
+
+SPLIT = {"split_f32": ("f32", 1, 5, 4, 2, 64, 5000, (4999,), None, -1, 0, 0, 0, "tree", 0)}
+
+
+def spoiled_check(d, where, op=None, scale=0.0):
+    """where: [(tensor, index)] set to +inf. Elements that see one are not finite, all others as without it."""
+    clean = dict(d, pv=d["pv"].copy(), v=d["v"].copy())
+    for name, at in where:
+        clean[name][at] = 1.0
+    for x in ("pv", "v"):
+        d[x] = clean[x].copy()
+    for name, at in where:
+        d[name][at] = np.inf
+
+    def forward(x):
+        return ot.forward(x["q"], x["k"], x["v"], x["parents"], x["totals"] - 1, x["news"], x["pk"].copy(), x["pv"].copy(),
+                          x["N"], x["Nkv"], scale=scale, softcap=x["softcap"], window=x["window"], sink=x["sink"],
+                          smooth=bool(x["smooth"]))
+
+    with np.errstate(invalid="ignore"):
+        spoiled = ~np.isfinite(forward(d)[0])
+    ref, mag, reach = forward(clean)
+    assert spoiled.any() and not spoiled.all()
+    got = run_gpu(d, op or operator(d, scale=scale))[0].astype(np.float64)
+    assert not np.isfinite(got[spoiled]).any(), (~spoiled & ~np.isfinite(got)).sum()
+    bad = ~spoiled & ~(np.abs(got - ref) <= tolerance(clean, ref, mag, reach))
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:3].tolist())
+
+
+@pytest.mark.parametrize("name", ["split", "split_f32", "mma_h256", "one_tile", "two_tiles", "mma_f32"])
+def test_infinite_values_of_a_split_range(name):
+    """A cached value in the middle: the heads that read it are spoiled in its coordinate, in whichever worker's piece
+    it lies."""
+    d = make({**CASES, **FORMS, **SPLIT}[name], seed=8)
+    spoiled_check(d, [("pv", (0, 0, int(d["totals"][0]) // 2, 7))])
+
+
+@pytest.mark.parametrize("name", ["split", "split_f32", "mma_h256", "one_tile", "two_tiles", "mma_f32", "forest", "forest_window_f32"])
+@pytest.mark.parametrize("what", ["cached", "node"])
+def test_infinite_values_of_no_weight(name, what):
+    """The same beside a key of such a score that the weight of every other one is far below the smallest float: an
+    infinite value times that is infinite still."""
+    d = make({**CASES, **FORMS, **SPLIT}[name], seed=9)
+    last = int(d["totals"][0]) - d["S"] - 1
+    d["q"][:] = np.where(np.isnan(d["q"]), d["q"], 1)
+    d["k"][:], d["pk"][:] = np.where(np.isnan(d["k"]), d["k"], 0), np.where(np.isnan(d["pk"]), d["pk"], 0)
+    d["pk"][0, 0, last] = 1                               # score H scale, the others 0
+    scale = 400.0 / d["H"]
+    row = last // 2 if d["window"] < 0 else last - 1
+    spoiled_check(d, [("pv", (0, 0, row, 7)) if what == "cached" else ("v", (0, 2, 9))], scale=scale)

@@ -93,7 +93,7 @@ gqa_status plan_tree(const gqa_handle* h, const gqa_tree_inputs* in, const gqa_t
                 "present_key/value must be (B, kv_num_heads, C, head_size) = (%lld,%lld,C,%lld) of the query dtype", B, Nkv, H);
   const long long C = c.shape[2], T = in->total_sequence_length, G = N / Nkv;
   if (T < 1 || T > C) return fail(GQA_ERR_INVALID_ARGUMENT, "total_sequence_length %lld must be in [1, C = %lld]", T, C);
-  if (C > (1LL << 30) || B * Nkv > 65535 || B * Nkv * C >= (1LL << 31))   // (rows are counted in 32 bits)
+  if (C > (1LL << 30) || B > 65535 || B * Nkv > 65535 || B * Nkv * C >= (1LL << 31))   // (rows are counted in 32 bits)
     return fail(GQA_ERR_UNSUPPORTED, "present_key/value: tensor too large");
   if (S * N > (1LL << 30) || B * S * N > (1LL << 31) - 65536 || N * H > (1LL << 30)) return fail(GQA_ERR_UNSUPPORTED, "query too large");
 
@@ -240,7 +240,8 @@ gqa_status gqa_tree_accept(gqa_handle* h, const gqa_accept_args* a, void* status
     return fail(GQA_ERR_INVALID_ARGUMENT, "caches must be non-empty (B, kv_num_heads, C, head_size)");
   const long long B = c.shape[0], C = c.shape[2], H = c.shape[3];
   if ((s = check_head_size(H)) != GQA_OK) return s;
-  if (C > (1LL << 30) || B * Nkv > 65535 || B * Nkv * C >= (1LL << 31)) return fail(GQA_ERR_UNSUPPORTED, "caches: tensor too large");
+  if (C > (1LL << 30) || B > 65535 || B * Nkv > 65535 || B * Nkv * C >= (1LL << 31))
+    return fail(GQA_ERR_UNSUPPORTED, "caches: tensor too large");
   if (!present(a->path) || a->path.dtype != GQA_I32 || a->path.ndim != 2 || a->path.shape[0] != B || a->path.shape[1] < 1)
     return fail(GQA_ERR_INVALID_ARGUMENT, "path must be int32 of shape (B, S)");
   if ((s = check_nodes(a->path.shape[1])) != GQA_OK) return s;

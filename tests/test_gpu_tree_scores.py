@@ -145,3 +145,52 @@ def test_infinite_values_of_no_weight(name, what):
     scale = 400.0 / d["H"]
     row = last // 2 if d["window"] < 0 else last - 1
     spoiled_check(d, [("pv", (0, 0, row, 7)) if what == "cached" else ("v", (0, 2, 9))], scale=scale)
+
+
+WINDOWED = {   # fp16: one, two row tiles a piece, many pieces; warp MMAs: fp16 heads of 256, fp32
+    "one_tile": ("f16", 2, 24, 4, 2, 64, 900, (900, 700), None, 300, 0, 0, 0, "chain", 0),
+    "two_tiles": ("f16", 2, 70, 8, 2, 128, 900, (900, 700), (70, 33), 300, 5.0, 1, 0, "chain", 0),
+    "all_nodes": ("f16", 1, 512, 2, 1, 64, 2000, (1990,), None, 600, 0, 0, 0, "chain", 0),
+    "pieces": ("f16", 2, 40, 16, 4, 96, 3000, (3000, 2700), None, 1250, 0, 0, 0, "tree", 0),
+    "h256": ("f16", 1, 20, 4, 2, 256, 500, (490,), None, 200, 0, 0, 1, "chain", 0),
+    "f32": ("f32", 2, 20, 4, 2, 128, 500, (490, 333), None, 100, 0, 1, 0, "tree", 0),
+    "f32_pieces": ("f32", 1, 33, 8, 2, 64, 6000, (5999,), None, 3000, 0, 0, 0, "chain", 0),
+}
+
+
+@pytest.mark.parametrize("name", WINDOWED)
+@pytest.mark.parametrize("behind", [0, 1, 3, 9, "last"])
+def test_cached_values_at_a_windows_edge(name, behind):
+    """A cached value that nodes of a depth up to `behind` see (the root sees furthest back): they are spoiled, in that
+    coordinate, and nobody else. One head of one sequence."""
+    d = make(WINDOWED[name], seed=6)
+    b = d["B"] - 1
+    n = d["S"] if d["news"] is None else int(d["news"][b])
+    depth = max(len(ot.ancestors(d["parents"], b, i)) - 1 for i in range(n))
+    off = min(depth, 1 << 20 if behind == "last" else behind)
+    row = int(d["totals"][b]) - n - d["window"] + off
+    spoiled_check(d, [("pv", (b, d["Nkv"] - 1, row, 5)), ("pv", (b, 0, max(0, row - 1), d["H"] - 1))])
+
+
+@pytest.mark.parametrize("name", WINDOWED)
+def test_nan_keys_at_a_windows_edge(name):
+    """A cached key of NaN: rows that see it are NaN, the others as they were."""
+    d = make(WINDOWED[name], seed=7)
+    b = d["B"] - 1
+    n = d["S"] if d["news"] is None else int(d["news"][b])
+    row = int(d["totals"][b]) - n - d["window"] + 2
+    ref, mag, reach, _, _ = run_oracle(d)
+    tol = tolerance(d, ref, mag, reach)
+    d["pk"][b, 0, row, 3] = np.nan
+    got = run_gpu(d)[0].astype(np.float64).reshape(d["B"], d["S"], d["N"], d["H"])
+    ref, tol = ref.reshape(got.shape), tol.reshape(got.shape)
+    G, seen = d["N"] // d["Nkv"], 0
+    for i in range(n):
+        sees = len(ot.ancestors(d["parents"], b, i)) - 1 <= 2
+        seen += sees
+        if sees:
+            assert np.isnan(got[b, i, :G]).all()
+        else:
+            assert (np.abs(got - ref) <= tol)[b, i].all()
+        assert (np.abs(got - ref) <= tol)[b, i, G:].all()
+    assert 0 < seen < n

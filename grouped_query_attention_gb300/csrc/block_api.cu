@@ -52,7 +52,7 @@ gqa_status check_block_cache(const gqa_block_cache& c, const char* name, long lo
     if (t->dtype != GQA_F32 || !shape_is(*t, 3, ss))
       return fail(GQA_ERR_INVALID_ARGUMENT, "%s: scales must be float32 (B, kv_num_heads, ceil(C / block_size)) = (%lld,%lld,%lld)",
                   name, B, Nkv, (long long)ss[2]);
-  if (*C > (1LL << 30) || B * Nkv > 65535 || B * Nkv * *C >= (1LL << 31))   // TMA rows are 32-bit
+  if (*C > (1LL << 30) || B > 65535 || B * Nkv > 65535 || B * Nkv * *C >= (1LL << 31))   // TMA rows are 32-bit
     return fail(GQA_ERR_UNSUPPORTED, "%s: tensor too large", name);
   return GQA_OK;
 }

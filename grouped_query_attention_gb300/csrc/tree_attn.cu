@@ -24,7 +24,7 @@
 // sequences of 4096..16384 rows, 8 nodes, 32 heads over 8: 236 us for 674 MB (2.9
 // TB/s); the MMA pipe is busy 38 % of the time (the MMAs alone take 110 us), and two
 // warps a scheduler (255 registers) cannot hide the chains around them. Measured
-// there: eight warps of 16 rows 275 us, 32 rows a warp 265, units of 16 keys and
+// there (events around single cold launches): eight warps of 16 rows 275 us, 32 rows a warp 265, units of 16 keys and
 // three CTAs an SM 255, queries split ahead in shared memory 263, rows brought by
 // bulk copies 359. fp16 heads of 256, 32 rows: 64 us for 101 MB, 256 rows 117.
 #include <cuda_fp16.h>
@@ -771,7 +771,7 @@ cudaError_t launch_t(const TreeParams& p, cudaStream_t st) {
 
 // The tensor-core pipeline where it can: it holds 128 rows as cheaply as 16, and its copies run across the ends of
 // ranges (16 sequences of 1k to 8k rows, 16 query rows: 74 us, the warp MMAs 80; 32 rows 76, 89; 5 nodes on 1030 rows
-// 15, 17). It takes row maxima before the scale, which a negative one would turn, and softcaps of a range (softcap_fits;
+// 15, 17; events around single cold launches). It takes row maxima before the scale, which a negative one would turn, and softcaps of a range (softcap_fits;
 // scale / softcap far from the ends of the floats).
 bool use_tc(const TreeParams& p) {
   if (p.t_type != kF16 || p.H > 128 || !(p.scale > 0.f) || !softcap_fits(p.softcap)) return false;

@@ -25,15 +25,16 @@
 // roundings out.
 //
 // What bounds it. Few rows: HBM. 16 sequences of 1024..8176 rows, 16 nodes, 32
-// heads over 8: 60 us for 310 MB, 5.2 TB/s (0.76 of the measured copy); the rest
+// heads over 8: 60 us (ncu) for 310 MB, 5.2 TB/s (0.76 of the measured copy); the rest
 // are the starts and ends of ranges, which the ring runs across. More rows: the
 // chain S, maximum, exponents, P V of two groups, with two softmax warps a
 // scheduler (1.5 to 1.7 instructions a clock; the MMA pipe is busy 26 % of the
 // time, the exponents' 27 %). 208 rows of 64 dims: 1.8 us a unit of 256 rows (200k
-// keys: 41 us); 256 rows of 128 dims with a softcap 3.5 us, 0.69 PFLOP/s (without
-// one 83 us where it takes 101). Steps of 64 keys with two S tiles a group measured
-// 126 against 105 us (softcap) and 50 against 44 (200k keys); scores kept in
-// registers between maximum and exponents spilled (107 to 115, 44 to 52).
+// keys: 42 us, ncu); 256 rows of 128 dims with a softcap 3.5 us, 0.69 PFLOP/s (without
+// one 83 us where it takes 101). Measured by events around single cold launches: steps
+// of 64 keys with two S tiles a group 126 against 105 us (softcap) and 50 against 44
+// (200k keys); scores kept in registers between maximum and exponents spilled (107 to
+// 115, 44 to 52).
 #include <cuda_fp16.h>
 
 #include "block_tc.cuh"

@@ -48,8 +48,8 @@ __device__ __forceinline__ float cap_far(float u, float c2) {
   return fmaf(r, -2.f * c2, c2);
 }
 // What the kernels that use these forms take: a reference maximum from cap_far may differ from the exponents' own form by
-// 2^-22 of c2, and between lift, lag and fp16's largest number there are two bits. Larger softcaps, and ones that s / c
-// of any score would overflow with, go to the warp MMAs, whose maximum is that of the very scores.
+// 2^-22 of c2, and between lift, lag and fp16's largest number there are two bits. Larger softcaps, and ones so small
+// that scale / c may be no float, go to the warp MMAs, whose maximum is that of the very scores.
 inline bool softcap_fits(float softcap) { return softcap == 0.f || (softcap >= 0x1p-40f && softcap <= 0x1p19f); }
 // Both forms computed, one selected (no branch).
 __device__ __forceinline__ float2 cap_any(float2 u, float c2) {

@@ -771,8 +771,8 @@ cudaError_t launch_t(const TreeParams& p, cudaStream_t st) {
 
 // The tensor-core pipeline where it can: it holds 128 rows as cheaply as 16, and its copies run across the ends of
 // ranges (16 sequences of 1k to 8k rows, 16 query rows: 74 us, the warp MMAs 80; 32 rows 76, 89; 5 nodes on 1030 rows
-// 15, 17; events around single cold launches). It takes row maxima before the scale, which a negative one would turn, and softcaps of a range (softcap_fits;
-// scale / softcap far from the ends of the floats).
+// 15, 17; events around single cold launches). It takes row maxima before the scale, which a negative one would turn,
+// and softcaps of a range (softcap_fits; scale / softcap far from the ends of the floats).
 bool use_tc(const TreeParams& p) {
   if (p.t_type != kF16 || p.H > 128 || !(p.scale > 0.f) || !softcap_fits(p.softcap)) return false;
   return p.softcap == 0.f || (p.scale > 0x1p-40f && p.scale < 0x1p40f);

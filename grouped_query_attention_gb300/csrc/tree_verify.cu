@@ -85,9 +85,9 @@ __device__ __forceinline__ Pair shfl_up(Pair a, int o) {
 // a > b
 __device__ __forceinline__ bool above(Pair a, Pair b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
 
-// Probabilities as the definition reads them: numbers from 2^15 on are none, so that no sum or product of theirs overflows.
+// Probabilities as the definition reads them: numbers from 2^40 on are none, so that no sum of theirs overflows.
 // (The bits of negative, infinite and NaN values lie above those of the positive ones.)
-__device__ __forceinline__ float proper(float p) { return __float_as_uint(p) < 0x47000000u ? p : 0.f; }
+__device__ __forceinline__ float proper(float p) { return __float_as_uint(p) < 0x53800000u ? p : 0.f; }
 template <bool HALF>
 __device__ __forceinline__ float prob(const void* base, long long i) {
   if constexpr (HALF) return proper(__half2float(static_cast<const __half*>(base)[i]));
@@ -201,7 +201,7 @@ __device__ __forceinline__ Pair left_of(float p, float q, Pair a, Pair b) {
 __device__ __noinline__ Pair left_fine(float p, float q, const Pair* over, int round) {
   Pair r = two_sum(p, -q);
   for (int j = 0; j + 1 < round && r.hi > 0.f; ++j) {
-    const Pair t = mul(raised(r), over[j]);
+    const Pair t = raised(mul(r, over[j]));
     r = two_sum(t.hi, -q);
     r = two_sum(r.hi, __fadd_rn(r.lo, t.lo));
   }
@@ -405,13 +405,18 @@ tree_verify_kernel(const VerifyParams p) {
             }
           }
           if (next >= n) break;
-          const float qv = c.q[next] * kUp;
-          pv = c.p[next] * kUp;
-          Pair r = {pv, 0.f};
+          pv = c.p[next];
+          const float up = fmaxf(pv, c.q[next]) < 1.f ? kUp : 1.f;   // (numbers far above 1 have no room for it)
+          const float ps = pv * up, qv = c.q[next] * up;
+          Pair r = {ps, 0.f};
           if (round > 0) {
             if (p.draft) {
-              if (fine) r = left_fine(pv, qv, c.over, round);
-              else r = round == 1 ? two_sum(pv, -qv) : add(mul(c.left.a, {pv, 0.f}), neg(mul(c.left.b, {qv, 0.f})));
+              if (fine) {
+                r = left_fine(pv * kUp, c.q[next] * kUp, c.over, round);
+                r = {r.hi * (up / kUp), r.lo * (up / kUp)};
+              } else {
+                r = round == 1 ? two_sum(ps, -qv) : add(mul(c.left.a, {ps, 0.f}), neg(mul(c.left.b, {qv, 0.f})));
+              }
             } else {
               for (int x = lane; x < turned_down; x += 32) dup |= c.gone[x] == c.token[next];
               dup = __any_sync(0xffffffffu, dup);
@@ -459,7 +464,7 @@ tree_verify_kernel(const VerifyParams p) {
         if (lane == 0) c.gone[turned_down] = c.token[last];
         __syncwarp();
         ++turned_down;
-        z = turned_down == 1 ? add(whole, {-pv, 0.f}) : dup ? z : add(z, {-pv, 0.f});
+        z = turned_down == 1 ? add(whole, {-pv * kUp, 0.f}) : dup ? z : add(z, {-pv * kUp, 0.f});
         if (!(z.hi > whole.hi * kCoarse)) {   // too little of that sum for a difference to hold: add it up
           command = kSum;
           break;

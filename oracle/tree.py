@@ -62,7 +62,7 @@ def forward(query, key, value, parents, seqlens_k, new_lens, present_key, presen
 
 def _proper(row):
     row = np.asarray(row, np.float64)
-    return np.where((row > 0) & (row < 2.0 ** 15), row, 0.0)
+    return np.where((row > 0) & (row < 2.0 ** 40), row, 0.0)
 
 
 def verify(tokens, parents, target_probs, accept_uniforms, sample_uniforms, draft_probs=None, new_lens=None):

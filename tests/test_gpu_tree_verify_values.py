@@ -179,16 +179,29 @@ def test_sums_of_large_vocabularies_keep_their_bits():
 
 @pytest.mark.parametrize("drafts", [True, False])
 def test_numbers_too_large_for_a_probability(drafts):
-    """Numbers from 2^15 on count as none, whatever their sum; just below it they count. A row without another is reported."""
+    """Numbers from 2^40 on count as none, whatever their sum; below it they count. A row without another is reported."""
     rng = np.random.default_rng(31)
     p = rng.random((6, 3000)) / 3000
-    p[:4, [3, 200, 1700, 2999]] = np.array([[2e38], [3e4], [2.0 ** 15], [1e30]])
+    p[:4, [3, 200, 1700, 2999]] = np.array([[2e38], [3e11], [2.0 ** 40], [1e30]])
     p[4] = 0.0
     p[4, [3, 200]] = 2e38
     q = np.full(3000, 1.0 / 3000)
     q[[3, 77]] = 3e38
+    q[1000] = 1e11
     v = star(np.tile([3, 77, 1000, 2999], (6, 1)), p, q if drafts else None, 1.0, [0.05, 0.1, 0.5, 0.7, 0.7, 0.9])
     op = GroupQueryAttention(1, 1)
     got = run_verify(v, op)
     same(got, ot.verify(**v))
     assert got[2].min() == got[2][4] == -1 and op.block_status() == capi.GQA_DEVICE_BAD_PROBS
+
+
+@pytest.mark.parametrize("drafts", [True, False])
+@pytest.mark.parametrize("size", [1e-6, 1.0, 1e3, 1e6, 1e10])
+def test_rows_that_are_not_normalised(size, drafts):
+    """Rows whose sums are far from 1: the tests are those of the definition, the draw takes a share of what is left."""
+    for seed in range(3):
+        v = make_verify(5, 14, 700, drafts=drafts, kind="star", seed=seed, std=1.0)
+        v["target_probs"] = (v["target_probs"] * np.float32(size * 30)).astype(np.float32)
+        if drafts:
+            v["draft_probs"] = (v["draft_probs"] * np.float32(size * (1 + 40 * seed))).astype(np.float32)
+        same(run_verify(v), ot.verify(**v))

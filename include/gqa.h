@@ -533,8 +533,9 @@ typedef struct gqa_verify_args {
  * sum(r) = 0. The tokens of the path and next_token are then distributed as if
  * drawn from the target alone. Values and sums over the vocabulary are held in
  * 48 bits, of which what is left of a row keeps at least 36 (up to 2^20 tokens),
- * however many of a node's children are turned down. A number that is not positive and below
- * 2^40 is no probability and counts as 0; so does that of a token outside [0, V).
+ * however many of a node's children are turned down. A number that is not
+ * positive and below 2^40 is no probability and counts as 0; so does that of a
+ * token outside [0, V).
  * A sequence with n_b = 0, or outside [0, S] (GQA_DEVICE_BAD_SEQLEN), gets path
  * -1, path_lens 0 and next_token -1; one without a positive probability to draw
  * from next_token -1 (GQA_DEVICE_BAD_PROBS). status: see gqa_block_forward. */
